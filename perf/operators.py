@@ -197,13 +197,11 @@ def prepare(case, seed):
             flat["v"][a:a + n] = size.square() * (0.5 + torch.rand(n, generator=g, device="cuda"))
         flat["param"], flat["grad"] = flat["param"].to(DT[case["param"]]), flat["grad"].to(DT[case["grad"]])
         if case["bits"] == 8:
-            for name, new in (("m", "m"), ("v", "r")):
-                x = flat.pop(name)
-                x = x.sqrt() if name == "v" else x
-                scale = x.view(-1, 128).abs().amax(1) / 448.0
-                code = x.view(-1, 128) / scale.clamp_min(1e-38)[:, None]
-                flat[new] = code.view(-1).to(torch.float8_e4m3fn)
-                flat[new + "_scale"] = scale
+            for name in ("m", "v"):
+                x = flat[name].view(-1, 128)
+                scale = x.abs().amax(1) / 448.0
+                flat[name] = (x / scale.clamp_min(1e-38)[:, None]).view(-1).to(torch.float8_e4m3fn)
+                flat[name + "_scale"] = scale
         s = {"case": case, "flat": flat, "at": at, "sizes": sizes, "steps": 1000,
              "decay": [DECAY if len(sh) > 1 else 0.0 for sh in shapes], "grad_scale": torch.full((1,), 0.75, device="cuda")}
         s["begins"] = torch.tensor(at + [end], device="cuda")
@@ -309,8 +307,8 @@ def _to_e4m3(x, rand16, floor):
 def _quantize8(x, rand16, floor):
     blocks = x.view(-1, 128)
     top = blocks.abs().amax(1)
-    inv = torch.where(top > 0, torch.clamp(448.0 / top, max=torch.finfo(torch.float32).max), 0.0)
-    return _to_e4m3((blocks * inv[:, None]).view(-1), rand16, floor), top / 448.0
+    inv = torch.where(top > 0, torch.clamp(torch.full_like(top, 448.0) / top, max=torch.finfo(torch.float32).max), 0.0)
+    return _to_e4m3((blocks * inv[:, None]).view(-1), rand16, floor), top * (1 / 448)
 
 
 def _dequantize8(code, scale):
@@ -329,20 +327,19 @@ def _adamw(s):
     keep = (1 - LR * s["decays"])[owner].repeat_interleave(4).float()
     g = flat["grad"].float() * s["grad_scale"]
     if case["bits"] == 8:
-        m, v = _dequantize8(flat["m"], flat["m_scale"]), _dequantize8(flat["r"], flat["r_scale"]).square()
+        m, v = _dequantize8(flat["m"], flat["m_scale"]), _dequantize8(flat["v"], flat["v_scale"])
     else:
         m, v = flat["m"], flat["v"]
     m = m * b1 + g * (1 - b1)
     v = v * b2 + g * g * (1 - b2)
-    r = v.sqrt()
-    new = flat["param"].float() * keep - m * size / (r * unbias + ADAM_EPS)
+    new = flat["param"].float() * keep - m * size / (v.sqrt() * unbias + ADAM_EPS)
     if case["param"] == "bf16":
         bits = new.view(torch.int32) + (random_words(group, 2 * owner + 1, t) & 0xFFFF).int()
         new = (bits & -65536).view(torch.float32).bfloat16()
     flat["param"].copy_(new)
     if case["bits"] == 8:
         w = random_words(group, 2 * owner, t)
-        for name, x, rand, floor in (("m", m, w & 0xFFFF, False), ("r", r, w >> 16, True)):
+        for name, x, rand, floor in (("m", m, w & 0xFFFF, False), ("v", v, w >> 16, True)):
             code, scale = _quantize8(x, rand, floor)
             flat[name].copy_(code), flat[name + "_scale"].copy_(scale)
     else:
@@ -498,7 +495,7 @@ def _exact_adamw(s):
         g = get("grad") * 0.75
         blocks, groups = torch.arange(n, device="cuda") // 128, torch.arange((n + 3) // 4, device="cuda")
         if case["bits"] == 8:
-            m, v = get("m") * get("m_scale")[blocks], (get("r") * get("r_scale")[blocks]) ** 2
+            m, v = get("m") * get("m_scale")[blocks], get("v") * get("v_scale")[blocks]
         else:
             m, v = get("m"), get("v")
         m, v = b1 * m + (1 - b1) * g, b2 * v + (1 - b2) * g ** 2
@@ -514,7 +511,7 @@ def _exact_adamw(s):
         out["param"][a:a + n] = p
         if case["bits"] == 8:
             w = random_words(groups, 2 * i, t)[:n]
-            for name, x, rand, floor in (("m", m, w & 0xFFFF, False), ("r", torch.sqrt(v), w >> 16, True)):
+            for name, x, rand, floor in (("m", m, w & 0xFFFF, False), ("v", v, w >> 16, True)):
                 top = torch.zeros((n + 127) // 128, dtype=torch.float64, device="cuda")
                 top.scatter_reduce_(0, blocks, x.abs(), "amax")
                 out[name + "_scale"][a // 128:a // 128 + len(top)] = top / 448
