@@ -405,6 +405,146 @@ NVFP4_API nvfp4_status nvfp4_linear_wgrad(const void* dY, int32_t dy_dtype, int6
 NVFP4_API nvfp4_status nvfp4_sqrelu_forward(const void* h, void* a, int64_t n, void* stream);
 NVFP4_API nvfp4_status nvfp4_sqrelu_backward(const void* h, const void* da, void* dh, int64_t n, void* stream);
 
+/*
+ * Layer norm, forward.  With residual: h = x + residual, rounded to x's type and stored in h;
+ * without, h = x (pass residual = h = NULL).  For each row, over its cols elements, in fp32:
+ *   mean = sum(h) / cols;  rstd = 1 / sqrt(sum((h - mean)^2) / cols + eps);
+ *   y = (h - mean) * rstd * weight + bias            (bias NULL: none)
+ * x, residual, h: [rows, cols] of x_dtype with row pitches ldx, ldr, ldh; y of y_dtype, pitch ldy
+ * (pitches in elements, >= cols); weight, bias: [cols] of w_dtype; mean, rstd: [rows] fp32.
+ * cols >= 1, rows >= 0 (0: nothing is done), eps >= 0 and finite.  Pointers need the alignment of
+ * their element type only; 16-byte aligned rows of a multiple of 8 elements run fastest.  h may be
+ * x or residual, and y may be x (in place) where types and pitches are equal.
+ */
+NVFP4_API nvfp4_status nvfp4_layer_norm_forward(const void* x, int32_t x_dtype, int64_t rows, int64_t cols,
+                                                int64_t ldx, const void* residual, int64_t ldr, const void* weight,
+                                                const void* bias, int32_t w_dtype, float eps, void* y, int32_t y_dtype,
+                                                int64_t ldy, void* h, int64_t ldh, float* mean, float* rstd,
+                                                void* stream);
+
+/* Workspace bytes nvfp4_layer_norm_backward needs on the current device (partial column sums). */
+NVFP4_API size_t nvfp4_layer_norm_backward_workspace_bytes(int64_t rows, int64_t cols);
+
+/*
+ * Layer norm, backward.  x: the rows that were normalised (the forward call's h), with its mean
+ * and rstd.  With xhat = (x - mean) * rstd and g = dy * weight, in fp32:
+ *   dx = rstd * (g - mean_c(g) - xhat * mean_c(g * xhat)) + dh     (dh NULL: none)
+ *   dweight = sum over rows of dy * xhat;  dbias = sum over rows of dy
+ * dy: [rows, cols] of y_dtype; dh (the gradient that reaches h by the residual path), dx: of
+ * x_dtype; dweight, dbias: [cols] fp32, overwritten; dbias may be NULL.  dx may be dh or dy where
+ * types and pitches are equal.  The column sums have a fixed order: results are deterministic.
+ * rows = 0 leaves dweight = dbias = 0.  workspace: device memory, 16-byte aligned, any contents.
+ */
+NVFP4_API nvfp4_status nvfp4_layer_norm_backward(const void* dy, int32_t y_dtype, int64_t lddy, const void* x,
+                                                 int32_t x_dtype, int64_t rows, int64_t cols, int64_t ldx,
+                                                 const void* weight, int32_t w_dtype, const float* mean,
+                                                 const float* rstd, const void* dh, int64_t lddh, void* dx,
+                                                 int64_t lddx, float* dweight, float* dbias, void* workspace,
+                                                 size_t workspace_bytes, void* stream);
+
+/*
+ * AdamW over many tensors.  One tensor: param [n] and grad [n] (F32 or BF16, contiguous) and the
+ * two moments.  bits = 32: m, v are fp32 [n].  bits = 8: m, v hold E4M3 codes with one fp32 scale
+ * per 128 consecutive elements (m_scale, v_scale: [ceil(n / 128)]); the value is code * scale.
+ * With t = step (counted from 1) and gs = *grad_scale (1 if NULL), each line one fp32 operation
+ * after another, rounded to nearest:
+ *   g = grad * gs;  m = m * beta1 + g * (1 - beta1);  v = v * beta2 + (g * g) * (1 - beta2)
+ *   p = p * K - (m * A) / (sqrt(v) * B + eps)
+ * with K = 1 - lr * weight_decay, A = lr / (1 - beta1^t), B = 1 / sqrt(1 - beta2^t), these and
+ * 1 - beta computed in fp64 and rounded once.  8-bit states: per block, scale = max|x| * (1 / 448)
+ * and inv = min(448 / max|x|, FLT_MAX) (both 0 for an all-zero block), code = e4m3(x * inv), rounded
+ * to nearest even or stochastically, saturating; v's code is at least 1 where v > 0, so that no
+ * stored denominator falls to zero.  BF16 parameters are rounded likewise.  Random bits: element i
+ * of tensor `id` draws on word (i & 3) of Philox(key = sr_seed, counter = (lo32(i >> 2),
+ * hi32(i >> 2), 2 id + s, step)): s = 0 for the states (low half m, high half v), s = 1, low half, for BF16 parameters; with R those 16 bits and p the position between the two neighbouring
+ * grid points, it goes up iff p + R * 2^-16 >= 1.
+ * n = 0 and grad = NULL leave a tensor alone.  A non-finite gradient (after gs) sets
+ * NVFP4_ERR_NONFINITE on dev_status; it reaches the tensor's values as the formulas have it, and an 8-bit
+ * block with such a value is left with a non-finite scale.
+ */
+typedef struct {
+    void* param;
+    const void* grad;
+    void* m;
+    void* v;
+    float* m_scale;              /* bits = 8 only */
+    float* v_scale;
+    int64_t n;
+    int32_t param_dtype;         /* nvfp4_dtype */
+    int32_t grad_dtype;
+    double weight_decay;
+    int64_t id;                  /* 0 .. 2^30 - 1: which random stream the tensor draws on */
+} nvfp4_adamw_tensor;
+
+typedef struct {
+    int32_t bits;                /* 32 or 8 */
+    int32_t round;               /* nvfp4_round, of 8-bit states and BF16 parameters */
+    int64_t step;                /* 1, 2, ... */
+    double lr, beta1, beta2, eps;
+    uint64_t sr_seed;
+} nvfp4_adamw_params;
+
+/* `tensors` and `params` are HOST pointers, read before the call returns; grad_scale is a device
+   pointer or NULL.  Tensors must not overlap. */
+NVFP4_API nvfp4_status nvfp4_adamw_step(const nvfp4_adamw_tensor* tensors, int32_t count,
+                                        const nvfp4_adamw_params* params, const float* grad_scale,
+                                        uint32_t* dev_status, void* stream);
+
+/*
+ * Attention over packed sequences.  q: [tq, heads, dim]; k, v: [tk, kv_heads, dim], BF16, the last
+ * axis contiguous, tokens and heads at strides of their own (elements): slices of one fused
+ * projection will do.  heads is a multiple of kv_heads; query head h reads key head
+ * h / (heads / kv_heads).  dim: a multiple of 8, at most 128.  Sequence i holds the queries
+ * cu_q[i] .. cu_q[i+1] - 1 and the keys cu_k[i] .. cu_k[i+1] - 1 (device int32 [nseq + 1], from 0
+ * to tq / tk, not decreasing; empty sequences are fine); cu_q = cu_k = NULL: one sequence.  A query
+ * sees the keys of its sequence; with causal, query a of Sq and key b of Sk (counted in the
+ * sequence) only where b <= a + Sk - Sq.  With z = scale * q.k over those keys:
+ *   lse = log(sum(exp(z)));  out = sum(exp(z - lse) v)
+ * fp32 sums and softmax statistics; the probabilities are rounded to BF16 for the product with v.
+ * A query that sees no key gets out = 0, lse = -inf.  lse: [heads, tq] fp32.
+ * Offsets that break the rules set NVFP4_ERR_INVALID_ARG on dev_status (nothing is read or written
+ * out of bounds; the outputs are unspecified).  What lies outside a sequence does not reach it,
+ * whatever it holds.
+ */
+typedef struct {
+    void* data;
+    int64_t token_stride;        /* elements; a positive multiple of 8 unless there is one token */
+    int64_t head_stride;         /* likewise; data itself 16-byte aligned */
+} nvfp4_heads;
+
+typedef struct {
+    int64_t tq, tk;
+    int32_t heads, kv_heads, dim;
+    int32_t causal;
+    float scale;
+    int32_t nseq;                /* 1 where cu_q = cu_k = NULL */
+    const int32_t* cu_q;
+    const int32_t* cu_k;
+} nvfp4_attention_shape;
+
+/* `shape` and the nvfp4_heads are HOST structs, read before the call returns. */
+NVFP4_API nvfp4_status nvfp4_attention_forward(const nvfp4_attention_shape* shape, const nvfp4_heads* q,
+                                               const nvfp4_heads* k, const nvfp4_heads* v, const nvfp4_heads* out,
+                                               float* lse, uint32_t* dev_status, void* stream);
+
+/* Workspace bytes nvfp4_attention_backward needs. */
+NVFP4_API size_t nvfp4_attention_backward_workspace_bytes(const nvfp4_attention_shape* shape);
+
+/*
+ * The backward pass: recomputes P = exp(z - lse) from q, k and lse, and with dP = dout.v and
+ * delta = sum(dout * out):
+ *   dv = P^T dout;  dS = P (dP - delta) scale;  dq = dS k;  dk = dS^T q
+ * (dk and dv summed over the query heads of a key head; P and dS rounded to BF16 for the products,
+ * sums in fp32).  out and lse are the forward call's.  dq, dk, dv are laid out like q, k, v, with
+ * strides of their own, and must not overlap one another or the inputs.  No atomics: results are
+ * deterministic.  workspace: device memory, 16-byte aligned, any contents.
+ */
+NVFP4_API nvfp4_status nvfp4_attention_backward(const nvfp4_attention_shape* shape, const nvfp4_heads* dout,
+                                                const nvfp4_heads* q, const nvfp4_heads* k, const nvfp4_heads* v,
+                                                const nvfp4_heads* out, const float* lse, const nvfp4_heads* dq,
+                                                const nvfp4_heads* dk, const nvfp4_heads* dv, void* workspace,
+                                                size_t workspace_bytes, uint32_t* dev_status, void* stream);
+
 /* Synchronises `stream`, reads *dev_status and returns it as a status. */
 NVFP4_API nvfp4_status nvfp4_status_query(const uint32_t* dev_status, void* stream);
 

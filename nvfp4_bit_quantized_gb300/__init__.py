@@ -16,10 +16,13 @@ from .api import (QTensor, quantize, quantize_dual, gemm, linear_fprop, linear_d
                   status_query, dev_status, reset_status, scales_mma_bytes, NVFP4Error, sqrelu_forward,
                   sqrelu_backward, gemm_sqrelu_backward, gemm_sqrelu_maxima, MXTensor, mx_quantize, mx_gemm, mx_scales_mma_bytes,
                   reset_gemm_workspaces)
+from .training import (layer_norm_forward, layer_norm_backward, attention_forward, attention_backward, AdamW,
+                       STATE_BLOCK)
 from ._lib import F32, BF16, RNE, SR, ROW, COL, TILE16, EXPORTS, LIB_PATH
 
 __all__ = ["QTensor", "quantize", "quantize_dual", "gemm", "linear_fprop", "linear_dgrad", "linear_wgrad", "quantize_weight",
            "status_query", "dev_status", "reset_status", "scales_mma_bytes", "NVFP4Error", "sqrelu_forward",
            "sqrelu_backward", "gemm_sqrelu_backward", "gemm_sqrelu_maxima", "MXTensor", "mx_quantize", "mx_gemm", "mx_scales_mma_bytes",
-           "reset_gemm_workspaces",
+           "reset_gemm_workspaces", "layer_norm_forward", "layer_norm_backward", "attention_forward",
+           "attention_backward", "AdamW", "STATE_BLOCK",
            "F32", "BF16", "RNE", "SR", "ROW", "COL", "TILE16", "EXPORTS", "LIB_PATH"]

@@ -25,6 +25,9 @@ EXPORTS = [
     "nvfp4_mx_scales_mma_bytes", "nvfp4_mx_quantize", "nvfp4_mx_gemm", "nvfp4_gemm_sqrelu_bwd",
     "nvfp4_sqrelu_maxima_bytes", "nvfp4_gemm_sqrelu_maxima", "nvfp4_quantize_dual_sqrelu_premax",
     "nvfp4_gemm_sqrelu_bwd_maxima", "nvfp4_quantize_dual_premax",
+    "nvfp4_layer_norm_forward", "nvfp4_layer_norm_backward_workspace_bytes", "nvfp4_layer_norm_backward",
+    "nvfp4_attention_forward", "nvfp4_attention_backward_workspace_bytes", "nvfp4_attention_backward",
+    "nvfp4_adamw_step",
 ]
 
 
@@ -37,6 +40,29 @@ class QTensorC(ctypes.Structure):
     _fields_ = [("codes", ctypes.c_void_p), ("scales", ctypes.c_void_p), ("scales_mma", ctypes.c_void_p),
                 ("s_dec", ctypes.c_void_p), ("codes_t", ctypes.c_void_p), ("scales_mma_t", ctypes.c_void_p),
                 ("rows", ctypes.c_int64), ("cols", ctypes.c_int64)]
+
+
+class AdamWTensorC(ctypes.Structure):
+    _fields_ = [("param", ctypes.c_void_p), ("grad", ctypes.c_void_p), ("m", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("m_scale", ctypes.c_void_p), ("v_scale", ctypes.c_void_p), ("n", ctypes.c_int64),
+                ("param_dtype", ctypes.c_int32), ("grad_dtype", ctypes.c_int32), ("weight_decay", ctypes.c_double),
+                ("id", ctypes.c_int64)]
+
+
+class AdamWParams(ctypes.Structure):
+    _fields_ = [("bits", ctypes.c_int32), ("round", ctypes.c_int32), ("step", ctypes.c_int64), ("lr", ctypes.c_double),
+                ("beta1", ctypes.c_double), ("beta2", ctypes.c_double), ("eps", ctypes.c_double),
+                ("sr_seed", ctypes.c_uint64)]
+
+
+class HeadsC(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("token_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class AttentionShapeC(ctypes.Structure):
+    _fields_ = [("tq", ctypes.c_int64), ("tk", ctypes.c_int64), ("heads", ctypes.c_int32), ("kv_heads", ctypes.c_int32),
+                ("dim", ctypes.c_int32), ("causal", ctypes.c_int32), ("scale", ctypes.c_float), ("nseq", ctypes.c_int32),
+                ("cu_q", ctypes.c_void_p), ("cu_k", ctypes.c_void_p)]
 
 
 class NVFP4Error(RuntimeError):
@@ -63,7 +89,9 @@ def lib():
         L = ctypes.CDLL(LIB_PATH)
         c = ctypes
         P, I64, I32, U32, U64, SZ = c.c_void_p, c.c_int64, c.c_int32, c.c_uint32, c.c_uint64, c.c_size_t
+        F32T = c.c_float
         QP, QT = c.POINTER(QParams), c.POINTER(QTensorC)
+        HD, AS = c.POINTER(HeadsC), c.POINTER(AttentionShapeC)
         sigs = {
             "nvfp4_scales_mma_bytes": (SZ, [I64, I64]),
             "nvfp4_quantize_workspace_bytes": (SZ, [I64, I64, QP]),
@@ -99,6 +127,15 @@ def lib():
             "nvfp4_quantize_dual_sqrelu_premax": (I32, [P, I32, I64, I64, I64, QP, QT, QP, QT, P, SZ, P, P]),
             "nvfp4_gemm_sqrelu_bwd_maxima": (I32, [QT, QT, P, I64, P, I64, U64, P, SZ, P, P]),
             "nvfp4_quantize_dual_premax": (I32, [P, I32, I64, I64, I64, QP, QT, QP, QT, P, SZ, P, P]),
+            "nvfp4_layer_norm_forward": (I32, [P, I32, I64, I64, I64, P, I64, P, P, I32, F32T, P, I32, I64, P, I64,
+                                               P, P, P]),
+            "nvfp4_layer_norm_backward_workspace_bytes": (SZ, [I64, I64]),
+            "nvfp4_layer_norm_backward": (I32, [P, I32, I64, P, I32, I64, I64, I64, P, I32, P, P, P, I64, P, I64,
+                                                P, P, P, SZ, P]),
+            "nvfp4_attention_forward": (I32, [AS, HD, HD, HD, HD, P, P, P]),
+            "nvfp4_attention_backward_workspace_bytes": (SZ, [AS]),
+            "nvfp4_attention_backward": (I32, [AS, HD, HD, HD, HD, HD, P, HD, HD, HD, P, SZ, P, P]),
+            "nvfp4_adamw_step": (I32, [P, I32, c.POINTER(AdamWParams), P, P, P]),
         }
         for name, (res, args) in sigs.items():
             fn = getattr(L, name)

@@ -1,0 +1,110 @@
+"""Argument checks of the training operators' C entries, on the CPU: nothing is launched."""
+import ctypes
+
+import pytest
+
+
+@pytest.fixture(scope="module")
+def lib():
+    import __graft_entry__
+    __graft_entry__.build_library()
+    from nvfp4_bit_quantized_gb300 import _lib
+    return _lib
+
+
+FAR = 0x10000
+
+
+def test_layer_norm_rejects_bad_arguments(lib):
+    L = lib.lib()
+    good = dict(x=FAR, xt=1, rows=4, cols=64, ldx=64, res=None, ldr=0, w=FAR, b=None, wt=0, eps=1e-5, y=FAR, yt=1, ldy=64,
+                h=None, ldh=0, mean=FAR, rstd=FAR)
+
+    def fwd(**kw):
+        return L.nvfp4_layer_norm_forward(*{**good, **kw}.values(), None)
+    for kw, want in [(dict(xt=3), lib.ERR_INVALID_ARG), (dict(yt=-1), lib.ERR_INVALID_ARG), (dict(wt=2), lib.ERR_INVALID_ARG),
+                     (dict(cols=0), lib.ERR_SHAPE), (dict(rows=-1), lib.ERR_SHAPE), (dict(ldx=63), lib.ERR_SHAPE),
+                     (dict(ldy=63), lib.ERR_SHAPE), (dict(eps=-1.0), lib.ERR_INVALID_ARG),
+                     (dict(eps=float("inf")), lib.ERR_INVALID_ARG), (dict(eps=float("nan")), lib.ERR_INVALID_ARG),
+                     (dict(x=None), lib.ERR_INVALID_ARG), (dict(w=None), lib.ERR_INVALID_ARG),
+                     (dict(mean=None), lib.ERR_INVALID_ARG), (dict(res=FAR, ldr=64), lib.ERR_INVALID_ARG),
+                     (dict(res=FAR, ldr=63, h=FAR, ldh=64), lib.ERR_SHAPE), (dict(x=FAR + 1), lib.ERR_ALIGNMENT),
+                     (dict(w=FAR + 2), lib.ERR_ALIGNMENT), (dict(rows=0, x=None), lib.OK)]:
+        assert fwd(**kw) == want, kw
+    size = L.nvfp4_layer_norm_backward_workspace_bytes(4, 64)
+    assert size > 0 and L.nvfp4_layer_norm_backward_workspace_bytes(4, 0) == 0
+    good = dict(dy=FAR, yt=1, lddy=64, x=FAR, xt=1, rows=4, cols=64, ldx=64, w=FAR, wt=0, mean=FAR, rstd=FAR, dh=None, lddh=0,
+                dx=FAR, lddx=64, dw=FAR, db=None, ws=FAR, n=size)
+
+    def bwd(**kw):
+        return L.nvfp4_layer_norm_backward(*{**good, **kw}.values(), None)
+    for kw, want in [(dict(xt=9), lib.ERR_INVALID_ARG), (dict(cols=0), lib.ERR_SHAPE), (dict(lddy=1), lib.ERR_SHAPE),
+                     (dict(lddx=1), lib.ERR_SHAPE), (dict(dh=FAR, lddh=3), lib.ERR_SHAPE), (dict(dw=None), lib.ERR_INVALID_ARG),
+                     (dict(rstd=None), lib.ERR_INVALID_ARG), (dict(dw=FAR + 2), lib.ERR_ALIGNMENT),
+                     (dict(ws=None), lib.ERR_WORKSPACE), (dict(n=size - 1), lib.ERR_WORKSPACE),
+                     (dict(ws=FAR + 4), lib.ERR_WORKSPACE)]:
+        assert bwd(**kw) == want, kw
+
+
+def test_attention_rejects_bad_arguments(lib):
+    L, ref = lib.lib(), ctypes.byref
+
+    def shape(**kw):
+        a = dict(tq=8, tk=8, heads=4, kv_heads=2, dim=64, causal=1, scale=0.125, nseq=1, cu_q=None, cu_k=None)
+        return lib.AttentionShapeC(*{**a, **kw}.values())
+
+    def heads(data=FAR, ts=512, hs=64):
+        return lib.HeadsC(data, ts, hs)
+
+    def fwd(s, q=None, lse=FAR):
+        q = heads() if q is None else q
+        return L.nvfp4_attention_forward(ref(s), ref(q), ref(heads()), ref(heads()), ref(heads()), lse, None, None)
+
+    def bwd(s, ws=FAR, n=1 << 30):
+        h = ref(heads())
+        return L.nvfp4_attention_backward(ref(s), h, h, h, h, h, FAR, h, h, h, ws, n, None, None)
+    for kw, want in [(dict(tq=-1), lib.ERR_SHAPE), (dict(heads=3), lib.ERR_SHAPE), (dict(kv_heads=0), lib.ERR_SHAPE),
+                     (dict(dim=60), lib.ERR_SHAPE), (dict(dim=136), lib.ERR_SHAPE), (dict(dim=0), lib.ERR_SHAPE),
+                     (dict(nseq=0), lib.ERR_INVALID_ARG), (dict(nseq=2), lib.ERR_INVALID_ARG),
+                     (dict(cu_q=FAR), lib.ERR_INVALID_ARG), (dict(cu_q=FAR, cu_k=FAR + 2), lib.ERR_ALIGNMENT),
+                     (dict(scale=float("nan")), lib.ERR_INVALID_ARG)]:
+        assert fwd(shape(**kw)) == want, kw
+        assert bwd(shape(**kw)) == want, kw
+        assert L.nvfp4_attention_backward_workspace_bytes(ref(shape(**kw))) == 0
+    assert fwd(shape(), heads(None)) == lib.ERR_INVALID_ARG
+    assert fwd(shape(), heads(FAR + 8)) == lib.ERR_ALIGNMENT
+    assert fwd(shape(), heads(ts=260)) == lib.ERR_ALIGNMENT
+    assert fwd(shape(), heads(hs=68)) == lib.ERR_ALIGNMENT
+    assert fwd(shape(), heads(hs=0)) == lib.ERR_SHAPE
+    assert fwd(shape(), heads(ts=32)) == lib.ERR_SHAPE
+    assert fwd(shape(), lse=None) == lib.ERR_INVALID_ARG
+    assert fwd(shape(tq=0), heads(None)) == lib.OK
+    need = L.nvfp4_attention_backward_workspace_bytes(ref(shape()))
+    assert need >= 4 * 8 * 4
+    assert bwd(shape(), ws=None) == lib.ERR_WORKSPACE
+    assert bwd(shape(), n=need - 1) == lib.ERR_WORKSPACE
+    assert bwd(shape(), ws=FAR + 4) == lib.ERR_WORKSPACE
+
+
+def test_adamw_rejects_bad_arguments(lib):
+    L = lib.lib()
+
+    def call(t=None, count=1, **kw):
+        a = dict(param=FAR, grad=FAR, m=FAR, v=FAR, ms=FAR, vs=FAR, n=100, pt=0, gt=1, wd=0.1, id=0)
+        h = dict(bits=8, round=1, step=1, lr=0.1, b1=0.9, b2=0.95, eps=1e-8, seed=1)
+        tensor = (lib.AdamWTensorC * 1)(lib.AdamWTensorC(*{**a, **(t or {})}.values()))
+        hp = lib.AdamWParams(*{**h, **kw}.values())
+        return L.nvfp4_adamw_step(tensor, count, ctypes.byref(hp), None, None, None)
+    for t, kw, want in [({}, dict(bits=16), lib.ERR_INVALID_ARG), ({}, dict(round=2), lib.ERR_INVALID_ARG),
+                        ({}, dict(step=0), lib.ERR_INVALID_ARG), ({}, dict(step=2**32), lib.ERR_INVALID_ARG),
+                        ({}, dict(b1=1.0), lib.ERR_INVALID_ARG), ({}, dict(b2=-0.1), lib.ERR_INVALID_ARG),
+                        ({}, dict(eps=-1.0), lib.ERR_INVALID_ARG), ({}, dict(lr=float("inf")), lib.ERR_INVALID_ARG),
+                        (dict(n=-1), {}, lib.ERR_SHAPE), (dict(pt=2), {}, lib.ERR_INVALID_ARG),
+                        (dict(gt=-1), {}, lib.ERR_INVALID_ARG), (dict(id=-1), {}, lib.ERR_INVALID_ARG),
+                        (dict(wd=float("nan")), {}, lib.ERR_INVALID_ARG), (dict(param=None), {}, lib.ERR_INVALID_ARG),
+                        (dict(ms=None), {}, lib.ERR_INVALID_ARG), (dict(param=FAR + 2), {}, lib.ERR_ALIGNMENT),
+                        (dict(m=FAR + 1), dict(bits=32), lib.ERR_ALIGNMENT), (dict(vs=FAR + 1), {}, lib.ERR_ALIGNMENT),
+                        (dict(n=0, param=None), {}, lib.OK), (dict(grad=None), {}, lib.OK)]:
+        assert call(t, **kw) == want, (t, kw)
+    assert call(count=0) == lib.OK and call(count=-1) == lib.ERR_INVALID_ARG
+    assert L.nvfp4_adamw_step(None, 1, None, None, None, None) == lib.ERR_INVALID_ARG
