@@ -19,7 +19,7 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libnvfp4_gb300.so")
 SOURCES = ["quantize.cu", "gemm.cu", "linear.cu", "capi.cu", "activation.cu", "mx.cu", "norm.cu", "attention.cu",
            "optimizer.cu"]
-HEADERS = ["device_common.cuh", "host_common.h"]
+HEADERS = ["device_common.cuh", "host_common.h", "tcgen05_bf16.cuh"]
 
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 NVCC_FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "-Xcompiler", "-fvisibility=hidden",

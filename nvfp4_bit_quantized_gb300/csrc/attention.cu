@@ -1,17 +1,47 @@
 // attention.cu -- attention over packed sequences, forward and backward (include/nvfp4.h has the
-// formulas).  bf16 heads of at most 128 elements; sums and softmax statistics in fp32.
+// formulas), on the tcgen05 tensor cores: bf16 heads of at most 128 elements, fp32 accumulators in
+// TMEM, fp32 softmax statistics and sums.
+//
+// Three kernels, each one CTA per SM on one tile of rows that stays in shared memory while tiles of
+// 128 rows of the other side stream past by TMA (HD = 64 or 128: the head size rounded up; the MMAs
+// themselves run over the head size rounded up to 16):
+//   fwd   256 queries of a head as two tiles; S = Q K^T, P = exp2(c S - m), O += P V;
+//   dq    128 queries of a head;   S = Q K^T, dP = dO V^T, dS = P (dP - delta), dQ += dS K;
+//   dkv   128 keys of a key head, over all query heads that read it;
+//         S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q.
+// P and dS go back to TMEM as bf16 and are the A operand of their product from there; the streamed
+// tile that was the K-major B operand of the first product is the MN-major B operand of the second, so
+// each tile is loaded once.  The backward pass computes S and dP in both of its kernels (7 products
+// instead of 5): in exchange dQ needs neither atomics (whose order would change the result from run
+// to run) nor a pass of partial sums through memory.
+//
+// Tiles that reach past their sequence: rows past the tensor's end arrive as zeros (TMA); rows
+// of a neighbouring sequence are zeroed in shared memory before the MMAs read them where they are summed
+// over (a zero probability times a neighbour's NaN would be NaN).
+//
+// Every wait is bounded (mbar_wait_bounded): on a timeout the kernel records NVFP4_ERR_TIMEOUT, every
+// role leaves its loop, copies and MMAs in flight are waited for, TMEM is freed.
+#include <cuda.h>
+#include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
+#include <climits>
 #include <cmath>
 #include <cstdint>
+#include <cstring>
+#include <mutex>
 
 #include "device_common.cuh"
 #include "host_common.h"
+#include "tcgen05_bf16.cuh"
 
 namespace nvfp4 {
 namespace attn {
 
 using bf16 = __nv_bfloat16;
+using namespace tc;
+
+constexpr float kLog2e = 1.4426950408889634f, kLn2 = 0.6931471805599453f;
 
 struct Heads {
     bf16* p;
@@ -20,163 +50,929 @@ struct Heads {
 };
 
 struct Params {
-    Heads q, k, v, out, dout, dq, dk, dv;
-    float* lse;
-    float* delta;
+    Heads out, dout, dq, dk, dv;               // tensors reached by plain loads and stores
+    float *lse, *delta;
     int64_t tq, tk;
     int heads, kv_heads, dim, causal, nseq;
     float scale;
+    float c;                                   // |scale| log2(e), kept off zero; the MMAs negate A for scale < 0
     const int32_t *cu_q, *cu_k;
     uint32_t* dev_status;
+    uint64_t timeout_ns;
 };
 
-// Bounds of sequence s among `total` tokens, forced into range whatever the offsets hold.
+// One CTA's rows.  `first` .. first + rows - 1 are its tile's tokens of one sequence; the other
+// side's sequence is `other` .. other + other_len - 1.  diag: row r of the tile faces other row
+// r + diag on the causal diagonal.
+struct Item {
+    int valid;
+    int head;
+    int64_t first, other;
+    int rows, other_len, diag;
+};
+
 __device__ __forceinline__ void seq_bounds(const int32_t* cu, int s, int64_t total, int64_t& a, int64_t& b) {
     if (!cu) {
         a = 0;
         b = total;
         return;
     }
-    a = min(max((int64_t)cu[s], (int64_t)0), total);
+    a = min(max((int64_t)cu[s], (int64_t)0), total);       // in range whatever the offsets hold
     b = min(max((int64_t)cu[s + 1], a), total);
 }
 
-// The sequence a token belongs to: the first whose end lies beyond it.
-__device__ __forceinline__ int seq_of(const int32_t* cu, int nseq, int64_t t) {
-    if (!cu) return 0;
-    int lo = 0, hi = nseq - 1;
-    while (lo < hi) {
-        const int mid = (lo + hi) / 2;
-        if (cu[mid + 1] > t) hi = mid;
-        else lo = mid + 1;
-    }
-    return lo;
-}
-
-__global__ void check_offsets_kernel(Params p) {
-    pdl_launch_dependents();
-    pdl_wait();
-    for (int which = 0; which < 2; ++which) {
-        const int32_t* cu = which ? p.cu_k : p.cu_q;
-        const int64_t total = which ? p.tk : p.tq;
-        for (int i = threadIdx.x; i < p.nseq; i += blockDim.x)
-            if (cu[i] > cu[i + 1] || (i == 0 && cu[0] != 0) || (i == p.nseq - 1 && cu[p.nseq] != total))
-                set_status(p.dev_status, NVFP4_ERR_INVALID_ARG);
-    }
-}
-
-__device__ __forceinline__ void load_row(const bf16* p, int dim, float (&f)[4]) {
+// Whole warp: the tile and head of this CTA.  Tiles are numbered through the sequences; CTAs take
+// the last first (with a causal mask the longest of a sequence, of queries; of keys the other way
+// round), heads fastest, so that CTAs that run together read the same K and V.
+__device__ __forceinline__ void find_item(const Params& p, bool rows_are_q, int tile, int heads, Item* out) {
     const int lane = threadIdx.x & 31;
+    const int32_t* cu = rows_are_q ? p.cu_q : p.cu_k;
+    const int64_t total = rows_are_q ? p.tq : p.tk;
+    const int head = blockIdx.x % heads;
+    int64_t n = 0;                                         // tiles in all
+    bool bad = false;
+    for (int s0 = 0; s0 < p.nseq; s0 += 32) {
+        const int s = s0 + lane;
+        int64_t tiles = 0;
+        if (s < p.nseq) {
+            int64_t a, b;
+            seq_bounds(cu, s, total, a, b);
+            tiles = (b - a + tile - 1) / tile;
+            if (p.cu_q && blockIdx.x == 0)
+                for (int w = 0; w < 2; ++w) {
+                    const int32_t* o = w ? p.cu_k : p.cu_q;
+                    bad |= o[s] > o[s + 1] || (s == 0 && o[0] != 0) ||
+                           (s == p.nseq - 1 && o[p.nseq] != (w ? p.tk : p.tq));
+                }
+        }
 #pragma unroll
-    for (int j = 0; j < 4; ++j) f[j] = lane + 32 * j < dim ? __bfloat162float(p[lane + 32 * j]) : 0.0f;
+        for (int d = 16; d; d >>= 1) tiles += __shfl_xor_sync(~0u, tiles, d);
+        n += tiles;
+    }
+    if (bad) set_status(p.dev_status, NVFP4_ERR_INVALID_ARG);
+    int64_t want = blockIdx.x / heads;
+    if (rows_are_q) want = n - 1 - want;
+    if (want < 0 || want >= n) {
+        if (lane == 0) out->valid = 0;
+        return;
+    }
+    for (int s0 = 0; s0 < p.nseq; s0 += 32) {
+        const int s = s0 + lane;
+        int64_t a = 0, b = 0;
+        if (s < p.nseq) seq_bounds(cu, s, total, a, b);
+        const int64_t tiles = (b - a + tile - 1) / tile;
+        int64_t upto = tiles;                              // inclusive prefix
+#pragma unroll
+        for (int d = 1; d < 32; d <<= 1) {
+            const int64_t v = __shfl_up_sync(~0u, upto, d);
+            if (lane >= d) upto += v;
+        }
+        if (want >= upto - tiles && want < upto) {
+            const int64_t t0 = (want - (upto - tiles)) * tile;
+            int64_t oa, ob;
+            seq_bounds(rows_are_q ? p.cu_k : p.cu_q, s, rows_are_q ? p.tk : p.tq, oa, ob);
+            out->valid = 1;
+            out->head = head;
+            out->first = a + t0;
+            out->rows = (int)min((int64_t)tile, b - a - t0);
+            out->other = oa;
+            out->other_len = (int)(ob - oa);
+            out->diag = (int)(t0 + (ob - oa) - (b - a));
+        }
+        const int64_t all = __shfl_sync(~0u, upto, 31);
+        if (want < all) break;
+        want -= all;
+    }
 }
-__device__ __forceinline__ void store_row(bf16* p, int dim, const float (&f)[4]) {
+
+struct Wait {
+    uint64_t timeout_ns;
+    volatile uint32_t* abort;
+    uint32_t* dev_status;
+    __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+        return mbar_wait_bounded(bar, parity & 1u, timeout_ns, abort, dev_status);
+    }
+    // after an abort: still bounded, but not cut short by it
+    __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) const {
+        mbar_wait_bounded(bar, parity & 1u, timeout_ns, nullptr, dev_status);
+    }
+};
+
+// One lane: a tile of 128 tokens from token t of head h, HD / 64 boxes.
+template <int HD>
+__device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* tm, int64_t t, int h, uint64_t* bar) {
+#pragma unroll
+    for (int b = 0; b < HD / 64; ++b)
+        tma_load_3d(smem_addr(dst + b * kBoxBytes), tm, b * 64, (int)t, h, smem_addr(bar));
+}
+
+// Whole warp: zeroes rows `valid` .. 127 of a tile that the async proxy reads next.
+template <int HD>
+__device__ __forceinline__ void zero_tail(uint8_t* tile, int valid) {
     const int lane = threadIdx.x & 31;
+    for (int i = lane; i < (kRows - valid) * 8; i += 32)
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-        if (lane + 32 * j < dim) p[lane + 32 * j] = __float2bfloat16_rn(f[j]);
-}
-__device__ __forceinline__ float dot(const float (&a)[4], const float (&b)[4]) {
-    float s = a[0] * b[0] + a[1] * b[1] + a[2] * b[2] + a[3] * b[3];
-#pragma unroll
-    for (int d = 16; d; d >>= 1) s += __shfl_xor_sync(~0u, s, d);
-    return s;
+        for (int b = 0; b < HD / 64; ++b)
+            *reinterpret_cast<uint4*>(tile + b * kBoxBytes + valid * 128 + i * 16) = make_uint4(0, 0, 0, 0);
+    fence_proxy_async_smem();
+    __syncwarp();
 }
 
-// Keys [k0, kend) that query t of its sequence sees.
-__device__ __forceinline__ void keys_of(const Params& p, int64_t t, int64_t& k0, int64_t& kend) {
-    const int s = seq_of(p.cu_q, p.nseq, t);
-    int64_t q0, q1, k1;
-    seq_bounds(p.cu_q, s, p.tq, q0, q1);
-    seq_bounds(p.cu_k, s, p.tk, k0, k1);
-    kend = p.causal ? max(k0, min(k1, k1 - (q1 - t) + 1)) : k1;
-}
-
-// One warp per query and head: the running maximum and sum of the softmax over the keys in turn.
-__global__ void __launch_bounds__(256) fwd_kernel(Params p) {
-    pdl_launch_dependents();
-    pdl_wait();
-    const int64_t t = blockIdx.x * 8ll + (threadIdx.x >> 5);
-    const int h = blockIdx.y, hk = h / (p.heads / p.kv_heads);
-    if (t >= p.tq) return;
-    int64_t k0, kend;
-    keys_of(p, t, k0, kend);
-    float q[4], o[4] = {0, 0, 0, 0}, m = -INFINITY, l = 0.0f;
-    load_row(p.q.at(t, h), p.dim, q);
-    for (int64_t j = k0; j < kend; ++j) {
-        float k[4], v[4];
-        load_row(p.k.at(j, hk), p.dim, k);
-        load_row(p.v.at(j, hk), p.dim, v);
-        const float z = dot(q, k) * p.scale, mn = fmaxf(m, z), ms = mn == -INFINITY ? 0.0f : mn;
-        const float a = expf(m - ms), e = expf(z - ms);
-        l = l * a + e;
-#pragma unroll
-        for (int i = 0; i < 4; ++i) o[i] = o[i] * a + e * v[i];
-        m = mn;
+// One lane.  D[128, n] (+)= A B^T over the head dimension: both tiles K-major.
+__device__ __forceinline__ void mma_heads(uint32_t d, const uint8_t* a, const uint8_t* b, int dim, uint32_t idesc) {
+    const uint32_t sa = smem_addr(a), sb = smem_addr(b);
+    for (int k = 0; k < dim; k += 16) {
+        const uint32_t off = (k >> 6) * kBoxBytes + (k & 63) * 2;
+        mma_ss(d, desc_k_major(sa + off), desc_k_major(sb + off), idesc, k != 0);
     }
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+}
+// One lane.  D[128, dim] (+)= A B with A 128 x 128 bf16 in TMEM: K 0-63 at a0, 64-127 at a1; B a tile of 128 rows.
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a0, uint32_t a1, const uint8_t* b, uint32_t idesc,
+                                         bool accumulate) {
+    const uint32_t sb = smem_addr(b);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] *= inv;
-    store_row(p.out.at(t, h), p.dim, o);
-    if ((threadIdx.x & 31) == 0) p.lse[h * p.tq + t] = m + logf(l);
+    for (int k = 0; k < 8; ++k)
+        mma_ts(d, k < 4 ? a0 + k * 8 : a1 + (k - 4) * 8, desc_mn_major(sb + k * 2048), idesc, accumulate || k != 0);
 }
 
-// delta = sum(dout * out), and dq of one query and head per warp.
-__global__ void __launch_bounds__(256) bwd_dq_kernel(Params p) {
-    pdl_launch_dependents();
-    pdl_wait();
-    const int64_t t = blockIdx.x * 8ll + (threadIdx.x >> 5);
-    const int h = blockIdx.y, hk = h / (p.heads / p.kv_heads);
-    if (t >= p.tq) return;
-    int64_t k0, kend;
-    keys_of(p, t, k0, kend);
-    float q[4], o[4], d[4], dq[4] = {0, 0, 0, 0};
-    load_row(p.q.at(t, h), p.dim, q);
-    load_row(p.out.at(t, h), p.dim, o);
-    load_row(p.dout.at(t, h), p.dim, d);
-    const float delta = dot(o, d), lse = p.lse[h * p.tq + t];
-    if ((threadIdx.x & 31) == 0) p.delta[h * p.tq + t] = delta;
-    for (int64_t j = k0; j < kend; ++j) {
-        float k[4], v[4];
-        load_row(p.k.at(j, hk), p.dim, k);
-        load_row(p.v.at(j, hk), p.dim, v);
-        const float ds = expf(dot(q, k) * p.scale - lse) * (dot(d, v) - delta) * p.scale;
+// A row of `dim` bf16 values (a multiple of 8), 32 columns at a time: v * f, or zeros.
+__device__ __forceinline__ void store32(bf16* row, int col, int dim, const uint32_t (&v)[32], float f) {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) dq[i] += ds * k[i];
+    for (int i = 0; i < 32; i += 8)
+        if (col + i < dim) {
+            uint32_t w[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                w[j] = pack_bf16(__uint_as_float(v[i + 2 * j]) * f, __uint_as_float(v[i + 2 * j + 1]) * f);
+            *reinterpret_cast<uint4*>(row + col + i) = make_uint4(w[0], w[1], w[2], w[3]);
+        }
+}
+__device__ __forceinline__ void store_zeros(bf16* row, int dim) {
+    for (int i = 0; i < dim; i += 8) *reinterpret_cast<uint4*>(row + i) = make_uint4(0, 0, 0, 0);
+}
+
+__device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
+    return p + ((1024u - (smem_addr(p) & 1023u)) & 1023u);
+}
+
+// ---------------------------------------------------------------------------- forward
+// Warps 0-3 and 4-7: the softmax of tile 0 and tile 1, a row per thread; warp 8: TMA; warp 9: MMAs.  While one
+// tile's softmax runs, the tensor cores work on the other tile.  TMEM: S (then P, bf16, in its first 64
+// columns) of tile t at 128 t, O of tile t at 256 + 128 t.  O is rescaled only when a row's maximum has
+// grown by more than 2^8 since it was last taken: P stays below 2^8 and the final division by the
+// sum cancels the choice.
+constexpr int kFwdThreads = 320;
+template <int HD> struct Fwd {
+    static constexpr int TILE = kRows * HD * 2;
+    static constexpr int STAGES = HD == 128 ? 4 : 8;
+    static constexpr int SMEM = (2 + STAGES) * TILE + 1024;
+};
+
+template <int HD>
+__global__ void __launch_bounds__(kFwdThreads, 1)
+fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+           const __grid_constant__ CUtensorMap tmv, const Params p) {
+    constexpr int TILE = Fwd<HD>::TILE, ST = Fwd<HD>::STAGES;
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t q_full, full[ST], empty[ST], s_full[2], p_ready[2], o_full[2], mma_done;
+    __shared__ uint32_t tmem_slot, abort_flag;
+    __shared__ Item item;
+    uint8_t* smem_q = align1024(raw);
+    uint8_t* ring = smem_q + 2 * TILE;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    pdl_launch_dependents();
+    if (threadIdx.x == 0) {
+        mbar_init(&q_full, 1);
+        for (int i = 0; i < ST; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&s_full[t], 1);
+            mbar_init(&p_ready[t], 4);
+            mbar_init(&o_full[t], 1);
+        }
+        mbar_init(&mma_done, 1);
+        abort_flag = 0u;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    store_row(p.dq.at(t, h), p.dim, dq);
-}
-
-// dk and dv of one key and key head per warp, over the queries of the heads that share it.
-__global__ void __launch_bounds__(256) bwd_dkv_kernel(Params p) {
-    pdl_launch_dependents();
+    if (warp == 9) tmem_alloc_all(&tmem_slot);
     pdl_wait();
-    const int64_t j = blockIdx.x * 8ll + (threadIdx.x >> 5);
-    const int hk = blockIdx.y, share = p.heads / p.kv_heads;
-    if (j >= p.tk) return;
-    const int s = seq_of(p.cu_k, p.nseq, j);
-    int64_t q0, q1, k0, k1;
-    seq_bounds(p.cu_q, s, p.tq, q0, q1);
-    seq_bounds(p.cu_k, s, p.tk, k0, k1);
-    const int64_t first = p.causal ? max(q0, q1 - (k1 - j)) : q0;
-    float k[4], v[4], dk[4] = {0, 0, 0, 0}, dv[4] = {0, 0, 0, 0};
-    load_row(p.k.at(j, hk), p.dim, k);
-    load_row(p.v.at(j, hk), p.dim, v);
-    for (int h = hk * share; h < (hk + 1) * share; ++h)
-        for (int64_t t = first; t < q1; ++t) {
-            float q[4], d[4];
-            load_row(p.q.at(t, h), p.dim, q);
-            load_row(p.dout.at(t, h), p.dim, d);
-            const float e = expf(dot(q, k) * p.scale - p.lse[h * p.tq + t]);
-            const float ds = e * (dot(d, v) - p.delta[h * p.tq + t]) * p.scale;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                dv[i] += e * d[i];
-                dk[i] += ds * q[i];
+    if (warp == 8) find_item(p, true, 2 * kRows, p.heads, &item);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = tmem_slot;
+    const Wait wait{p.timeout_ns, &abort_flag, p.dev_status};
+    const int hk = item.head / (p.heads / p.kv_heads);
+
+    // rows and key tiles of each of the two query tiles
+    int rows[2] = {0, 0}, n[2] = {0, 0}, steps = 0;
+    if (item.valid) {
+        for (int t = 0; t < 2; ++t) {
+            rows[t] = min(max(item.rows - kRows * t, 0), kRows);
+            int keys = item.other_len;
+            if (p.causal) keys = min(keys, max(0, kRows * t + rows[t] + item.diag));
+            n[t] = rows[t] ? (keys + kRows - 1) / kRows : 0;
+            steps = max(steps, n[t]);
+        }
+    }
+
+    if (warp == 8 && steps > 0) {
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&q_full, TILE * (rows[1] ? 2 : 1));
+            load_tile<HD>(smem_q, &tmq, item.first, item.head, &q_full);
+            if (rows[1]) load_tile<HD>(smem_q + TILE, &tmq, item.first + kRows, item.head, &q_full);
+            int i = 0;                                     // K of step 0, V of step 0, K of step 1, ...
+            for (; i < 2 * steps; ++i) {
+                const int slot = i % ST;
+                if (i >= ST && !wait(&empty[slot], i / ST - 1)) break;
+                mbar_arrive_expect_tx(&full[slot], TILE);
+                load_tile<HD>(ring + slot * TILE, (i & 1) ? &tmv : &tmk, item.other + (int64_t)(i >> 1) * kRows, hk, &full[slot]);
+            }
+            if (i < 2 * steps) {                           // aborted: the copies in flight land first
+                wait.drain(&q_full, 0);
+                for (int j = max(0, i - ST); j < i; ++j) wait.drain(&full[j % ST], j / ST);
             }
         }
-    store_row(p.dk.at(j, hk), p.dim, dk);
-    store_row(p.dv.at(j, hk), p.dim, dv);
+    } else if (warp == 9 && steps > 0) {
+        const uint32_t idesc_s = idesc_bf16(kRows, false, p.scale < 0.0f);
+        const uint32_t idesc_o = idesc_bf16((p.dim + 15) & ~15, true, false);
+        const bool neighbours = item.other + item.other_len < p.tk;
+        // the tile of step j (what = 0: K, 1: V) once it has arrived, its foreign rows zeroed
+        auto tile = [&](int j, int what) -> uint8_t* {
+            const int i = 2 * j + what, slot = i % ST;
+            if (!wait(&full[slot], i / ST)) return nullptr;
+            uint8_t* b = ring + slot * TILE;
+            const int valid = item.other_len - j * kRows;
+            if (valid < kRows && neighbours) zero_tail<HD>(b, valid);
+            return b;
+        };
+        bool ok = wait(&q_full, 0);
+        const uint8_t* k = ok ? tile(0, 0) : nullptr;
+        ok = ok && k;
+        if (ok && lane == 0) {
+            for (int t = 0; t < 2; ++t)
+                if (n[t] > 0) {
+                    mma_heads(tmem + 128 * t, smem_q + t * TILE, k, p.dim, idesc_s);
+                    commit(&s_full[t]);
+                }
+            commit(&empty[0]);
+        }
+        for (int j = 0; ok && j < steps; ++j) {
+            const uint8_t* v = tile(j, 1);
+            ok = v != nullptr;
+            const bool more = j + 1 < steps;
+            k = nullptr;
+            for (int t = 0; ok && t < 2; ++t) {
+                if (j >= n[t]) continue;
+                ok = wait(&p_ready[t], j);
+                if (!ok) break;
+                fence_after();
+                const uint32_t sp = tmem + 128 * t;
+                if (lane == 0) {
+                    mma_rows(tmem + 256 + 128 * t, sp, sp + 32, v, idesc_o, j > 0);
+                    if (j + 1 == n[t]) commit(&o_full[t]);
+                }
+                if (j + 1 < n[t]) {
+                    if (!k) k = tile(j + 1, 0);
+                    ok = k != nullptr;
+                    if (ok && lane == 0) {
+                        mma_heads(sp, smem_q + t * TILE, k, p.dim, idesc_s);
+                        commit(&s_full[t]);
+                    }
+                }
+            }
+            if (ok && lane == 0) {
+                commit(&empty[(2 * j + 1) % ST]);
+                if (more) commit(&empty[(2 * j + 2) % ST]);
+            }
+        }
+        if (lane == 0) {
+            commit(&mma_done);
+            wait.drain(&mma_done, 0);
+        }
+        __syncwarp();
+    } else if (warp < 8) {
+        const int t = warp >> 2, r = (warp & 3) * 32 + lane, row = kRows * t + r;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + 128 * t + lanes, to = tmem + 256 + 128 * t + lanes;
+        // keys this row sees, and those that every row of the tile sees
+        const int limit = p.causal ? min(item.other_len, max(0, row + item.diag + 1)) : item.other_len;
+        const int common = p.causal ? min(item.other_len, kRows * t + item.diag + 1) : item.other_len;
+        const float2 c2 = make_float2(p.c, p.c);
+        float m = -INFINITY, l = 0.0f;
+        bool ok = true;
+        for (int j = 0; j < n[t]; ++j) {
+            ok = wait(&s_full[t], j);
+            if (!ok) break;
+            fence_after();
+            uint32_t s[4][32];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) ld32(ts + 32 * i, s[i]);
+            ld_wait();
+#pragma unroll
+            for (int i = 0; i < 4; ++i) fence32(s[i]);
+            if ((j + 1) * kRows > common) {
+                const int lim = limit - j * kRows;
+#pragma unroll
+                for (int i = 0; i < 128; ++i)
+                    if (i >= lim) s[i >> 5][i & 31] = 0xFF800000u;
+            }
+            float mx[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                mx[i] = __uint_as_float(s[i][0]);
+#pragma unroll
+                for (int e = 1; e < 32; ++e) mx[i] = fmaxf(mx[i], __uint_as_float(s[i][e]));
+            }
+            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
+            const bool grow = top > m + 8.0f;
+            if (__any_sync(~0u, grow)) {
+                const float mn = grow ? top : m, f = grow ? ex2(m - mn) : 1.0f;
+                m = mn;
+                l *= f;
+                if (j > 0) {
+                    for (int i = 0; i < p.dim; i += 32) {
+                        uint32_t o[32];
+                        ld32(to + i, o);
+                        ld_wait();
+                        fence32(o);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                        st32(to + i, o);
+                    }
+                }
+            }
+            const float neg = m == -INFINITY ? 0.0f : -m;
+            const float2 neg2 = make_float2(neg, neg);
+            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t w[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    float2 x = make_float2(__uint_as_float(s[i][2 * e]), __uint_as_float(s[i][2 * e + 1]));
+                    x = __ffma2_rn(x, c2, neg2);
+                    x = make_float2(ex2(x.x), ex2(x.y));
+                    sum[e & 1] = __fadd2_rn(sum[e & 1], x);
+                    w[e] = pack_bf16(x.x, x.y);
+                }
+                st16(ts + 16 * i, w);
+            }
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            st_wait();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_ready[t]);
+        }
+        if (ok && n[t] > 0) {
+            ok = wait(&o_full[t], 0);
+            fence_after();
+        }
+        if (ok && rows[t] > 0) {                           // whole warps: the TMEM loads are collective
+            const bool store = r < rows[t];
+            bf16* dst = p.out.at(item.first + (store ? row : 0), item.head);
+            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+            if (n[t] == 0) {
+                if (store) store_zeros(dst, p.dim);
+            } else {
+                for (int i = 0; i < p.dim; i += 32) {
+                    uint32_t o[32];
+                    ld32(to + i, o);
+                    ld_wait();
+                    fence32(o);
+                    if (store) store32(dst, i, p.dim, o, inv);
+                }
+            }
+            if (store)
+                p.lse[(int64_t)item.head * p.tq + item.first + row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        fence_after();
+        tmem_free_all(tmem);
+    }
+}
+
+// ---------------------------------------------------------------------------- backward, dQ
+// Warps 0-7: a row per thread, warps 0-3 the first 64 keys of a tile, warps 4-7 the last 64; warp 8: TMA; warp 9:
+// MMAs.  TMEM: S of even and odd steps at 0 and 128 (dS takes S's place, in the columns its own warps
+// have read), dP at 256, dQ at 384.  The tensor cores do dQ of a step and S of the one after next while
+// the warps work on the step between.  The first kernel of the backward pass: it also leaves delta.
+constexpr int kDqThreads = 320;
+template <int HD> struct Dq {
+    static constexpr int TILE = kRows * HD * 2;
+    static constexpr int SMEM = 7 * TILE + 1024;           // Q, dO, three K, two V
+    static constexpr int PAD = HD == 128 ? SMEM : 120 * 1024;   // one CTA per SM: TMEM is taken whole
+};
+
+template <int HD>
+__global__ void __launch_bounds__(kDqThreads, 1)
+dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+          const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmdo, const Params p) {
+    constexpr int TILE = Dq<HD>::TILE;
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t q_full, k_full[3], k_empty[3], v_full[2], v_empty[2], s_full[2], dp_full, ds_ready, mma_done;
+    __shared__ uint32_t tmem_slot, abort_flag;
+    __shared__ Item item;
+    __shared__ float part[2][kRows];
+    uint8_t* smem_q = align1024(raw);
+    uint8_t* smem_do = smem_q + TILE;
+    uint8_t* ring_k = smem_do + TILE;
+    uint8_t* ring_v = ring_k + 3 * TILE;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    pdl_launch_dependents();
+    if (threadIdx.x == 0) {
+        mbar_init(&q_full, 1);
+        for (int i = 0; i < 3; ++i) {
+            mbar_init(&k_full[i], 1);
+            mbar_init(&k_empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&v_full[i], 1);
+            mbar_init(&v_empty[i], 1);
+            mbar_init(&s_full[i], 1);
+        }
+        mbar_init(&dp_full, 1);
+        mbar_init(&ds_ready, 8);
+        mbar_init(&mma_done, 1);
+        abort_flag = 0u;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 9) tmem_alloc_all(&tmem_slot);
+    pdl_wait();
+    if (warp == 8) find_item(p, true, kRows, p.heads, &item);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = tmem_slot;
+    const Wait wait{p.timeout_ns, &abort_flag, p.dev_status};
+    const int hk = item.head / (p.heads / p.kv_heads);
+    int steps = 0;
+    if (item.valid) {
+        const int keys = p.causal ? min(item.other_len, max(0, item.rows + item.diag)) : item.other_len;
+        steps = (keys + kRows - 1) / kRows;
+    }
+
+    if (warp == 8 && steps > 0) {
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&q_full, 2 * TILE);
+            load_tile<HD>(smem_q, &tmq, item.first, item.head, &q_full);
+            load_tile<HD>(smem_do, &tmdo, item.first, item.head, &q_full);
+            int got_k = 0, got_v = 0;
+            for (int j = 0; j < steps; ++j) {
+                if (j >= 3 && !wait(&k_empty[j % 3], j / 3 - 1)) break;
+                mbar_arrive_expect_tx(&k_full[j % 3], TILE);
+                load_tile<HD>(ring_k + (j % 3) * TILE, &tmk, item.other + (int64_t)j * kRows, hk, &k_full[j % 3]);
+                got_k = j + 1;
+                if (j >= 2 && !wait(&v_empty[j & 1], j / 2 - 1)) break;
+                mbar_arrive_expect_tx(&v_full[j & 1], TILE);
+                load_tile<HD>(ring_v + (j & 1) * TILE, &tmv, item.other + (int64_t)j * kRows, hk, &v_full[j & 1]);
+                got_v = j + 1;
+            }
+            if (got_v < steps) {                           // aborted: the copies in flight land first
+                wait.drain(&q_full, 0);
+                for (int i = max(0, got_k - 3); i < got_k; ++i) wait.drain(&k_full[i % 3], i / 3);
+                for (int i = max(0, got_v - 2); i < got_v; ++i) wait.drain(&v_full[i & 1], i / 2);
+            }
+        }
+    } else if (warp == 9 && steps > 0) {
+        const uint32_t idesc_s = idesc_bf16(kRows, false, p.scale < 0.0f), idesc_dp = idesc_bf16(kRows, false, false);
+        const uint32_t idesc_dq = idesc_bf16((p.dim + 15) & ~15, true, false);
+        const bool neighbours = item.other + item.other_len < p.tk;
+        auto k_tile = [&](int j) -> uint8_t* {
+            if (!wait(&k_full[j % 3], j / 3)) return nullptr;
+            uint8_t* b = ring_k + (j % 3) * TILE;
+            const int valid = item.other_len - j * kRows;
+            if (valid < kRows && neighbours) zero_tail<HD>(b, valid);
+            return b;
+        };
+        auto issue_s = [&](int j) -> bool {
+            const uint8_t* k = k_tile(j);
+            if (!k) return false;
+            if (lane == 0) {
+                mma_heads(tmem + 128 * (j & 1), smem_q, k, p.dim, idesc_s);
+                commit(&s_full[j & 1]);
+            }
+            return true;
+        };
+        // V's rows past the sequence reach only columns of dP that are masked: no need to zero them
+        auto issue_dp = [&](int j) -> bool {
+            if (!wait(&v_full[j & 1], j / 2)) return false;
+            if (lane == 0) {
+                mma_heads(tmem + 256, smem_do, ring_v + (j & 1) * TILE, p.dim, idesc_dp);
+                commit(&dp_full);
+                commit(&v_empty[j & 1]);
+            }
+            return true;
+        };
+        bool ok = wait(&q_full, 0) && issue_s(0) && issue_dp(0) && (steps < 2 || issue_s(1));
+        for (int j = 0; ok && j < steps; ++j) {
+            ok = wait(&ds_ready, j);
+            if (!ok) break;
+            fence_after();
+            if (j + 1 < steps) ok = issue_dp(j + 1);
+            if (!ok) break;
+            if (lane == 0) {
+                const uint32_t ds = tmem + 128 * (j & 1);
+                mma_rows(tmem + 384, ds, ds + 64, ring_k + (j % 3) * TILE, idesc_dq, j > 0);
+                commit(&k_empty[j % 3]);
+            }
+            if (j + 2 < steps) ok = issue_s(j + 2);
+        }
+        if (lane == 0) {
+            commit(&mma_done);
+            wait.drain(&mma_done, 0);
+        }
+        __syncwarp();
+    } else if (warp < 8 && item.valid) {
+        const int half = warp >> 2, r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const bool in = r < item.rows;
+        const int64_t tok = item.first + (in ? r : 0), at = (int64_t)item.head * p.tq + tok;
+        // delta = dout . out, half a row each
+        float d = 0.0f;
+        {
+            const bf16 *o = p.out.at(tok, item.head), *g = p.dout.at(tok, item.head);
+            const int mid = min(p.dim, 64);
+            for (int i = half ? mid : 0; i < (half ? p.dim : mid); i += 8) {
+                const uint4 a = *reinterpret_cast<const uint4*>(o + i), b = *reinterpret_cast<const uint4*>(g + i);
+                const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) d += bf16_lo(x[e]) * bf16_lo(y[e]) + bf16_hi(x[e]) * bf16_hi(y[e]);
+            }
+            part[half][r] = d;
+            asm volatile("bar.sync 1, 256;" ::: "memory");
+            d = part[0][r] + part[1][r];
+            if (in && half == 0) p.delta[at] = d;
+        }
+        const float lse = in ? p.lse[at] : 0.0f;
+        const float neg = lse == -INFINITY ? -INFINITY : -lse * kLog2e;      // a row that sees no key: P = 0
+        const int limit = p.causal ? min(item.other_len, max(0, r + item.diag + 1)) : item.other_len;
+        const int common = p.causal ? min(item.other_len, item.diag + 1) : item.other_len;
+        const float2 c2 = make_float2(p.c, p.c), neg2 = make_float2(neg, neg), delta2 = make_float2(-d, -d);
+        bool ok = true;
+        for (int j = 0; j < steps; ++j) {
+            const uint32_t ts = tmem + 128 * (j & 1) + 64 * half + lanes, tdp = tmem + 256 + 64 * half + lanes;
+            ok = wait(&s_full[j & 1], j >> 1);
+            if (!ok) break;
+            fence_after();
+            uint32_t s[2][32], g[2][32], w[32];
+            ld32(ts, s[0]);
+            ld32(ts + 32, s[1]);
+            ld_wait();
+            fence32(s[0]);
+            fence32(s[1]);
+#pragma unroll
+            for (int i = 0; i < 64; i += 2) {
+                float2 x = make_float2(__uint_as_float(s[i >> 5][i & 31]), __uint_as_float(s[i >> 5][(i & 31) + 1]));
+                x = __ffma2_rn(x, c2, neg2);
+                s[i >> 5][i & 31] = __float_as_uint(ex2(x.x));
+                s[i >> 5][(i & 31) + 1] = __float_as_uint(ex2(x.y));
+            }
+            ok = wait(&dp_full, j);
+            if (!ok) break;
+            fence_after();
+            ld32(tdp, g[0]);
+            ld32(tdp + 32, g[1]);
+            ld_wait();
+            fence32(g[0]);
+            fence32(g[1]);
+#pragma unroll
+            for (int i = 0; i < 64; i += 2) {
+                const float2 pr = make_float2(__uint_as_float(s[i >> 5][i & 31]), __uint_as_float(s[i >> 5][(i & 31) + 1]));
+                float2 x = make_float2(__uint_as_float(g[i >> 5][i & 31]), __uint_as_float(g[i >> 5][(i & 31) + 1]));
+                x = __fmul2_rn(pr, __fadd2_rn(x, delta2));
+                w[i >> 1] = pack_bf16(x.x, x.y);
+            }
+            if ((j + 1) * kRows > common) {                // masked pairs count for nothing, whatever they hold
+                const int lim = limit - j * kRows - 64 * half;
+#pragma unroll
+                for (int i = 0; i < 32; ++i) {
+                    if (2 * i >= lim) w[i] = 0u;
+                    else if (2 * i + 1 >= lim) w[i] &= 0xFFFFu;
+                }
+            }
+            st32(ts, w);
+            st_wait();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&ds_ready);
+        }
+        bf16* dst = p.dq.at(tok, item.head);
+        if (steps == 0) {
+            if (in && half == 0) store_zeros(dst, p.dim);
+        } else if (ok) {
+            ok = wait(&mma_done, 0);
+            fence_after();
+            if (ok)
+                for (int i = 64 * half; i < min(p.dim, 64 * half + 64); i += 32) {
+                    uint32_t v[32];
+                    ld32(tmem + 384 + i + lanes, v);
+                    ld_wait();
+                    fence32(v);
+                    if (in) store32(dst, i, p.dim, v, p.scale);
+                }
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        fence_after();
+        tmem_free_all(tmem);
+    }
+}
+
+// ---------------------------------------------------------------------------- backward, dK and dV
+// Warps 0-7: a key per thread, warps 0-3 the first 64 queries of a tile, warps 4-7 the last 64; warp 8: TMA; warp 9:
+// MMAs; warp 10: lse and delta of the queries.  A step is one query tile of one of the heads that read the
+// key head.  TMEM: S^T then P^T at 0, dP^T then dS^T at 128, dV at 256, dK at 384.  The tensor cores do dV of a
+// step and S of the next while the warps compute dS, and dK and the next dP while they compute P.
+constexpr int kDkvThreads = 352;
+template <int HD> struct Dkv {
+    static constexpr int TILE = kRows * HD * 2;
+    static constexpr int SMEM = 6 * TILE + 1024;           // K, V, two Q, two dO
+    static constexpr int PAD = HD == 128 ? SMEM : 120 * 1024;
+};
+
+template <int HD>
+__global__ void __launch_bounds__(kDkvThreads, 1)
+dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
+           const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmdo, const Params p) {
+    constexpr int TILE = Dkv<HD>::TILE;
+    extern __shared__ uint8_t raw[];
+    __shared__ uint64_t kv_full, q_full[2], q_empty[2], do_full[2], do_empty[2], st_full[2], st_empty[2], s_full, dp_full,
+        p_ready, ds_ready, mma_done;
+    __shared__ uint32_t tmem_slot, abort_flag;
+    __shared__ Item item;
+    __shared__ __align__(16) float stat[2][2][kRows];      // per slot: -lse log2(e), -delta
+    uint8_t* smem_k = align1024(raw);
+    uint8_t* smem_v = smem_k + TILE;
+    uint8_t* ring_q = smem_v + TILE;
+    uint8_t* ring_do = ring_q + 2 * TILE;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    pdl_launch_dependents();
+    if (threadIdx.x == 0) {
+        mbar_init(&kv_full, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&q_full[i], 1);
+            mbar_init(&q_empty[i], 1);
+            mbar_init(&do_full[i], 1);
+            mbar_init(&do_empty[i], 1);
+            mbar_init(&st_full[i], 1);
+            mbar_init(&st_empty[i], 8);
+        }
+        mbar_init(&s_full, 1);
+        mbar_init(&dp_full, 1);
+        mbar_init(&p_ready, 8);
+        mbar_init(&ds_ready, 8);
+        mbar_init(&mma_done, 1);
+        abort_flag = 0u;
+        asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    }
+    if (warp == 9) tmem_alloc_all(&tmem_slot);
+    pdl_wait();
+    if (warp == 8) find_item(p, false, kRows, p.kv_heads, &item);
+    fence_before();
+    __syncthreads();
+    fence_after();
+    const uint32_t tmem = tmem_slot;
+    const Wait wait{p.timeout_ns, &abort_flag, p.dev_status};
+    const int share = p.heads / p.kv_heads;
+    // With the causal mask key r of the tile is seen by the queries from r + diag on.
+    int first_tile = 0, tiles = 0, steps = 0;
+    if (item.valid) {
+        if (p.causal) first_tile = max(0, item.diag) / kRows;
+        tiles = max(0, (item.other_len + kRows - 1) / kRows - first_tile);
+        steps = tiles * share;
+    }
+    auto head_of = [&](int i) { return item.head * share + i / tiles; };
+    auto row_of = [&](int i) { return (first_tile + i % tiles) * kRows; };
+
+    if (warp == 8 && steps > 0) {
+        if (lane == 0) {
+            mbar_arrive_expect_tx(&kv_full, 2 * TILE);
+            load_tile<HD>(smem_k, &tmk, item.first, item.head, &kv_full);
+            load_tile<HD>(smem_v, &tmv, item.first, item.head, &kv_full);
+            int got_q = 0, got_do = 0;
+            for (int i = 0; i < steps; ++i) {
+                const int slot = i & 1;
+                if (i >= 2 && !wait(&q_empty[slot], i / 2 - 1)) break;
+                mbar_arrive_expect_tx(&q_full[slot], TILE);
+                load_tile<HD>(ring_q + slot * TILE, &tmq, item.other + row_of(i), head_of(i), &q_full[slot]);
+                got_q = i + 1;
+                if (i >= 2 && !wait(&do_empty[slot], i / 2 - 1)) break;
+                mbar_arrive_expect_tx(&do_full[slot], TILE);
+                load_tile<HD>(ring_do + slot * TILE, &tmdo, item.other + row_of(i), head_of(i), &do_full[slot]);
+                got_do = i + 1;
+            }
+            if (got_do < steps) {                          // aborted: the copies in flight land first
+                wait.drain(&kv_full, 0);
+                for (int i = max(0, got_q - 2); i < got_q; ++i) wait.drain(&q_full[i & 1], i / 2);
+                for (int i = max(0, got_do - 2); i < got_do; ++i) wait.drain(&do_full[i & 1], i / 2);
+            }
+        }
+    } else if (warp == 10 && steps > 0) {
+        for (int i = 0; i < steps; ++i) {
+            const int slot = i & 1;
+            if (i >= 2 && !wait(&st_empty[slot], i / 2 - 1)) break;
+            const int64_t at = (int64_t)head_of(i) * p.tq + item.other;
+            for (int r = lane; r < kRows; r += 32) {
+                const int q = row_of(i) + r;
+                const bool in = q < item.other_len;
+                const float lse = in ? p.lse[at + q] : -INFINITY;
+                stat[slot][0][r] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;   // such queries: P = 0
+                stat[slot][1][r] = in ? -p.delta[at + q] : 0.0f;
+            }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&st_full[slot]);
+        }
+    } else if (warp == 9 && steps > 0) {
+        const uint32_t idesc_s = idesc_bf16(kRows, false, p.scale < 0.0f), idesc_dp = idesc_bf16(kRows, false, false);
+        const uint32_t idesc_d = idesc_bf16((p.dim + 15) & ~15, true, false);
+        const bool neighbours = item.other + item.other_len < p.tq;
+        auto issue_s = [&](int i) -> bool {
+            const int slot = i & 1, valid = item.other_len - row_of(i);
+            if (!wait(&q_full[slot], i / 2)) return false;
+            uint8_t* q = ring_q + slot * TILE;
+            if (valid < kRows && neighbours) zero_tail<HD>(q, valid);
+            if (lane == 0) {
+                mma_heads(tmem, smem_k, q, p.dim, idesc_s);
+                commit(&s_full);
+            }
+            return true;
+        };
+        auto issue_dp = [&](int i) -> bool {
+            const int slot = i & 1, valid = item.other_len - row_of(i);
+            if (!wait(&do_full[slot], i / 2)) return false;
+            uint8_t* d = ring_do + slot * TILE;
+            if (valid < kRows && neighbours) zero_tail<HD>(d, valid);
+            if (lane == 0) {
+                mma_heads(tmem + 128, smem_v, d, p.dim, idesc_dp);
+                commit(&dp_full);
+            }
+            return true;
+        };
+        bool ok = wait(&kv_full, 0) && issue_s(0) && issue_dp(0);
+        for (int i = 0; ok && i < steps; ++i) {
+            const int slot = i & 1;
+            ok = wait(&p_ready, i);
+            if (!ok) break;
+            fence_after();
+            if (lane == 0) {
+                mma_rows(tmem + 256, tmem, tmem + 64, ring_do + slot * TILE, idesc_d, i > 0);
+                commit(&do_empty[slot]);
+            }
+            if (i + 1 < steps) ok = issue_s(i + 1);
+            ok = ok && wait(&ds_ready, i);
+            if (!ok) break;
+            fence_after();
+            if (lane == 0) {
+                mma_rows(tmem + 384, tmem + 128, tmem + 192, ring_q + slot * TILE, idesc_d, i > 0);
+                commit(&q_empty[slot]);
+            }
+            if (i + 1 < steps) ok = issue_dp(i + 1);
+        }
+        if (lane == 0) {
+            commit(&mma_done);
+            wait.drain(&mma_done, 0);
+        }
+        __syncwarp();
+    } else if (warp < 8 && item.valid) {
+        const int half = warp >> 2, r = (warp & 3) * 32 + lane;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + 64 * half + lanes, tdp = tmem + 128 + 64 * half + lanes;
+        const float2 c2 = make_float2(p.c, p.c);
+        bool ok = true;
+        for (int i = 0; i < steps; ++i) {
+            const int slot = i & 1;
+            ok = wait(&st_full[slot], i / 2) && wait(&s_full, i);
+            if (!ok) break;
+            fence_after();
+            uint32_t s[2][32], w[32];
+            ld32(ts, s[0]);
+            ld32(ts + 32, s[1]);
+            ld_wait();
+            fence32(s[0]);
+            fence32(s[1]);
+            const float2* lse2 = reinterpret_cast<const float2*>(&stat[slot][0][64 * half]);
+            const float2* del2 = reinterpret_cast<const float2*>(&stat[slot][1][64 * half]);
+#pragma unroll
+            for (int e = 0; e < 64; e += 2) {
+                float2 x = make_float2(__uint_as_float(s[e >> 5][e & 31]), __uint_as_float(s[e >> 5][(e & 31) + 1]));
+                x = __ffma2_rn(x, c2, lse2[e >> 1]);
+                s[e >> 5][e & 31] = __float_as_uint(ex2(x.x));
+                s[e >> 5][(e & 31) + 1] = __float_as_uint(ex2(x.y));
+            }
+            // masked pairs: queries before r + diag
+            const int from = p.causal ? r + item.diag - row_of(i) - 64 * half : 0;
+            if (p.causal && kRows - 1 + item.diag > row_of(i)) {
+#pragma unroll
+                for (int e = 0; e < 64; ++e)
+                    if (e < from) s[e >> 5][e & 31] = 0u;
+            }
+#pragma unroll
+            for (int e = 0; e < 64; e += 2)
+                w[e >> 1] = pack_bf16(__uint_as_float(s[e >> 5][e & 31]), __uint_as_float(s[e >> 5][(e & 31) + 1]));
+            st32(ts, w);
+            st_wait();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&p_ready);
+            ok = wait(&dp_full, i);
+            if (!ok) break;
+            fence_after();
+            uint32_t g[2][32];
+            ld32(tdp, g[0]);
+            ld32(tdp + 32, g[1]);
+            ld_wait();
+            fence32(g[0]);
+            fence32(g[1]);
+#pragma unroll
+            for (int e = 0; e < 64; e += 2) {
+                const float2 pr = make_float2(__uint_as_float(s[e >> 5][e & 31]), __uint_as_float(s[e >> 5][(e & 31) + 1]));
+                float2 x = make_float2(__uint_as_float(g[e >> 5][e & 31]), __uint_as_float(g[e >> 5][(e & 31) + 1]));
+                x = __fmul2_rn(pr, __fadd2_rn(x, del2[e >> 1]));
+                w[e >> 1] = pack_bf16(x.x, x.y);
+            }
+            st32(tdp, w);
+            st_wait();
+            fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                mbar_arrive(&ds_ready);
+                mbar_arrive(&st_empty[slot]);
+            }
+        }
+        const bool in = r < item.rows;
+        const int64_t tok = item.first + (in ? r : 0);
+        bf16* dst = half ? p.dk.at(tok, item.head) : p.dv.at(tok, item.head);
+        if (steps == 0) {
+            if (in) store_zeros(dst, p.dim);
+        } else if (ok) {
+            ok = wait(&mma_done, 0);
+            fence_after();
+            if (ok)
+                for (int i = 0; i < p.dim; i += 32) {
+                    uint32_t v[32];
+                    ld32(tmem + 256 + 128 * half + i + lanes, v);
+                    ld_wait();
+                    fence32(v);
+                    if (in) store32(dst, i, p.dim, v, half ? p.scale : 1.0f);
+                }
+        }
+    }
+    fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        fence_after();
+        tmem_free_all(tmem);
+    }
+}
+
+// ---------------------------------------------------------------------------- host
+PFN_cuTensorMapEncodeTiled_v12000 encode_fn() {
+    static PFN_cuTensorMapEncodeTiled_v12000 fn = nullptr;
+    static std::once_flag once;
+    std::call_once(once, [] {
+        cudaDriverEntryPointQueryResult q;
+        void* f = nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) ==
+                cudaSuccess && q == cudaDriverEntryPointSuccess)
+            fn = reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f);
+    });
+    return fn;
+}
+
+// [heads, tokens, dim] with boxes of 128 tokens x 64 elements.  The stride of an axis of one element
+// is never used; any valid one will do.
+bool make_map(CUtensorMap* m, const nvfp4_heads* h, int64_t tokens, int heads, int dim) {
+    auto fn = encode_fn();
+    if (!fn) return false;
+    if (tokens == 0) {
+        std::memset(m, 0, sizeof(*m));
+        return true;
+    }
+    cuuint64_t dims[3] = {(cuuint64_t)dim, (cuuint64_t)tokens, (cuuint64_t)heads};
+    cuuint64_t strides[2] = {(cuuint64_t)(tokens > 1 ? h->token_stride : dim) * 2,
+                             (cuuint64_t)(heads > 1 ? h->head_stride : dim) * 2};
+    cuuint32_t box[3] = {64, kRows, 1}, estr[3] = {1, 1, 1};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, h->data, dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
+              CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+              CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <typename Kernel, typename... Args>
+cudaError_t launch(Kernel kern, int smem, int threads, int64_t grid, cudaStream_t s, const Args&... args) {
+    // set on every call: a kernel's attribute belongs to the current device
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    return e == cudaSuccess ? launch_pdl(kern, dim3((unsigned)grid), dim3(threads), smem, s, args...) : e;
 }
 
 nvfp4_status check_shape(const nvfp4_attention_shape* s) {
@@ -186,7 +982,7 @@ nvfp4_status check_shape(const nvfp4_attention_shape* s) {
         return NVFP4_ERR_SHAPE;
     if (s->nseq < 1 || (!s->cu_q) != (!s->cu_k) || (!s->cu_q && s->nseq != 1) || !std::isfinite(s->scale))
         return NVFP4_ERR_INVALID_ARG;
-    if (s->nseq > (1 << 24)) return NVFP4_ERR_SHAPE;
+    if ((std::max(s->tq, s->tk) / kRows + s->nseq) * s->heads > INT_MAX) return NVFP4_ERR_SHAPE;   // the largest grid
     if ((reinterpret_cast<uintptr_t>(s->cu_q) | reinterpret_cast<uintptr_t>(s->cu_k)) % 4) return NVFP4_ERR_ALIGNMENT;
     return NVFP4_OK;
 }
@@ -197,6 +993,7 @@ nvfp4_status check_heads(const nvfp4_heads* h, int64_t tokens, int heads, int di
     if (tokens == 0) return NVFP4_OK;
     if (!h->data) return NVFP4_ERR_INVALID_ARG;
     if ((tokens > 1 && h->token_stride < dim) || (heads > 1 && h->head_stride < dim)) return NVFP4_ERR_SHAPE;
+    if (h->token_stride > (1ll << 38) || h->head_stride > (1ll << 38)) return NVFP4_ERR_SHAPE;
     if (!aligned16(h->data) || (tokens > 1 && h->token_stride % 8) || (heads > 1 && h->head_stride % 8))
         return NVFP4_ERR_ALIGNMENT;
     return NVFP4_OK;
@@ -214,10 +1011,17 @@ Params params_of(const nvfp4_attention_shape* s, uint32_t* dev_status) {
     p.causal = s->causal != 0;
     p.nseq = s->nseq;
     p.scale = s->scale;
+    p.c = std::max(std::fabs(s->scale) * kLog2e, 1e-30f);   // 0 would make -inf * 0 of a masked score
     p.cu_q = s->cu_q;
     p.cu_k = s->cu_k;
     p.dev_status = dev_status;
+    p.timeout_ns = wait_timeout_ns();
     return p;
+}
+
+// CTAs for tiles of `tile` rows: at most one part tile more per sequence.
+int64_t tiles_of(int64_t tokens, int nseq, int tile) {
+    return nseq == 1 ? (tokens + tile - 1) / tile : tokens / tile + nseq;
 }
 
 }  // namespace attn
@@ -239,16 +1043,16 @@ extern "C" nvfp4_status nvfp4_attention_forward(const nvfp4_attention_shape* sha
     if (!lse) return NVFP4_ERR_INVALID_ARG;
     if (reinterpret_cast<uintptr_t>(lse) % 4) return NVFP4_ERR_ALIGNMENT;
     Params p = params_of(shape, dev_status);
-    p.q = heads_of(q);
-    p.k = heads_of(k);
-    p.v = heads_of(v);
     p.out = heads_of(out);
     p.lse = lse;
+    CUtensorMap mq, mk, mv;
+    if (!make_map(&mq, q, p.tq, p.heads, p.dim) || !make_map(&mk, k, p.tk, p.kv_heads, p.dim) ||
+        !make_map(&mv, v, p.tk, p.kv_heads, p.dim))
+        return NVFP4_ERR_CUDA;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    cudaError_t e = cudaSuccess;
-    if (p.cu_q) e = launch_pdl(check_offsets_kernel, dim3(1), dim3(256), 0, s, p);
-    if (e == cudaSuccess)
-        e = launch_pdl(fwd_kernel, dim3((unsigned)((p.tq + 7) / 8), p.heads), dim3(256), 0, s, p);
+    const int64_t grid = tiles_of(p.tq, p.nseq, 2 * kRows) * p.heads;
+    const cudaError_t e = p.dim <= 64 ? launch(fwd_kernel<64>, Fwd<64>::SMEM, kFwdThreads, grid, s, mq, mk, mv, p)
+                                      : launch(fwd_kernel<128>, Fwd<128>::SMEM, kFwdThreads, grid, s, mq, mk, mv, p);
     return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
 
@@ -275,9 +1079,6 @@ extern "C" nvfp4_status nvfp4_attention_backward(const nvfp4_attention_shape* sh
         workspace_bytes < nvfp4_attention_backward_workspace_bytes(shape))
         return NVFP4_ERR_WORKSPACE;
     Params p = params_of(shape, dev_status);
-    p.q = heads_of(q);
-    p.k = heads_of(k);
-    p.v = heads_of(v);
     p.out = heads_of(out);
     p.dout = heads_of(dout);
     p.dq = heads_of(dq);
@@ -285,12 +1086,19 @@ extern "C" nvfp4_status nvfp4_attention_backward(const nvfp4_attention_shape* sh
     p.dv = heads_of(dv);
     p.lse = const_cast<float*>(lse);
     p.delta = static_cast<float*>(workspace);
+    CUtensorMap mq, mk, mv, mdo;
+    if (!make_map(&mq, q, p.tq, p.heads, p.dim) || !make_map(&mk, k, p.tk, p.kv_heads, p.dim) ||
+        !make_map(&mv, v, p.tk, p.kv_heads, p.dim) || !make_map(&mdo, dout, p.tq, p.heads, p.dim))
+        return NVFP4_ERR_CUDA;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const int64_t grid_q = tiles_of(p.tq, p.nseq, kRows) * p.heads, grid_k = tiles_of(p.tk, p.nseq, kRows) * p.kv_heads;
     cudaError_t e = cudaSuccess;
-    if (p.cu_q) e = launch_pdl(check_offsets_kernel, dim3(1), dim3(256), 0, s, p);
-    if (e == cudaSuccess && p.tq > 0)
-        e = launch_pdl(bwd_dq_kernel, dim3((unsigned)((p.tq + 7) / 8), p.heads), dim3(256), 0, s, p);
-    if (e == cudaSuccess && p.tk > 0)
-        e = launch_pdl(bwd_dkv_kernel, dim3((unsigned)((p.tk + 7) / 8), p.kv_heads), dim3(256), 0, s, p);
+    if (p.dim <= 64) {
+        if (p.tq > 0) e = launch(dq_kernel<64>, Dq<64>::PAD, kDqThreads, grid_q, s, mq, mk, mv, mdo, p);
+        if (e == cudaSuccess && p.tk > 0) e = launch(dkv_kernel<64>, Dkv<64>::PAD, kDkvThreads, grid_k, s, mq, mk, mv, mdo, p);
+    } else {
+        if (p.tq > 0) e = launch(dq_kernel<128>, Dq<128>::PAD, kDqThreads, grid_q, s, mq, mk, mv, mdo, p);
+        if (e == cudaSuccess && p.tk > 0) e = launch(dkv_kernel<128>, Dkv<128>::PAD, kDkvThreads, grid_k, s, mq, mk, mv, mdo, p);
+    }
     return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }

@@ -1,6 +1,7 @@
 """Attention on the GPU against its definition in 64 bits, head by head.
 
-Tolerances, with u = 2^-9 the rounding of a bf16 value.  out: the probabilities are rounded to bf16 (u of each, so u * sum p |v|
+Tolerances, with u = 2^-8 the unit roundoff of bf16 (8 bits of significand: between 1 and 2 its values lie 2^-7 apart,
+so rounding to the nearest moves a value by up to 2^-8 of it).  out: the probabilities are rounded to bf16 (u of each, so u * sum p |v|
 at most) and the result once more (u |out|); 2 u * sum(p |v|) + u |out| is allowed.  Gradients: P and dS are rounded once each (u of
 each term), delta comes from the rounded out (u * sum |dout| |out|, times P), and the result is rounded (u of it); the sums of the
 terms' magnitudes are computed beside the values and 2 u of them allowed (4 u for the terms with delta).  fp32 sums and the exponential
@@ -13,7 +14,7 @@ import torch
 
 pytestmark = pytest.mark.gpu
 BF16 = torch.bfloat16
-U = 2.0 ** -9
+U = 2.0 ** -8
 
 
 @pytest.fixture(scope="module")

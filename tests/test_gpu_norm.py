@@ -2,7 +2,7 @@
 
 Tolerances.  A float32 result is a short chain of operations on sums of n terms that are added in a tree
 of at most 32 sequential steps per level: its error is below 64 * 2^-24 of the largest term of the
-chain.  A bfloat16 result adds half a unit in the last place, 2^-9 of the value (2^-8 is allowed).
+chain.  A bfloat16 result adds half a unit in the last place, up to 2^-8 of the value.
 A column sum over R rows in float32 is within 2^-24 * (R / 64 + 64) of the sum of its terms' magnitudes."""
 import numpy as np
 import pytest
