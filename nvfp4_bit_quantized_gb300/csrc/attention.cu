@@ -145,12 +145,21 @@ __device__ __forceinline__ void find_item(const Params& p, bool rows_are_q, int 
     }
 }
 
+// Bounded waits, as mbar_wait_bounded, with the clock read only where a wait runs long: reading it after
+// the first failed try, as that one does, costs more than most waits here last.
 struct Wait {
     uint64_t timeout_ns;
     volatile uint32_t* abort;
     uint32_t* dev_status;
     __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
+        const uint32_t a = smem_addr(bar);
+        for (int i = 0; i < 64; ++i)
+            if (mbar_try_wait(a, parity & 1u)) return true;
         return mbar_wait_bounded(bar, parity & 1u, timeout_ns, abort, dev_status);
+    }
+    // whole warp; the same answer in all lanes, so that what follows is known not to diverge
+    __device__ __forceinline__ bool all(uint64_t* bar, uint32_t parity) const {
+        return __all_sync(~0u, (*this)(bar, parity));
     }
     // after an abort: still bounded, but not cut short by it
     __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) const {
@@ -178,21 +187,24 @@ __device__ __forceinline__ void zero_tail(uint8_t* tile, int valid) {
     __syncwarp();
 }
 
-// One lane.  D[128, n] (+)= A B^T over the head dimension: both tiles K-major.
-__device__ __forceinline__ void mma_heads(uint32_t d, const uint8_t* a, const uint8_t* b, int dim, uint32_t idesc) {
-    const uint32_t sa = smem_addr(a), sb = smem_addr(b);
-    for (int k = 0; k < dim; k += 16) {
-        const uint32_t off = (k >> 6) * kBoxBytes + (k & 63) * 2;
-        mma_ss(d, desc_k_major(sa + off), desc_k_major(sb + off), idesc, k != 0);
+// Whole warp.  D[128, 128] = A B^T over `ksteps` times 16 elements of the head: both tiles K-major, given by their
+// descriptors.
+template <int HD>
+__device__ __forceinline__ void mma_heads(uint32_t d, uint32_t a, uint32_t b, int ksteps, uint32_t idesc) {
+    const uint32_t lead = elect_one();
+#pragma unroll
+    for (int k = 0; k < HD / 16; ++k) {
+        const uint32_t off = (k >> 2) * (kBoxBytes >> 4) + (k & 3) * 2;
+        if (k < ksteps) mma_ss(d, a + off, b + off, idesc, k != 0, lead);
     }
 }
-// One lane.  D[128, dim] (+)= A B with A 128 x 128 bf16 in TMEM: K 0-63 at a0, 64-127 at a1; B a tile of 128 rows.
-__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a0, uint32_t a1, const uint8_t* b, uint32_t idesc,
-                                         bool accumulate) {
-    const uint32_t sb = smem_addr(b);
+// Whole warp.  D[128, n] (+)= A B with A 128 x 128 bf16 in TMEM: K 0-63 at a0, 64-127 at a1; B a tile of 128 rows.
+__device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a0, uint32_t a1, uint32_t b, uint32_t idesc,
+                                         uint32_t accumulate) {
+    const uint32_t lead = elect_one();
 #pragma unroll
     for (int k = 0; k < 8; ++k)
-        mma_ts(d, k < 4 ? a0 + k * 8 : a1 + (k - 4) * 8, desc_mn_major(sb + k * 2048), idesc, accumulate || k != 0);
+        mma_ts(d, k < 4 ? a0 + k * 8 : a1 + (k - 4) * 8, b + k * (2048 >> 4), idesc, k ? 1u : accumulate, lead);
 }
 
 // A row of `dim` bf16 values (a multiple of 8), 32 columns at a time: v * f, or zeros.
@@ -221,7 +233,10 @@ __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
 // columns) of tile t at 128 t, O of tile t at 256 + 128 t.  O is rescaled only when a row's maximum has
 // grown by more than 2^8 since it was last taken: P stays below 2^8 and the final division by the
 // sum cancels the choice.
-constexpr int kFwdThreads = 320;
+// A softmax thread holds a row's 128 scores at once: registers move from the third warpgroup to its two.
+constexpr int kFwdThreads = 384;
+constexpr int kFwdRegs = 168, kFwdRegsSoftmax = 208, kFwdRegsOther = 88;    // at launch, after setmaxnreg
+static_assert(2 * kFwdRegsSoftmax + kFwdRegsOther <= 3 * kFwdRegs, "register split within the launch's registers");
 template <int HD> struct Fwd {
     static constexpr int TILE = kRows * HD * 2;
     static constexpr int STAGES = HD == 128 ? 4 : 8;
@@ -239,7 +254,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
     __shared__ Item item;
     uint8_t* smem_q = align1024(raw);
     uint8_t* ring = smem_q + 2 * TILE;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
 
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
@@ -263,7 +278,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = tmem_slot;
+    const uint32_t tmem = uniform(tmem_slot);
     const Wait wait{p.timeout_ns, &abort_flag, p.dev_status};
     const int hk = item.head / (p.heads / p.kv_heads);
 
@@ -275,11 +290,16 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
             int keys = item.other_len;
             if (p.causal) keys = min(keys, max(0, kRows * t + rows[t] + item.diag));
             n[t] = rows[t] ? (keys + kRows - 1) / kRows : 0;
-            steps = max(steps, n[t]);
         }
     }
+    n[0] = uniform(n[0]);
+    n[1] = uniform(n[1]);
+    steps = max(n[0], n[1]);
 
-    if (warp == 8 && steps > 0) {
+    // inside the roles' own branches: code after a join is compiled for the smaller share
+    if (warp >= 8) {
+      asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kFwdRegsOther));
+      if (warp == 8 && steps > 0) {
         if (lane == 0) {
             mbar_arrive_expect_tx(&q_full, TILE * (rows[1] ? 2 : 1));
             load_tile<HD>(smem_q, &tmq, item.first, item.head, &q_full);
@@ -300,61 +320,57 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
         const uint32_t idesc_s = idesc_bf16(kRows, false, p.scale < 0.0f);
         const uint32_t idesc_o = idesc_bf16((p.dim + 15) & ~15, true, false);
         const bool neighbours = item.other + item.other_len < p.tk;
-        // the tile of step j (what = 0: K, 1: V) once it has arrived, its foreign rows zeroed
-        auto tile = [&](int j, int what) -> uint8_t* {
-            const int i = 2 * j + what, slot = i % ST;
-            if (!wait(&full[slot], i / ST)) return nullptr;
-            uint8_t* b = ring + slot * TILE;
-            const int valid = item.other_len - j * kRows;
-            if (valid < kRows && neighbours) zero_tail<HD>(b, valid);
-            return b;
+        const int ksteps = (p.dim + 15) / 16;
+        const uint32_t desc_q = uniform(desc_k_major(smem_addr(smem_q)));
+        const uint32_t desc_k = uniform(desc_k_major(smem_addr(ring))), desc_v = uniform(desc_mn_major(smem_addr(ring)));
+        const int len = uniform(item.other_len);
+        // waits for tile i (K of step 0, V of step 0, K of step 1, ...) and zeroes its foreign rows
+        auto tile = [&](int i) {
+            const int valid = len - (i >> 1) * kRows;
+            if (!wait.all(&full[i % ST], i / ST)) return false;
+            if (valid < kRows && neighbours) zero_tail<HD>(ring + (i % ST) * TILE, valid);
+            return true;
         };
-        bool ok = wait(&q_full, 0);
-        const uint8_t* k = ok ? tile(0, 0) : nullptr;
-        ok = ok && k;
-        if (ok && lane == 0) {
+        bool ok = wait.all(&q_full, 0) && tile(0);
+        if (ok) {
+#pragma unroll
             for (int t = 0; t < 2; ++t)
                 if (n[t] > 0) {
-                    mma_heads(tmem + 128 * t, smem_q + t * TILE, k, p.dim, idesc_s);
-                    commit(&s_full[t]);
+                    mma_heads<HD>(tmem + 128 * t, desc_q + t * (TILE >> 4), desc_k, ksteps, idesc_s);
+                    commit(&s_full[t], elect_one());
                 }
-            commit(&empty[0]);
+            commit(&empty[0], elect_one());
         }
         for (int j = 0; ok && j < steps; ++j) {
-            const uint8_t* v = tile(j, 1);
-            ok = v != nullptr;
-            const bool more = j + 1 < steps;
-            k = nullptr;
-            for (int t = 0; ok && t < 2; ++t) {
-                if (j >= n[t]) continue;
-                ok = wait(&p_ready[t], j);
+            const int slot_v = (2 * j + 1) % ST, slot_k = (2 * j + 2) % ST;
+            ok = tile(2 * j + 1);
+            bool got_k = false;
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                if (!ok || j >= n[t]) continue;
+                ok = wait.all(&p_ready[t], j);
                 if (!ok) break;
                 fence_after();
                 const uint32_t sp = tmem + 128 * t;
-                if (lane == 0) {
-                    mma_rows(tmem + 256 + 128 * t, sp, sp + 32, v, idesc_o, j > 0);
-                    if (j + 1 == n[t]) commit(&o_full[t]);
-                }
+                mma_rows(tmem + 256 + 128 * t, sp, sp + 32, desc_v + slot_v * (TILE >> 4), idesc_o, j > 0);
+                if (j + 1 == n[t]) commit(&o_full[t], elect_one());
                 if (j + 1 < n[t]) {
-                    if (!k) k = tile(j + 1, 0);
-                    ok = k != nullptr;
-                    if (ok && lane == 0) {
-                        mma_heads(sp, smem_q + t * TILE, k, p.dim, idesc_s);
-                        commit(&s_full[t]);
-                    }
+                    if (!got_k) got_k = ok = tile(2 * j + 2);
+                    if (!ok) break;
+                    mma_heads<HD>(sp, desc_q + t * (TILE >> 4), desc_k + slot_k * (TILE >> 4), ksteps, idesc_s);
+                    commit(&s_full[t], elect_one());
                 }
             }
-            if (ok && lane == 0) {
-                commit(&empty[(2 * j + 1) % ST]);
-                if (more) commit(&empty[(2 * j + 2) % ST]);
+            if (ok) {
+                commit(&empty[slot_v], elect_one());
+                if (j + 1 < steps) commit(&empty[slot_k], elect_one());
             }
         }
-        if (lane == 0) {
-            commit(&mma_done);
-            wait.drain(&mma_done, 0);
-        }
-        __syncwarp();
-    } else if (warp < 8) {
+        commit(&mma_done, elect_one());
+        wait.drain(&mma_done, 0);
+      }
+    } else {
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kFwdRegsSoftmax));
         const int t = warp >> 2, r = (warp & 3) * 32 + lane, row = kRows * t + r;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + 128 * t + lanes, to = tmem + 256 + 128 * t + lanes;
@@ -484,7 +500,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
     uint8_t* smem_do = smem_q + TILE;
     uint8_t* ring_k = smem_do + TILE;
     uint8_t* ring_v = ring_k + 3 * TILE;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
 
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
@@ -510,7 +526,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = tmem_slot;
+    const uint32_t tmem = uniform(tmem_slot);
     const Wait wait{p.timeout_ns, &abort_flag, p.dev_status};
     const int hk = item.head / (p.heads / p.kv_heads);
     int steps = 0;
@@ -518,6 +534,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         const int keys = p.causal ? min(item.other_len, max(0, item.rows + item.diag)) : item.other_len;
         steps = (keys + kRows - 1) / kRows;
     }
+    steps = uniform(steps);
 
     if (warp == 8 && steps > 0) {
         if (lane == 0) {
@@ -545,51 +562,41 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         const uint32_t idesc_s = idesc_bf16(kRows, false, p.scale < 0.0f), idesc_dp = idesc_bf16(kRows, false, false);
         const uint32_t idesc_dq = idesc_bf16((p.dim + 15) & ~15, true, false);
         const bool neighbours = item.other + item.other_len < p.tk;
-        auto k_tile = [&](int j) -> uint8_t* {
-            if (!wait(&k_full[j % 3], j / 3)) return nullptr;
-            uint8_t* b = ring_k + (j % 3) * TILE;
-            const int valid = item.other_len - j * kRows;
-            if (valid < kRows && neighbours) zero_tail<HD>(b, valid);
-            return b;
-        };
-        auto issue_s = [&](int j) -> bool {
-            const uint8_t* k = k_tile(j);
-            if (!k) return false;
-            if (lane == 0) {
-                mma_heads(tmem + 128 * (j & 1), smem_q, k, p.dim, idesc_s);
-                commit(&s_full[j & 1]);
-            }
+        const int ksteps = (p.dim + 15) / 16;
+        const uint32_t desc_q = uniform(desc_k_major(smem_addr(smem_q))), desc_do = desc_q + (TILE >> 4);
+        const uint32_t desc_k = uniform(desc_k_major(smem_addr(ring_k))), desc_v = uniform(desc_k_major(smem_addr(ring_v)));
+        const uint32_t desc_kt = uniform(desc_mn_major(smem_addr(ring_k)));
+        const int len = uniform(item.other_len);
+        auto issue_s = [&](int j) {
+            const int slot = j % 3, valid = len - j * kRows;
+            if (!wait.all(&k_full[slot], j / 3)) return false;
+            if (valid < kRows && neighbours) zero_tail<HD>(ring_k + slot * TILE, valid);
+            mma_heads<HD>(tmem + 128 * (j & 1), desc_q, desc_k + slot * (TILE >> 4), ksteps, idesc_s);
+            commit(&s_full[j & 1], elect_one());
             return true;
         };
         // V's rows past the sequence reach only columns of dP that are masked: no need to zero them
-        auto issue_dp = [&](int j) -> bool {
-            if (!wait(&v_full[j & 1], j / 2)) return false;
-            if (lane == 0) {
-                mma_heads(tmem + 256, smem_do, ring_v + (j & 1) * TILE, p.dim, idesc_dp);
-                commit(&dp_full);
-                commit(&v_empty[j & 1]);
-            }
+        auto issue_dp = [&](int j) {
+            if (!wait.all(&v_full[j & 1], j / 2)) return false;
+            mma_heads<HD>(tmem + 256, desc_do, desc_v + (j & 1) * (TILE >> 4), ksteps, idesc_dp);
+            commit(&dp_full, elect_one());
+            commit(&v_empty[j & 1], elect_one());
             return true;
         };
-        bool ok = wait(&q_full, 0) && issue_s(0) && issue_dp(0) && (steps < 2 || issue_s(1));
+        bool ok = wait.all(&q_full, 0) && issue_s(0) && issue_dp(0) && (steps < 2 || issue_s(1));
         for (int j = 0; ok && j < steps; ++j) {
-            ok = wait(&ds_ready, j);
+            ok = wait.all(&ds_ready, j);
             if (!ok) break;
             fence_after();
             if (j + 1 < steps) ok = issue_dp(j + 1);
             if (!ok) break;
-            if (lane == 0) {
-                const uint32_t ds = tmem + 128 * (j & 1);
-                mma_rows(tmem + 384, ds, ds + 64, ring_k + (j % 3) * TILE, idesc_dq, j > 0);
-                commit(&k_empty[j % 3]);
-            }
+            const uint32_t ds = tmem + 128 * (j & 1);
+            mma_rows(tmem + 384, ds, ds + 64, desc_kt + (j % 3) * (TILE >> 4), idesc_dq, j > 0);
+            commit(&k_empty[j % 3], elect_one());
             if (j + 2 < steps) ok = issue_s(j + 2);
         }
-        if (lane == 0) {
-            commit(&mma_done);
-            wait.drain(&mma_done, 0);
-        }
-        __syncwarp();
+        commit(&mma_done, elect_one());
+        wait.drain(&mma_done, 0);
     } else if (warp < 8 && item.valid) {
         const int half = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -715,7 +722,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
     uint8_t* smem_v = smem_k + TILE;
     uint8_t* ring_q = smem_v + TILE;
     uint8_t* ring_do = ring_q + 2 * TILE;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
 
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
@@ -742,7 +749,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = tmem_slot;
+    const uint32_t tmem = uniform(tmem_slot);
     const Wait wait{p.timeout_ns, &abort_flag, p.dev_status};
     const int share = p.heads / p.kv_heads;
     // With the causal mask key r of the tile is seen by the queries from r + diag on.
@@ -752,6 +759,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
         tiles = max(0, (item.other_len + kRows - 1) / kRows - first_tile);
         steps = tiles * share;
     }
+    steps = uniform(steps);
     auto head_of = [&](int i) { return item.head * share + i / tiles; };
     auto row_of = [&](int i) { return (first_tile + i % tiles) * kRows; };
 
@@ -797,53 +805,44 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
         const uint32_t idesc_s = idesc_bf16(kRows, false, p.scale < 0.0f), idesc_dp = idesc_bf16(kRows, false, false);
         const uint32_t idesc_d = idesc_bf16((p.dim + 15) & ~15, true, false);
         const bool neighbours = item.other + item.other_len < p.tq;
-        auto issue_s = [&](int i) -> bool {
+        const int ksteps = (p.dim + 15) / 16;
+        const uint32_t desc_k = uniform(desc_k_major(smem_addr(smem_k))), desc_v = desc_k + (TILE >> 4);
+        const uint32_t desc_q = uniform(desc_k_major(smem_addr(ring_q))), desc_do = desc_q + 2 * (TILE >> 4);
+        const uint32_t desc_qt = uniform(desc_mn_major(smem_addr(ring_q))), desc_dot = desc_qt + 2 * (TILE >> 4);
+        auto issue_s = [&](int i) {
             const int slot = i & 1, valid = item.other_len - row_of(i);
-            if (!wait(&q_full[slot], i / 2)) return false;
-            uint8_t* q = ring_q + slot * TILE;
-            if (valid < kRows && neighbours) zero_tail<HD>(q, valid);
-            if (lane == 0) {
-                mma_heads(tmem, smem_k, q, p.dim, idesc_s);
-                commit(&s_full);
-            }
+            if (!wait.all(&q_full[slot], i / 2)) return false;
+            if (valid < kRows && neighbours) zero_tail<HD>(ring_q + slot * TILE, valid);
+            mma_heads<HD>(tmem, desc_k, desc_q + slot * (TILE >> 4), ksteps, idesc_s);
+            commit(&s_full, elect_one());
             return true;
         };
-        auto issue_dp = [&](int i) -> bool {
+        auto issue_dp = [&](int i) {
             const int slot = i & 1, valid = item.other_len - row_of(i);
-            if (!wait(&do_full[slot], i / 2)) return false;
-            uint8_t* d = ring_do + slot * TILE;
-            if (valid < kRows && neighbours) zero_tail<HD>(d, valid);
-            if (lane == 0) {
-                mma_heads(tmem + 128, smem_v, d, p.dim, idesc_dp);
-                commit(&dp_full);
-            }
+            if (!wait.all(&do_full[slot], i / 2)) return false;
+            if (valid < kRows && neighbours) zero_tail<HD>(ring_do + slot * TILE, valid);
+            mma_heads<HD>(tmem + 128, desc_v, desc_do + slot * (TILE >> 4), ksteps, idesc_dp);
+            commit(&dp_full, elect_one());
             return true;
         };
-        bool ok = wait(&kv_full, 0) && issue_s(0) && issue_dp(0);
+        bool ok = wait.all(&kv_full, 0) && issue_s(0) && issue_dp(0);
         for (int i = 0; ok && i < steps; ++i) {
             const int slot = i & 1;
-            ok = wait(&p_ready, i);
+            ok = wait.all(&p_ready, i);
             if (!ok) break;
             fence_after();
-            if (lane == 0) {
-                mma_rows(tmem + 256, tmem, tmem + 64, ring_do + slot * TILE, idesc_d, i > 0);
-                commit(&do_empty[slot]);
-            }
+            mma_rows(tmem + 256, tmem, tmem + 64, desc_dot + slot * (TILE >> 4), idesc_d, i > 0);
+            commit(&do_empty[slot], elect_one());
             if (i + 1 < steps) ok = issue_s(i + 1);
-            ok = ok && wait(&ds_ready, i);
+            ok = ok && wait.all(&ds_ready, i);
             if (!ok) break;
             fence_after();
-            if (lane == 0) {
-                mma_rows(tmem + 384, tmem + 128, tmem + 192, ring_q + slot * TILE, idesc_d, i > 0);
-                commit(&q_empty[slot]);
-            }
+            mma_rows(tmem + 384, tmem + 128, tmem + 192, desc_qt + slot * (TILE >> 4), idesc_d, i > 0);
+            commit(&q_empty[slot], elect_one());
             if (i + 1 < steps) ok = issue_dp(i + 1);
         }
-        if (lane == 0) {
-            commit(&mma_done);
-            wait.drain(&mma_done, 0);
-        }
-        __syncwarp();
+        commit(&mma_done, elect_one());
+        wait.drain(&mma_done, 0);
     } else if (warp < 8 && item.valid) {
         const int half = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -975,6 +974,18 @@ cudaError_t launch(Kernel kern, int smem, int threads, int64_t grid, cudaStream_
     return e == cudaSuccess ? launch_pdl(kern, dim3((unsigned)grid), dim3(threads), smem, s, args...) : e;
 }
 
+// The forward kernel's setmaxnreg.inc completes only if the launch holds the split's total: a build
+// that allocated fewer registers a thread is never launched.
+template <int HD> bool fwd_registers_fit() {
+    static std::once_flag once;
+    static bool fit = false;
+    std::call_once(once, [] {
+        cudaFuncAttributes fa;
+        fit = cudaFuncGetAttributes(&fa, fwd_kernel<HD>) == cudaSuccess && fa.numRegs >= kFwdRegs;
+    });
+    return fit;
+}
+
 nvfp4_status check_shape(const nvfp4_attention_shape* s) {
     if (!s) return NVFP4_ERR_INVALID_ARG;
     if (s->tq < 0 || s->tk < 0 || s->tq > (1ll << 30) || s->tk > (1ll << 30) || s->heads < 1 || s->kv_heads < 1 ||
@@ -1051,6 +1062,7 @@ extern "C" nvfp4_status nvfp4_attention_forward(const nvfp4_attention_shape* sha
         return NVFP4_ERR_CUDA;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
     const int64_t grid = tiles_of(p.tq, p.nseq, 2 * kRows) * p.heads;
+    if (!(p.dim <= 64 ? fwd_registers_fit<64>() : fwd_registers_fit<128>())) return NVFP4_ERR_CUDA;
     const cudaError_t e = p.dim <= 64 ? launch(fwd_kernel<64>, Fwd<64>::SMEM, kFwdThreads, grid, s, mq, mk, mv, p)
                                       : launch(fwd_kernel<128>, Fwd<128>::SMEM, kFwdThreads, grid, s, mq, mk, mv, p);
     return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;

@@ -23,37 +23,57 @@ __device__ __forceinline__ void fence_proxy_async_smem() { asm volatile("fence.p
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 
-// Descriptor of a box used K-major: rows are M or N, the 64 elements of a row K.  8-row groups lie
-// 1024 bytes apart; a K step of 16 elements begins 32 bytes further on.
-__device__ __forceinline__ uint64_t desc_k_major(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)1 << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
-}
-// Descriptor of boxes used MN-major: rows are K, the 64 elements of a row N.  Eight rows of K make
-// 1024 bytes (the stride to the next eight); the next 64 elements of N are the next box.  A K step
-// of 16 rows begins 2048 bytes further on.
-__device__ __forceinline__ uint64_t desc_mn_major(uint32_t saddr) {
-    return (uint64_t)((saddr & 0x3FFFFu) >> 4) | ((uint64_t)(kBoxBytes >> 4) << 16) | ((uint64_t)(1024 >> 4) << 32) |
-           ((uint64_t)1 << 46) | ((uint64_t)2 << 61);
+// Shared-memory matrix descriptors: the low word holds the address and the leading stride, both in
+// units of 16 bytes; the high word the other stride (1024 bytes between groups of eight rows), the
+// version and the 128-byte swizzle, the same for all.  Steps along K add to the low word.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+// A box used K-major: rows are M or N, the 64 elements of a row K.  A K step of 16 elements is 32
+// bytes, 64 elements the next box.
+__device__ __forceinline__ uint32_t desc_k_major(uint32_t saddr) { return ((saddr & 0x3FFFFu) >> 4) | (1u << 16); }
+// Boxes used MN-major: rows are K, the 64 elements of a row N, the next 64 in the next box (the
+// leading stride).  A K step of 16 rows is 2048 bytes.
+__device__ __forceinline__ uint32_t desc_mn_major(uint32_t saddr) {
+    return ((saddr & 0x3FFFFu) >> 4) | ((uint32_t)(kBoxBytes >> 4) << 16);
 }
 // Instruction descriptor, kind::f16: fp32 accumulator, bf16 A and B, M = 128.
 __host__ __device__ constexpr uint32_t idesc_bf16(int n, bool b_mn_major, bool negate_a) {
     return (1u << 4) | (1u << 7) | (1u << 10) | ((negate_a ? 1u : 0u) << 13) | ((b_mn_major ? 1u : 0u) << 16) |
            ((uint32_t)(n >> 3) << 17) | ((uint32_t)(kRows >> 4) << 24);
 }
-__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
-                 :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+// One lane of a converged warp.
+__device__ __forceinline__ uint32_t elect_one() {
+    uint32_t r;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(r));
+    return r;
 }
-__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                 :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(accumulate) : "memory");
+// A value that is the same in all lanes, in a form that the compiler sees to be.
+__device__ __forceinline__ uint32_t uniform(uint32_t v) { return __shfl_sync(~0u, v, 0); }
+__device__ __forceinline__ int uniform(int v) { return __shfl_sync(~0u, v, 0); }
+
+// The MMAs and commits below are executed by a whole warp and issued by the lane with `lead` set
+// (elect_one).  How fast one warp can issue them bounds a kernel of small MMAs: 128 x 128 x 16 keeps
+// the tensor cores busy for 64 cycles, and issuing it took 62 .. 75 with `lead` from a comparison of the
+// lane number and operands that were not known to be uniform, 40 with both.
+__device__ __forceinline__ void mma_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate,
+                                       uint32_t lead) {
+    asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b64 da, db;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+                 "mov.b64 da, {%1, %6};\n\tmov.b64 db, {%2, %6};\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}"
+                 :: "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(lead), "r"(kDescHigh) : "memory");
 }
-__device__ __forceinline__ void commit(uint64_t* bar) {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
-                 :: "r"(smem_addr(bar)) : "memory");
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc, uint32_t accumulate,
+                                       uint32_t lead) {
+    asm volatile("{\n\t.reg .pred p, e;\n\t.reg .b64 db;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\tsetp.ne.b32 e, %5, 0;\n\t"
+                 "mov.b64 db, {%2, %6};\n\t"
+                 "@e tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}"
+                 :: "r"(d), "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "r"(lead), "r"(kDescHigh) : "memory");
+}
+__device__ __forceinline__ void commit(uint64_t* bar, uint32_t lead) {
+    asm volatile("{\n\t.reg .pred e;\n\tsetp.ne.b32 e, %1, 0;\n\t"
+                 "@e tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+                 :: "r"(smem_addr(bar)), "r"(lead) : "memory");
 }
 // Whole-warp: all 512 TMEM columns of the SM; *slot receives the address.
 __device__ __forceinline__ void tmem_alloc_all(uint32_t* slot) {
