@@ -145,17 +145,28 @@ __device__ __forceinline__ void find_item(const Params& p, bool rows_are_q, int 
     }
 }
 
-// Bounded waits, as mbar_wait_bounded, with the clock read only where a wait runs long: reading it after
-// the first failed try, as that one does, costs more than most waits here last.
+// Bounded waits, as mbar_wait_bounded, but timed by the SM's own clock: reading the global timer, as that one
+// does after the first failed try, takes longer than most waits here last.  Two cycles a nanosecond:
+// at the highest clock, 2.07 GHz, the limit, at lower clocks a multiple of it.
 struct Wait {
     uint64_t timeout_ns;
     volatile uint32_t* abort;
     uint32_t* dev_status;
     __device__ __forceinline__ bool operator()(uint64_t* bar, uint32_t parity) const {
         const uint32_t a = smem_addr(bar);
-        for (int i = 0; i < 64; ++i)
+        if (mbar_try_wait(a, parity & 1u)) return true;
+        const int64_t t0 = clock64();
+        for (uint32_t i = 1;; ++i) {
             if (mbar_try_wait(a, parity & 1u)) return true;
-        return mbar_wait_bounded(bar, parity & 1u, timeout_ns, abort, dev_status);
+            if ((i & 63u) == 0) {
+                if (*abort) return false;
+                if ((uint64_t)(clock64() - t0) > 2 * timeout_ns) {
+                    set_status(dev_status, NVFP4_ERR_TIMEOUT);
+                    *abort = 1u;
+                    return false;
+                }
+            }
+        }
     }
     // whole warp; the same answer in all lanes, so that what follows is known not to diverge
     __device__ __forceinline__ bool all(uint64_t* bar, uint32_t parity) const {
@@ -164,6 +175,22 @@ struct Wait {
     // after an abort: still bounded, but not cut short by it
     __device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) const {
         mbar_wait_bounded(bar, parity & 1u, timeout_ns, nullptr, dev_status);
+    }
+};
+
+// The two MMA warps issue their groups of MMAs in turns, first (w = 0) and second (w = 1) of each round: the tensor
+// cores then work off one group after the other.  Groups issued at will run interleaved and end
+// together, and nothing is left to run while the softmax warps work on what both produced.
+struct Turns {
+    uint64_t* bar;                                         // two barriers, one arrival each
+    Wait wait;
+    int w;
+    __device__ __forceinline__ bool take(int round) const {
+        return w ? wait.all(&bar[1], round) : round == 0 || wait.all(&bar[0], round - 1);
+    }
+    __device__ __forceinline__ void pass() const {
+        if (elect_one()) mbar_arrive(&bar[w ^ 1]);
+        __syncwarp();
     }
 };
 
@@ -228,8 +255,9 @@ __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
 }
 
 // ---------------------------------------------------------------------------- forward
-// Warps 0-3 and 4-7: the softmax of tile 0 and tile 1, a row per thread; warp 8: TMA; warp 9: MMAs.  While one
-// tile's softmax runs, the tensor cores work on the other tile.  TMEM: S (then P, bf16, in its first 64
+// Warps 0-3 and 4-7: the softmax of tile 0 and tile 1, a row per thread; warp 8: TMA; warps 9 and 10: the MMAs
+// of tile 0 and of tile 1 (one warp cannot issue MMAs of 64 cycles fast enough beside the softmax
+// warps).  While one tile's softmax runs, the tensor cores work on the other tile.  TMEM: S (then P, bf16, in its first 64
 // columns) of tile t at 128 t, O of tile t at 256 + 128 t.  O is rescaled only when a row's maximum has
 // grown by more than 2^8 since it was last taken: P stays below 2^8 and the final division by the
 // sum cancels the choice.
@@ -249,7 +277,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
            const __grid_constant__ CUtensorMap tmv, const Params p) {
     constexpr int TILE = Fwd<HD>::TILE, ST = Fwd<HD>::STAGES;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t q_full, full[ST], empty[ST], s_full[2], p_ready[2], o_full[2], mma_done;
+    __shared__ uint64_t q_full, full[ST], empty[ST], s_full[2], p_ready[2], o_full[2], turn[2], mma_done[2];
     __shared__ uint32_t tmem_slot, abort_flag;
     __shared__ Item item;
     uint8_t* smem_q = align1024(raw);
@@ -261,14 +289,15 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
         mbar_init(&q_full, 1);
         for (int i = 0; i < ST; ++i) {
             mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+            mbar_init(&empty[i], 2);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(&s_full[t], 1);
             mbar_init(&p_ready[t], 4);
             mbar_init(&o_full[t], 1);
+            mbar_init(&turn[t], 1);
+            mbar_init(&mma_done[t], 1);
         }
-        mbar_init(&mma_done, 1);
         abort_flag = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -316,58 +345,53 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
                 for (int j = max(0, i - ST); j < i; ++j) wait.drain(&full[j % ST], j / ST);
             }
         }
-    } else if (warp == 9 && steps > 0) {
+    } else if ((warp == 9 || warp == 10) && steps > 0) {
+        const int t = warp - 9, nt = t ? n[1] : n[0];
         const uint32_t idesc_s = idesc_bf16(kRows, false, p.scale < 0.0f);
         const uint32_t idesc_o = idesc_bf16((p.dim + 15) & ~15, true, false);
         const bool neighbours = item.other + item.other_len < p.tk;
-        const int ksteps = (p.dim + 15) / 16;
-        const uint32_t desc_q = uniform(desc_k_major(smem_addr(smem_q)));
+        const int ksteps = (p.dim + 15) / 16, len = uniform(item.other_len);
+        const uint32_t desc_q = uniform(desc_k_major(smem_addr(smem_q + t * TILE)));
         const uint32_t desc_k = uniform(desc_k_major(smem_addr(ring))), desc_v = uniform(desc_mn_major(smem_addr(ring)));
-        const int len = uniform(item.other_len);
-        // waits for tile i (K of step 0, V of step 0, K of step 1, ...) and zeroes its foreign rows
+        const uint32_t ts = uniform(tmem + 128 * t), to = ts + 256;
+        // waits for tile i (K of step 0, V of step 0, K of step 1, ...); both warps zero its foreign rows
         auto tile = [&](int i) {
             const int valid = len - (i >> 1) * kRows;
             if (!wait.all(&full[i % ST], i / ST)) return false;
             if (valid < kRows && neighbours) zero_tail<HD>(ring + (i % ST) * TILE, valid);
             return true;
         };
-        bool ok = wait.all(&q_full, 0) && tile(0);
+        const Turns turns{turn, wait, t};
+        bool ok = wait.all(&q_full, 0) && tile(0) && turns.take(0);
         if (ok) {
-#pragma unroll
-            for (int t = 0; t < 2; ++t)
-                if (n[t] > 0) {
-                    mma_heads<HD>(tmem + 128 * t, desc_q + t * (TILE >> 4), desc_k, ksteps, idesc_s);
-                    commit(&s_full[t], elect_one());
-                }
+            if (nt > 0) {
+                mma_heads<HD>(ts, desc_q, desc_k, ksteps, idesc_s);
+                commit(&s_full[t], elect_one());
+            }
+            turns.pass();
             commit(&empty[0], elect_one());
         }
         for (int j = 0; ok && j < steps; ++j) {
             const int slot_v = (2 * j + 1) % ST, slot_k = (2 * j + 2) % ST;
-            ok = tile(2 * j + 1);
-            bool got_k = false;
-#pragma unroll
-            for (int t = 0; t < 2; ++t) {
-                if (!ok || j >= n[t]) continue;
-                ok = wait.all(&p_ready[t], j);
-                if (!ok) break;
+            // what comes last is waited for last: a wait costs time even where it is over
+            ok = tile(2 * j + 1) && (j + 1 >= steps || tile(2 * j + 2)) && turns.take(j + 1) &&
+                 (j >= nt || wait.all(&p_ready[t], j));
+            if (!ok) break;
+            if (j < nt) {
                 fence_after();
-                const uint32_t sp = tmem + 128 * t;
-                mma_rows(tmem + 256 + 128 * t, sp, sp + 32, desc_v + slot_v * (TILE >> 4), idesc_o, j > 0);
-                if (j + 1 == n[t]) commit(&o_full[t], elect_one());
-                if (j + 1 < n[t]) {
-                    if (!got_k) got_k = ok = tile(2 * j + 2);
-                    if (!ok) break;
-                    mma_heads<HD>(sp, desc_q + t * (TILE >> 4), desc_k + slot_k * (TILE >> 4), ksteps, idesc_s);
-                    commit(&s_full[t], elect_one());
-                }
+                mma_rows(to, ts, ts + 32, desc_v + slot_v * (TILE >> 4), idesc_o, j > 0);
+                if (j + 1 == nt) commit(&o_full[t], elect_one());
             }
-            if (ok) {
-                commit(&empty[slot_v], elect_one());
-                if (j + 1 < steps) commit(&empty[slot_k], elect_one());
+            if (j + 1 < nt) {
+                mma_heads<HD>(ts, desc_q, desc_k + slot_k * (TILE >> 4), ksteps, idesc_s);
+                commit(&s_full[t], elect_one());
             }
+            turns.pass();
+            commit(&empty[slot_v], elect_one());
+            if (j + 1 < steps) commit(&empty[slot_k], elect_one());
         }
-        commit(&mma_done, elect_one());
-        wait.drain(&mma_done, 0);
+        commit(&mma_done[t], elect_one());
+        wait.drain(&mma_done[t], 0);
       }
     } else {
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kFwdRegsSoftmax));
@@ -476,10 +500,10 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
 
 // ---------------------------------------------------------------------------- backward, dQ
 // Warps 0-7: a row per thread, warps 0-3 the first 64 keys of a tile, warps 4-7 the last 64; warp 8: TMA; warp 9:
-// MMAs.  TMEM: S of even and odd steps at 0 and 128 (dS takes S's place, in the columns its own warps
+// the MMAs of S and dQ; warp 10: those of dP.  TMEM: S of even and odd steps at 0 and 128 (dS takes S's place, in the columns its own warps
 // have read), dP at 256, dQ at 384.  The tensor cores do dQ of a step and S of the one after next while
 // the warps work on the step between.  The first kernel of the backward pass: it also leaves delta.
-constexpr int kDqThreads = 320;
+constexpr int kDqThreads = 352;
 template <int HD> struct Dq {
     static constexpr int TILE = kRows * HD * 2;
     static constexpr int SMEM = 7 * TILE + 1024;           // Q, dO, three K, two V
@@ -492,7 +516,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
           const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmdo, const Params p) {
     constexpr int TILE = Dq<HD>::TILE;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t q_full, k_full[3], k_empty[3], v_full[2], v_empty[2], s_full[2], dp_full, ds_ready, mma_done;
+    __shared__ uint64_t q_full, k_full[3], k_empty[3], v_full[2], v_empty[2], s_full[2], dp_full, ds_ready[2], turn[2], mma_done[2];
     __shared__ uint32_t tmem_slot, abort_flag;
     __shared__ Item item;
     __shared__ float part[2][kRows];
@@ -515,8 +539,12 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             mbar_init(&s_full[i], 1);
         }
         mbar_init(&dp_full, 1);
-        mbar_init(&ds_ready, 8);
-        mbar_init(&mma_done, 1);
+        mbar_init(&ds_ready[0], 8);
+        mbar_init(&ds_ready[1], 8);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&turn[i], 1);
+            mbar_init(&mma_done[i], 1);
+        }
         abort_flag = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -559,14 +587,12 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             }
         }
     } else if (warp == 9 && steps > 0) {
-        const uint32_t idesc_s = idesc_bf16(kRows, false, p.scale < 0.0f), idesc_dp = idesc_bf16(kRows, false, false);
+        const uint32_t idesc_s = idesc_bf16(kRows, false, p.scale < 0.0f);
         const uint32_t idesc_dq = idesc_bf16((p.dim + 15) & ~15, true, false);
         const bool neighbours = item.other + item.other_len < p.tk;
-        const int ksteps = (p.dim + 15) / 16;
-        const uint32_t desc_q = uniform(desc_k_major(smem_addr(smem_q))), desc_do = desc_q + (TILE >> 4);
-        const uint32_t desc_k = uniform(desc_k_major(smem_addr(ring_k))), desc_v = uniform(desc_k_major(smem_addr(ring_v)));
-        const uint32_t desc_kt = uniform(desc_mn_major(smem_addr(ring_k)));
-        const int len = uniform(item.other_len);
+        const int ksteps = (p.dim + 15) / 16, len = uniform(item.other_len);
+        const uint32_t desc_q = uniform(desc_k_major(smem_addr(smem_q)));
+        const uint32_t desc_k = uniform(desc_k_major(smem_addr(ring_k))), desc_kt = uniform(desc_mn_major(smem_addr(ring_k)));
         auto issue_s = [&](int j) {
             const int slot = j % 3, valid = len - j * kRows;
             if (!wait.all(&k_full[slot], j / 3)) return false;
@@ -575,28 +601,45 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             commit(&s_full[j & 1], elect_one());
             return true;
         };
-        // V's rows past the sequence reach only columns of dP that are masked: no need to zero them
-        auto issue_dp = [&](int j) {
-            if (!wait.all(&v_full[j & 1], j / 2)) return false;
-            mma_heads<HD>(tmem + 256, desc_do, desc_v + (j & 1) * (TILE >> 4), ksteps, idesc_dp);
-            commit(&dp_full, elect_one());
-            commit(&v_empty[j & 1], elect_one());
-            return true;
-        };
-        bool ok = wait.all(&q_full, 0) && issue_s(0) && issue_dp(0) && (steps < 2 || issue_s(1));
+        // rounds: S 0, dP 0; S 1, dP 1; dQ 0 and S 2, dP 2; ...: the warps wait for dP first
+        const Turns turns{turn, wait, 0};
+        bool ok = wait.all(&q_full, 0) && issue_s(0);
+        turns.pass();
+        if (steps > 1) {
+            ok = ok && turns.take(1) && issue_s(1);
+            turns.pass();
+        }
         for (int j = 0; ok && j < steps; ++j) {
-            ok = wait.all(&ds_ready, j);
+            ok = (j + 2 > steps || turns.take(j + 2)) && wait.all(&ds_ready[j & 1], j >> 1);
             if (!ok) break;
             fence_after();
-            if (j + 1 < steps) ok = issue_dp(j + 1);
-            if (!ok) break;
             const uint32_t ds = tmem + 128 * (j & 1);
             mma_rows(tmem + 384, ds, ds + 64, desc_kt + (j % 3) * (TILE >> 4), idesc_dq, j > 0);
             commit(&k_empty[j % 3], elect_one());
             if (j + 2 < steps) ok = issue_s(j + 2);
+            turns.pass();
         }
-        commit(&mma_done, elect_one());
-        wait.drain(&mma_done, 0);
+        commit(&mma_done[0], elect_one());
+        wait.drain(&mma_done[0], 0);
+    } else if (warp == 10 && steps > 0) {
+        // V's rows past the sequence reach only columns of dP that are masked: no need to zero them
+        const uint32_t idesc_dp = idesc_bf16(kRows, false, false);
+        const int ksteps = (p.dim + 15) / 16;
+        const uint32_t desc_do = uniform(desc_k_major(smem_addr(smem_do))), desc_v = uniform(desc_k_major(smem_addr(ring_v)));
+        const Turns turns{turn, wait, 1};
+        bool ok = wait.all(&q_full, 0);
+        for (int j = 0; ok && j < steps; ++j) {
+            ok = wait.all(&v_full[j & 1], j / 2) && turns.take(j) &&
+                 (j == 0 || wait.all(&ds_ready[(j - 1) & 1], (j - 1) >> 1));    // dP of j - 1 has been read
+            if (!ok) break;
+            fence_after();
+            mma_heads<HD>(tmem + 256, desc_do, desc_v + (j & 1) * (TILE >> 4), ksteps, idesc_dp);
+            commit(&dp_full, elect_one());
+            turns.pass();
+            commit(&v_empty[j & 1], elect_one());
+        }
+        commit(&mma_done[1], elect_one());
+        wait.drain(&mma_done[1], 0);
     } else if (warp < 8 && item.valid) {
         const int half = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -669,13 +712,13 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             st_wait();
             fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ds_ready);
+            if (lane == 0) mbar_arrive(&ds_ready[j & 1]);
         }
         bf16* dst = p.dq.at(tok, item.head);
         if (steps == 0) {
             if (in && half == 0) store_zeros(dst, p.dim);
         } else if (ok) {
-            ok = wait(&mma_done, 0);
+            ok = wait(&mma_done[0], 0);
             fence_after();
             if (ok)
                 for (int i = 64 * half; i < min(p.dim, 64 * half + 64); i += 32) {
@@ -697,10 +740,10 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
 
 // ---------------------------------------------------------------------------- backward, dK and dV
 // Warps 0-7: a key per thread, warps 0-3 the first 64 queries of a tile, warps 4-7 the last 64; warp 8: TMA; warp 9:
-// MMAs; warp 10: lse and delta of the queries.  A step is one query tile of one of the heads that read the
+// the MMAs of S and dV; warp 10: those of dP and dK; warp 11: lse and delta of the queries.  A step is one query tile of one of the heads that read the
 // key head.  TMEM: S^T then P^T at 0, dP^T then dS^T at 128, dV at 256, dK at 384.  The tensor cores do dV of a
 // step and S of the next while the warps compute dS, and dK and the next dP while they compute P.
-constexpr int kDkvThreads = 352;
+constexpr int kDkvThreads = 384;
 template <int HD> struct Dkv {
     static constexpr int TILE = kRows * HD * 2;
     static constexpr int SMEM = 6 * TILE + 1024;           // K, V, two Q, two dO
@@ -714,7 +757,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
     constexpr int TILE = Dkv<HD>::TILE;
     extern __shared__ uint8_t raw[];
     __shared__ uint64_t kv_full, q_full[2], q_empty[2], do_full[2], do_empty[2], st_full[2], st_empty[2], s_full, dp_full,
-        p_ready, ds_ready, mma_done;
+        p_ready, ds_ready, turn[2], mma_done[2];
     __shared__ uint32_t tmem_slot, abort_flag;
     __shared__ Item item;
     __shared__ __align__(16) float stat[2][2][kRows];      // per slot: -lse log2(e), -delta
@@ -729,9 +772,9 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
         mbar_init(&kv_full, 1);
         for (int i = 0; i < 2; ++i) {
             mbar_init(&q_full[i], 1);
-            mbar_init(&q_empty[i], 1);
+            mbar_init(&q_empty[i], 2);
             mbar_init(&do_full[i], 1);
-            mbar_init(&do_empty[i], 1);
+            mbar_init(&do_empty[i], 2);
             mbar_init(&st_full[i], 1);
             mbar_init(&st_empty[i], 8);
         }
@@ -739,7 +782,10 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
         mbar_init(&dp_full, 1);
         mbar_init(&p_ready, 8);
         mbar_init(&ds_ready, 8);
-        mbar_init(&mma_done, 1);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&turn[i], 1);
+            mbar_init(&mma_done[i], 1);
+        }
         abort_flag = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
@@ -786,7 +832,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
                 for (int i = max(0, got_do - 2); i < got_do; ++i) wait.drain(&do_full[i & 1], i / 2);
             }
         }
-    } else if (warp == 10 && steps > 0) {
+    } else if (warp == 11 && steps > 0) {
         for (int i = 0; i < steps; ++i) {
             const int slot = i & 1;
             if (i >= 2 && !wait(&st_empty[slot], i / 2 - 1)) break;
@@ -801,48 +847,54 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
             __syncwarp();
             if (lane == 0) mbar_arrive(&st_full[slot]);
         }
-    } else if (warp == 9 && steps > 0) {
-        const uint32_t idesc_s = idesc_bf16(kRows, false, p.scale < 0.0f), idesc_dp = idesc_bf16(kRows, false, false);
-        const uint32_t idesc_d = idesc_bf16((p.dim + 15) & ~15, true, false);
+    } else if ((warp == 9 || warp == 10) && steps > 0) {
+        // warp 9: S and dV, with K and then dout as B; warp 10: dP and dK, with V and then Q
+        const int w = warp - 9;
+        const uint32_t idesc_in = idesc_bf16(kRows, false, w == 0 && p.scale < 0.0f);
+        const uint32_t idesc_out = idesc_bf16((p.dim + 15) & ~15, true, false);
         const bool neighbours = item.other + item.other_len < p.tq;
-        const int ksteps = (p.dim + 15) / 16;
-        const uint32_t desc_k = uniform(desc_k_major(smem_addr(smem_k))), desc_v = desc_k + (TILE >> 4);
-        const uint32_t desc_q = uniform(desc_k_major(smem_addr(ring_q))), desc_do = desc_q + 2 * (TILE >> 4);
-        const uint32_t desc_qt = uniform(desc_mn_major(smem_addr(ring_q))), desc_dot = desc_qt + 2 * (TILE >> 4);
-        auto issue_s = [&](int i) {
-            const int slot = i & 1, valid = item.other_len - row_of(i);
-            if (!wait.all(&q_full[slot], i / 2)) return false;
-            if (valid < kRows && neighbours) zero_tail<HD>(ring_q + slot * TILE, valid);
-            mma_heads<HD>(tmem, desc_k, desc_q + slot * (TILE >> 4), ksteps, idesc_s);
-            commit(&s_full, elect_one());
+        const int ksteps = (p.dim + 15) / 16, len = uniform(item.other_len);
+        uint8_t *ring_in = w ? ring_do : ring_q, *ring_out = w ? ring_q : ring_do;
+        const uint32_t desc_a = uniform(desc_k_major(smem_addr(w ? smem_v : smem_k)));
+        const uint32_t desc_in = uniform(desc_k_major(smem_addr(ring_in))), desc_out = uniform(desc_mn_major(smem_addr(ring_out)));
+        const uint32_t ts = uniform(tmem + 128 * w), to = uniform(tmem + 256 + 128 * w);
+        uint64_t *in_full = w ? do_full : q_full, *in_done = w ? &dp_full : &s_full, *ready = w ? &ds_ready : &p_ready;
+        uint64_t *out_full = w ? q_full : do_full, *out_empty = w ? q_empty : do_empty;
+        const Turns turns{turn, wait, w};
+        auto clean = [&](uint8_t* tile, int i) {           // rows of a neighbouring sequence
+            const int valid = len - row_of(i);
+            if (valid < kRows && neighbours) zero_tail<HD>(tile, valid);
+        };
+        auto tile_in = [&](int i) {
+            if (!wait.all(&in_full[i & 1], i / 2)) return false;
+            clean(ring_in + (i & 1) * TILE, i);
             return true;
         };
-        auto issue_dp = [&](int i) {
-            const int slot = i & 1, valid = item.other_len - row_of(i);
-            if (!wait.all(&do_full[slot], i / 2)) return false;
-            if (valid < kRows && neighbours) zero_tail<HD>(ring_do + slot * TILE, valid);
-            mma_heads<HD>(tmem + 128, desc_v, desc_do + slot * (TILE >> 4), ksteps, idesc_dp);
-            commit(&dp_full, elect_one());
-            return true;
+        auto issue_in = [&](int i) {
+            const int slot = i & 1;
+            mma_heads<HD>(ts, desc_a, desc_in + slot * (TILE >> 4), ksteps, idesc_in);
+            commit(in_done, elect_one());
+            turns.pass();
+            commit(&(w ? do_empty : q_empty)[slot], elect_one());
         };
-        bool ok = wait.all(&kv_full, 0) && issue_s(0) && issue_dp(0);
+        // rounds: S 0, dP 0; dV 0 and S 1, dK 0 and dP 1; ...
+        bool ok = wait.all(&kv_full, 0) && tile_in(0) && turns.take(0);
+        if (ok) issue_in(0);
         for (int i = 0; ok && i < steps; ++i) {
             const int slot = i & 1;
-            ok = wait.all(&p_ready, i);
+            ok = wait.all(&out_full[slot], i / 2) && (i + 1 >= steps || tile_in(i + 1));
+            if (!ok) break;
+            clean(ring_out + slot * TILE, i);
+            ok = turns.take(i + 1) && wait.all(ready, i);
             if (!ok) break;
             fence_after();
-            mma_rows(tmem + 256, tmem, tmem + 64, desc_dot + slot * (TILE >> 4), idesc_d, i > 0);
-            commit(&do_empty[slot], elect_one());
-            if (i + 1 < steps) ok = issue_s(i + 1);
-            ok = ok && wait.all(&ds_ready, i);
-            if (!ok) break;
-            fence_after();
-            mma_rows(tmem + 384, tmem + 128, tmem + 192, desc_qt + slot * (TILE >> 4), idesc_d, i > 0);
-            commit(&q_empty[slot], elect_one());
-            if (i + 1 < steps) ok = issue_dp(i + 1);
+            mma_rows(to, ts, ts + 64, desc_out + slot * (TILE >> 4), idesc_out, i > 0);
+            commit(&out_empty[slot], elect_one());
+            if (i + 1 < steps) issue_in(i + 1);
+            else turns.pass();
         }
-        commit(&mma_done, elect_one());
-        wait.drain(&mma_done, 0);
+        commit(&mma_done[w], elect_one());
+        wait.drain(&mma_done[w], 0);
     } else if (warp < 8 && item.valid) {
         const int half = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -860,14 +912,18 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
             ld_wait();
             fence32(s[0]);
             fence32(s[1]);
-            const float2* lse2 = reinterpret_cast<const float2*>(&stat[slot][0][64 * half]);
-            const float2* del2 = reinterpret_cast<const float2*>(&stat[slot][1][64 * half]);
+            const float4* lse4 = reinterpret_cast<const float4*>(&stat[slot][0][64 * half]);
+            const float4* del4 = reinterpret_cast<const float4*>(&stat[slot][1][64 * half]);
 #pragma unroll
-            for (int e = 0; e < 64; e += 2) {
-                float2 x = make_float2(__uint_as_float(s[e >> 5][e & 31]), __uint_as_float(s[e >> 5][(e & 31) + 1]));
-                x = __ffma2_rn(x, c2, lse2[e >> 1]);
-                s[e >> 5][e & 31] = __float_as_uint(ex2(x.x));
-                s[e >> 5][(e & 31) + 1] = __float_as_uint(ex2(x.y));
+            for (int e = 0; e < 64; e += 4) {
+                uint32_t* v = &s[e >> 5][e & 31];
+                const float4 n4 = lse4[e >> 2];
+                const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), c2, make_float2(n4.x, n4.y));
+                const float2 y = __ffma2_rn(make_float2(__uint_as_float(v[2]), __uint_as_float(v[3])), c2, make_float2(n4.z, n4.w));
+                v[0] = __float_as_uint(ex2(x.x));
+                v[1] = __float_as_uint(ex2(x.y));
+                v[2] = __float_as_uint(ex2(y.x));
+                v[3] = __float_as_uint(ex2(y.y));
             }
             // masked pairs: queries before r + diag
             const int from = p.causal ? r + item.diag - row_of(i) - 64 * half : 0;
@@ -894,11 +950,15 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
             fence32(g[0]);
             fence32(g[1]);
 #pragma unroll
-            for (int e = 0; e < 64; e += 2) {
-                const float2 pr = make_float2(__uint_as_float(s[e >> 5][e & 31]), __uint_as_float(s[e >> 5][(e & 31) + 1]));
-                float2 x = make_float2(__uint_as_float(g[e >> 5][e & 31]), __uint_as_float(g[e >> 5][(e & 31) + 1]));
-                x = __fmul2_rn(pr, __fadd2_rn(x, del2[e >> 1]));
+            for (int e = 0; e < 64; e += 4) {
+                const uint32_t *v = &s[e >> 5][e & 31], *u = &g[e >> 5][e & 31];
+                const float4 n4 = del4[e >> 2];
+                const float2 x = __fmul2_rn(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])),
+                                            __fadd2_rn(make_float2(__uint_as_float(u[0]), __uint_as_float(u[1])), make_float2(n4.x, n4.y)));
+                const float2 y = __fmul2_rn(make_float2(__uint_as_float(v[2]), __uint_as_float(v[3])),
+                                            __fadd2_rn(make_float2(__uint_as_float(u[2]), __uint_as_float(u[3])), make_float2(n4.z, n4.w)));
                 w[e >> 1] = pack_bf16(x.x, x.y);
+                w[(e >> 1) + 1] = pack_bf16(y.x, y.y);
             }
             st32(tdp, w);
             st_wait();
@@ -915,7 +975,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
         if (steps == 0) {
             if (in) store_zeros(dst, p.dim);
         } else if (ok) {
-            ok = wait(&mma_done, 0);
+            ok = wait(&mma_done[half], 0);
             fence_after();
             if (ok)
                 for (int i = 0; i < p.dim; i += 32) {
