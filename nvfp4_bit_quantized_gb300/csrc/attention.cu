@@ -30,6 +30,7 @@
 #include <cstdint>
 #include <cstring>
 #include <mutex>
+#include <type_traits>
 
 #include "device_common.cuh"
 #include "host_common.h"
@@ -191,6 +192,18 @@ struct Turns {
     __device__ __forceinline__ void pass() const {
         if (elect_one()) mbar_arrive(&bar[w ^ 1]);
         __syncwarp();
+    }
+};
+
+// A slot of a ring of N and the parity of its barriers' present phase.
+template <int N> struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == N) {
+            slot = 0;
+            phase ^= 1u;
+        }
     }
 };
 
@@ -744,59 +757,71 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
 // key head.  TMEM: S^T then P^T at 0, dP^T then dS^T at 128, dV at 256, dK at 384.  The tensor cores do dV of a
 // step and S of the next while the warps compute dS, and dK and the next dP while they compute P.
 constexpr int kDkvThreads = 384;
+// Q is held from its first product to its last, a step and a half: with two slots a load had half a
+// step's time and the MMAs waited for it (a third slot took 0.13 ms off 1.76 ms for the whole backward
+// pass at 8192 tokens, 40 / 8 heads of 128, causal).
 template <int HD> struct Dkv {
     static constexpr int TILE = kRows * HD * 2;
-    static constexpr int SMEM = 6 * TILE + 1024;           // K, V, two Q, two dO
-    static constexpr int PAD = HD == 128 ? SMEM : 120 * 1024;
+    static constexpr int QS = HD == 128 ? 3 : 4, DS = HD == 128 ? 2 : 4;
+    struct Ctl {
+        float stat[2][2][kRows];                           // per slot: -lse log2(e), -delta
+        uint64_t kv_full, q_full[QS], q_empty[QS], do_full[DS], do_empty[DS], st_full[2], st_empty[2], s_full, dp_full,
+            p_ready, ds_ready, turn[2], mma_done[2];
+        Item item;
+        uint32_t tmem_slot, abort_flag;
+    };
+    static constexpr int TILES = (2 + QS + DS) * TILE;     // K, V, the Q's, the dO's
+    static constexpr int SMEM = TILES + (int)sizeof(Ctl);
+    static_assert(SMEM <= 232448 && SMEM > 116 * 1024, "one CTA fits an SM (TMEM is taken whole)");
 };
 
 template <int HD>
 __global__ void __launch_bounds__(kDkvThreads, 1)
 dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
            const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmdo, const Params p) {
-    constexpr int TILE = Dkv<HD>::TILE;
-    extern __shared__ uint8_t raw[];
-    __shared__ uint64_t kv_full, q_full[2], q_empty[2], do_full[2], do_empty[2], st_full[2], st_empty[2], s_full, dp_full,
-        p_ready, ds_ready, turn[2], mma_done[2];
-    __shared__ uint32_t tmem_slot, abort_flag;
-    __shared__ Item item;
-    __shared__ __align__(16) float stat[2][2][kRows];      // per slot: -lse log2(e), -delta
-    uint8_t* smem_k = align1024(raw);
+    using Cfg = Dkv<HD>;
+    constexpr int TILE = Cfg::TILE, QS = Cfg::QS, DS = Cfg::DS;
+    extern __shared__ __align__(1024) uint8_t tiles_smem[];
+    uint8_t* smem_k = tiles_smem;
     uint8_t* smem_v = smem_k + TILE;
     uint8_t* ring_q = smem_v + TILE;
-    uint8_t* ring_do = ring_q + 2 * TILE;
+    uint8_t* ring_do = ring_q + QS * TILE;
+    typename Cfg::Ctl& ctl = *reinterpret_cast<typename Cfg::Ctl*>(tiles_smem + Cfg::TILES);
     const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
 
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
-        mbar_init(&kv_full, 1);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&q_full[i], 1);
-            mbar_init(&q_empty[i], 2);
-            mbar_init(&do_full[i], 1);
-            mbar_init(&do_empty[i], 2);
-            mbar_init(&st_full[i], 1);
-            mbar_init(&st_empty[i], 8);
+        mbar_init(&ctl.kv_full, 1);
+        for (int i = 0; i < QS; ++i) {
+            mbar_init(&ctl.q_full[i], 1);
+            mbar_init(&ctl.q_empty[i], 2);
         }
-        mbar_init(&s_full, 1);
-        mbar_init(&dp_full, 1);
-        mbar_init(&p_ready, 8);
-        mbar_init(&ds_ready, 8);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&turn[i], 1);
-            mbar_init(&mma_done[i], 1);
+        for (int i = 0; i < DS; ++i) {
+            mbar_init(&ctl.do_full[i], 1);
+            mbar_init(&ctl.do_empty[i], 2);
         }
-        abort_flag = 0u;
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&ctl.st_full[i], 1);
+            mbar_init(&ctl.st_empty[i], 8);
+            mbar_init(&ctl.turn[i], 1);
+            mbar_init(&ctl.mma_done[i], 1);
+        }
+        mbar_init(&ctl.s_full, 1);
+        mbar_init(&ctl.dp_full, 1);
+        mbar_init(&ctl.p_ready, 8);
+        mbar_init(&ctl.ds_ready, 8);
+        ctl.abort_flag = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 9) tmem_alloc_all(&tmem_slot);
+    if (warp == 9) tmem_alloc_all(&ctl.tmem_slot);
     pdl_wait();
-    if (warp == 8) find_item(p, false, kRows, p.kv_heads, &item);
+    if (warp == 8) find_item(p, false, kRows, p.kv_heads, &ctl.item);
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = uniform(tmem_slot);
-    const Wait wait{p.timeout_ns, &abort_flag, p.dev_status};
+    const Item& item = ctl.item;
+    const uint32_t tmem = uniform(ctl.tmem_slot);
+    const Wait wait{p.timeout_ns, &ctl.abort_flag, p.dev_status};
     const int share = p.heads / p.kv_heads;
     // With the causal mask key r of the tile is seen by the queries from r + diag on.
     int first_tile = 0, tiles = 0, steps = 0;
@@ -806,141 +831,188 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
         steps = tiles * share;
     }
     steps = uniform(steps);
-    auto head_of = [&](int i) { return item.head * share + i / tiles; };
-    auto row_of = [&](int i) { return (first_tile + i % tiles) * kRows; };
+    first_tile = uniform(first_tile);
+    // the steps in order: the query tiles of the first head, of the second, ...
+    struct Step {
+        int head, tile, tiles;
+        __device__ __forceinline__ void next() {
+            if (++tile == tiles) {
+                tile = 0;
+                ++head;
+            }
+        }
+    };
+    const Step begin{uniform(item.head) * share, 0, uniform(tiles)};
+    auto row_of = [&](const Step& s) { return (first_tile + s.tile) * kRows; };
 
     if (warp == 8 && steps > 0) {
         if (lane == 0) {
-            mbar_arrive_expect_tx(&kv_full, 2 * TILE);
-            load_tile<HD>(smem_k, &tmk, item.first, item.head, &kv_full);
-            load_tile<HD>(smem_v, &tmv, item.first, item.head, &kv_full);
+            mbar_arrive_expect_tx(&ctl.kv_full, 2 * TILE);
+            load_tile<HD>(smem_k, &tmk, item.first, item.head, &ctl.kv_full);
+            load_tile<HD>(smem_v, &tmv, item.first, item.head, &ctl.kv_full);
             int got_q = 0, got_do = 0;
-            for (int i = 0; i < steps; ++i) {
-                const int slot = i & 1;
-                if (i >= 2 && !wait(&q_empty[slot], i / 2 - 1)) break;
-                mbar_arrive_expect_tx(&q_full[slot], TILE);
-                load_tile<HD>(ring_q + slot * TILE, &tmq, item.other + row_of(i), head_of(i), &q_full[slot]);
+            Ring<QS> q;
+            Ring<DS> d;
+            Step s = begin;
+            for (int i = 0; i < steps; ++i, s.next()) {
+                if (!wait(&ctl.q_empty[q.slot], q.phase ^ 1u)) break;
+                mbar_arrive_expect_tx(&ctl.q_full[q.slot], TILE);
+                load_tile<HD>(ring_q + q.slot * TILE, &tmq, item.other + row_of(s), s.head, &ctl.q_full[q.slot]);
                 got_q = i + 1;
-                if (i >= 2 && !wait(&do_empty[slot], i / 2 - 1)) break;
-                mbar_arrive_expect_tx(&do_full[slot], TILE);
-                load_tile<HD>(ring_do + slot * TILE, &tmdo, item.other + row_of(i), head_of(i), &do_full[slot]);
+                if (!wait(&ctl.do_empty[d.slot], d.phase ^ 1u)) break;
+                mbar_arrive_expect_tx(&ctl.do_full[d.slot], TILE);
+                load_tile<HD>(ring_do + d.slot * TILE, &tmdo, item.other + row_of(s), s.head, &ctl.do_full[d.slot]);
                 got_do = i + 1;
+                q.next();
+                d.next();
             }
             if (got_do < steps) {                          // aborted: the copies in flight land first
-                wait.drain(&kv_full, 0);
-                for (int i = max(0, got_q - 2); i < got_q; ++i) wait.drain(&q_full[i & 1], i / 2);
-                for (int i = max(0, got_do - 2); i < got_do; ++i) wait.drain(&do_full[i & 1], i / 2);
+                wait.drain(&ctl.kv_full, 0);
+                for (int i = max(0, got_q - QS); i < got_q; ++i) wait.drain(&ctl.q_full[i % QS], i / QS);
+                for (int i = max(0, got_do - DS); i < got_do; ++i) wait.drain(&ctl.do_full[i % DS], i / DS);
             }
         }
     } else if (warp == 11 && steps > 0) {
-        for (int i = 0; i < steps; ++i) {
-            const int slot = i & 1;
-            if (i >= 2 && !wait(&st_empty[slot], i / 2 - 1)) break;
-            const int64_t at = (int64_t)head_of(i) * p.tq + item.other;
-            for (int r = lane; r < kRows; r += 32) {
-                const int q = row_of(i) + r;
+        // a step's values are fetched while the step before waits for its slot
+        Ring<2> r;
+        Step s = begin;
+        float l[4], d[4];
+        auto fetch = [&] {
+            const int64_t at = (int64_t)s.head * p.tq + item.other;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const int q = row_of(s) + lane + 32 * e;
                 const bool in = q < item.other_len;
-                const float lse = in ? p.lse[at + q] : -INFINITY;
-                stat[slot][0][r] = lse == -INFINITY ? -INFINITY : -lse * kLog2e;   // such queries: P = 0
-                stat[slot][1][r] = in ? -p.delta[at + q] : 0.0f;
+                l[e] = in ? p.lse[at + q] : -INFINITY;
+                d[e] = in ? p.delta[at + q] : 0.0f;
+            }
+        };
+        fetch();
+        for (int i = 0; i < steps; ++i, r.next()) {
+            if (!wait(&ctl.st_empty[r.slot], r.phase ^ 1u)) break;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                ctl.stat[r.slot][0][lane + 32 * e] = l[e] == -INFINITY ? -INFINITY : -l[e] * kLog2e;   // such queries: P = 0
+                ctl.stat[r.slot][1][lane + 32 * e] = -d[e];
             }
             __syncwarp();
-            if (lane == 0) mbar_arrive(&st_full[slot]);
+            if (lane == 0) mbar_arrive(&ctl.st_full[r.slot]);
+            s.next();
+            if (i + 1 < steps) fetch();
         }
     } else if ((warp == 9 || warp == 10) && steps > 0) {
-        // warp 9: S and dV, with K and then dout as B; warp 10: dP and dK, with V and then Q
-        const int w = warp - 9;
-        const uint32_t idesc_in = idesc_bf16(kRows, false, w == 0 && p.scale < 0.0f);
+        // The same loop for both, on other tiles: A = K or V once with the `in` tile (a first product into ts), then,
+        // when the warps have put P or dS there, with the `out` tile (the sum at to).
         const uint32_t idesc_out = idesc_bf16((p.dim + 15) & ~15, true, false);
         const bool neighbours = item.other + item.other_len < p.tq;
         const int ksteps = (p.dim + 15) / 16, len = uniform(item.other_len);
-        uint8_t *ring_in = w ? ring_do : ring_q, *ring_out = w ? ring_q : ring_do;
-        const uint32_t desc_a = uniform(desc_k_major(smem_addr(w ? smem_v : smem_k)));
-        const uint32_t desc_in = uniform(desc_k_major(smem_addr(ring_in))), desc_out = uniform(desc_mn_major(smem_addr(ring_out)));
-        const uint32_t ts = uniform(tmem + 128 * w), to = uniform(tmem + 256 + 128 * w);
-        uint64_t *in_full = w ? do_full : q_full, *in_done = w ? &dp_full : &s_full, *ready = w ? &ds_ready : &p_ready;
-        uint64_t *out_full = w ? q_full : do_full, *out_empty = w ? q_empty : do_empty;
-        const Turns turns{turn, wait, w};
-        auto clean = [&](uint8_t* tile, int i) {           // rows of a neighbouring sequence
-            const int valid = len - row_of(i);
+        auto clean = [&](uint8_t* tile, const Step& s) {   // rows of a neighbouring sequence
+            const int valid = len - row_of(s);
             if (valid < kRows && neighbours) zero_tail<HD>(tile, valid);
         };
-        auto tile_in = [&](int i) {
-            if (!wait.all(&in_full[i & 1], i / 2)) return false;
-            clean(ring_in + (i & 1) * TILE, i);
-            return true;
+        auto chain = [&](auto in, auto out, int w, uint32_t idesc_in, const uint8_t* a, uint8_t* ring_in, uint8_t* ring_out,
+                         uint64_t* in_full, uint64_t* in_empty, uint64_t* out_full, uint64_t* out_empty, uint64_t* in_done,
+                         uint64_t* ready) {
+            const uint32_t desc_a = uniform(desc_k_major(smem_addr(a)));
+            const uint32_t desc_in = uniform(desc_k_major(smem_addr(ring_in))), desc_out = uniform(desc_mn_major(smem_addr(ring_out)));
+            const uint32_t ts = tmem + 128 * w, to = tmem + 256 + 128 * w;
+            const Turns turns{ctl.turn, wait, w};
+            Step si = begin, so = begin;
+            auto tile_in = [&] {
+                if (!wait.all(&in_full[in.slot], in.phase)) return false;
+                clean(ring_in + in.slot * TILE, si);
+                return true;
+            };
+            auto issue_in = [&] {
+                mma_heads<HD>(ts, desc_a, desc_in + in.slot * (TILE >> 4), ksteps, idesc_in);
+                commit(in_done, elect_one());
+                turns.pass();
+                commit(&in_empty[in.slot], elect_one());
+                in.next();
+                si.next();
+            };
+            // rounds: S 0, dP 0; dV 0 and S 1, dK 0 and dP 1; ...
+            bool ok = wait.all(&ctl.kv_full, 0) && tile_in() && turns.take(0);
+            if (ok) issue_in();
+            for (int i = 0; ok && i < steps; ++i) {
+                ok = wait.all(&out_full[out.slot], out.phase) && (i + 1 >= steps || tile_in());
+                if (!ok) break;
+                clean(ring_out + out.slot * TILE, so);
+                ok = turns.take(i + 1) && wait.all(ready, i);
+                if (!ok) break;
+                fence_after();
+                mma_rows(to, ts, ts + 64, desc_out + out.slot * (TILE >> 4), idesc_out, i > 0);
+                commit(&out_empty[out.slot], elect_one());
+                if (i + 1 < steps) issue_in();
+                else turns.pass();
+                out.next();
+                so.next();
+            }
+            commit(&ctl.mma_done[w], elect_one());
+            wait.drain(&ctl.mma_done[w], 0);
         };
-        auto issue_in = [&](int i) {
-            const int slot = i & 1;
-            mma_heads<HD>(ts, desc_a, desc_in + slot * (TILE >> 4), ksteps, idesc_in);
-            commit(in_done, elect_one());
-            turns.pass();
-            commit(&(w ? do_empty : q_empty)[slot], elect_one());
-        };
-        // rounds: S 0, dP 0; dV 0 and S 1, dK 0 and dP 1; ...
-        bool ok = wait.all(&kv_full, 0) && tile_in(0) && turns.take(0);
-        if (ok) issue_in(0);
-        for (int i = 0; ok && i < steps; ++i) {
-            const int slot = i & 1;
-            ok = wait.all(&out_full[slot], i / 2) && (i + 1 >= steps || tile_in(i + 1));
-            if (!ok) break;
-            clean(ring_out + slot * TILE, i);
-            ok = turns.take(i + 1) && wait.all(ready, i);
-            if (!ok) break;
-            fence_after();
-            mma_rows(to, ts, ts + 64, desc_out + slot * (TILE >> 4), idesc_out, i > 0);
-            commit(&out_empty[slot], elect_one());
-            if (i + 1 < steps) issue_in(i + 1);
-            else turns.pass();
-        }
-        commit(&mma_done[w], elect_one());
-        wait.drain(&mma_done[w], 0);
+        if (warp == 9)
+            chain(Ring<QS>{}, Ring<DS>{}, 0, idesc_bf16(kRows, false, p.scale < 0.0f), smem_k, ring_q, ring_do, ctl.q_full,
+                  ctl.q_empty, ctl.do_full, ctl.do_empty, &ctl.s_full, &ctl.p_ready);
+        else
+            chain(Ring<DS>{}, Ring<QS>{}, 1, idesc_bf16(kRows, false, false), smem_v, ring_do, ring_q, ctl.do_full,
+                  ctl.do_empty, ctl.q_full, ctl.q_empty, &ctl.dp_full, &ctl.ds_ready);
     } else if (warp < 8 && item.valid) {
         const int half = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + 64 * half + lanes, tdp = tmem + 128 + 64 * half + lanes;
         const float2 c2 = make_float2(p.c, p.c);
         bool ok = true;
-        for (int i = 0; i < steps; ++i) {
-            const int slot = i & 1;
-            ok = wait(&st_full[slot], i / 2) && wait(&s_full, i);
+        Ring<2> st;
+        Step step = begin;
+        for (int i = 0; i < steps; ++i, step.next(), st.next()) {
+            ok = wait(&ctl.st_full[st.slot], st.phase);
+            if (!ok) break;
+            // read ahead of S: beside MMAs that take all of shared memory's bandwidth these loads are slow
+            float4 lse4[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) lse4[e] = reinterpret_cast<const float4*>(&ctl.stat[st.slot][0][64 * half])[e];
+            ok = wait(&ctl.s_full, i);
             if (!ok) break;
             fence_after();
-            uint32_t s[2][32], w[32];
+            uint32_t s[2][32];
             ld32(ts, s[0]);
             ld32(ts + 32, s[1]);
             ld_wait();
             fence32(s[0]);
             fence32(s[1]);
-            const float4* lse4 = reinterpret_cast<const float4*>(&stat[slot][0][64 * half]);
-            const float4* del4 = reinterpret_cast<const float4*>(&stat[slot][1][64 * half]);
+            const float4* del4 = reinterpret_cast<const float4*>(&ctl.stat[st.slot][1][64 * half]);
+            const int from = r + item.diag - row_of(step) - 64 * half;     // masked pairs: queries before r + diag
+            auto probabilities = [&](auto masked) {
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) {
-                uint32_t* v = &s[e >> 5][e & 31];
-                const float4 n4 = lse4[e >> 2];
-                const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), c2, make_float2(n4.x, n4.y));
-                const float2 y = __ffma2_rn(make_float2(__uint_as_float(v[2]), __uint_as_float(v[3])), c2, make_float2(n4.z, n4.w));
-                v[0] = __float_as_uint(ex2(x.x));
-                v[1] = __float_as_uint(ex2(x.y));
-                v[2] = __float_as_uint(ex2(y.x));
-                v[3] = __float_as_uint(ex2(y.y));
-            }
-            // masked pairs: queries before r + diag
-            const int from = p.causal ? r + item.diag - row_of(i) - 64 * half : 0;
-            if (p.causal && kRows - 1 + item.diag > row_of(i)) {
+                for (int h = 0; h < 4; ++h) {
+                    uint32_t w[8];
 #pragma unroll
-                for (int e = 0; e < 64; ++e)
-                    if (e < from) s[e >> 5][e & 31] = 0u;
-            }
+                    for (int e = 0; e < 16; e += 4) {
+                        uint32_t* v = &s[h >> 1][(h & 1) * 16 + e];
+                        const float4 n4 = lse4[h * 4 + (e >> 2)];
+                        const float2 x = __ffma2_rn(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])), c2, make_float2(n4.x, n4.y));
+                        const float2 y = __ffma2_rn(make_float2(__uint_as_float(v[2]), __uint_as_float(v[3])), c2, make_float2(n4.z, n4.w));
+                        float f[4] = {ex2(x.x), ex2(x.y), ex2(y.x), ex2(y.y)};
+                        if constexpr (decltype(masked)::value)
 #pragma unroll
-            for (int e = 0; e < 64; e += 2)
-                w[e >> 1] = pack_bf16(__uint_as_float(s[e >> 5][e & 31]), __uint_as_float(s[e >> 5][(e & 31) + 1]));
-            st32(ts, w);
+                            for (int k = 0; k < 4; ++k)
+                                if (h * 16 + e + k < from) f[k] = 0.0f;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) v[k] = __float_as_uint(f[k]);
+                        w[e >> 1] = pack_bf16(f[0], f[1]);
+                        w[(e >> 1) + 1] = pack_bf16(f[2], f[3]);
+                    }
+                    st8(ts + 8 * h, w);
+                }
+            };
+            if (p.causal && kRows - 1 + item.diag > row_of(step)) probabilities(std::true_type{});
+            else probabilities(std::false_type{});
             st_wait();
             fence_before();
             __syncwarp();
-            if (lane == 0) mbar_arrive(&p_ready);
-            ok = wait(&dp_full, i);
+            if (lane == 0) mbar_arrive(&ctl.p_ready);
+            ok = wait(&ctl.dp_full, i);
             if (!ok) break;
             fence_after();
             uint32_t g[2][32];
@@ -950,23 +1022,27 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
             fence32(g[0]);
             fence32(g[1]);
 #pragma unroll
-            for (int e = 0; e < 64; e += 4) {
-                const uint32_t *v = &s[e >> 5][e & 31], *u = &g[e >> 5][e & 31];
-                const float4 n4 = del4[e >> 2];
-                const float2 x = __fmul2_rn(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])),
-                                            __fadd2_rn(make_float2(__uint_as_float(u[0]), __uint_as_float(u[1])), make_float2(n4.x, n4.y)));
-                const float2 y = __fmul2_rn(make_float2(__uint_as_float(v[2]), __uint_as_float(v[3])),
-                                            __fadd2_rn(make_float2(__uint_as_float(u[2]), __uint_as_float(u[3])), make_float2(n4.z, n4.w)));
-                w[e >> 1] = pack_bf16(x.x, x.y);
-                w[(e >> 1) + 1] = pack_bf16(y.x, y.y);
+            for (int h = 0; h < 4; ++h) {
+                uint32_t w[8];
+#pragma unroll
+                for (int e = 0; e < 16; e += 4) {
+                    const uint32_t *v = &s[h >> 1][(h & 1) * 16 + e], *u = &g[h >> 1][(h & 1) * 16 + e];
+                    const float4 n4 = del4[h * 4 + (e >> 2)];
+                    const float2 x = __fmul2_rn(make_float2(__uint_as_float(v[0]), __uint_as_float(v[1])),
+                                                __fadd2_rn(make_float2(__uint_as_float(u[0]), __uint_as_float(u[1])), make_float2(n4.x, n4.y)));
+                    const float2 y = __fmul2_rn(make_float2(__uint_as_float(v[2]), __uint_as_float(v[3])),
+                                                __fadd2_rn(make_float2(__uint_as_float(u[2]), __uint_as_float(u[3])), make_float2(n4.z, n4.w)));
+                    w[e >> 1] = pack_bf16(x.x, x.y);
+                    w[(e >> 1) + 1] = pack_bf16(y.x, y.y);
+                }
+                st8(tdp + 8 * h, w);
             }
-            st32(tdp, w);
             st_wait();
             fence_before();
             __syncwarp();
             if (lane == 0) {
-                mbar_arrive(&ds_ready);
-                mbar_arrive(&st_empty[slot]);
+                mbar_arrive(&ctl.ds_ready);
+                mbar_arrive(&ctl.st_empty[st.slot]);
             }
         }
         const bool in = r < item.rows;
@@ -975,7 +1051,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
         if (steps == 0) {
             if (in) store_zeros(dst, p.dim);
         } else if (ok) {
-            ok = wait(&mma_done[half], 0);
+            ok = wait(&ctl.mma_done[half], 0);
             fence_after();
             if (ok)
                 for (int i = 0; i < p.dim; i += 32) {
@@ -1167,10 +1243,10 @@ extern "C" nvfp4_status nvfp4_attention_backward(const nvfp4_attention_shape* sh
     cudaError_t e = cudaSuccess;
     if (p.dim <= 64) {
         if (p.tq > 0) e = launch(dq_kernel<64>, Dq<64>::PAD, kDqThreads, grid_q, s, mq, mk, mv, mdo, p);
-        if (e == cudaSuccess && p.tk > 0) e = launch(dkv_kernel<64>, Dkv<64>::PAD, kDkvThreads, grid_k, s, mq, mk, mv, mdo, p);
+        if (e == cudaSuccess && p.tk > 0) e = launch(dkv_kernel<64>, Dkv<64>::SMEM, kDkvThreads, grid_k, s, mq, mk, mv, mdo, p);
     } else {
         if (p.tq > 0) e = launch(dq_kernel<128>, Dq<128>::PAD, kDqThreads, grid_q, s, mq, mk, mv, mdo, p);
-        if (e == cudaSuccess && p.tk > 0) e = launch(dkv_kernel<128>, Dkv<128>::PAD, kDkvThreads, grid_k, s, mq, mk, mv, mdo, p);
+        if (e == cudaSuccess && p.tk > 0) e = launch(dkv_kernel<128>, Dkv<128>::SMEM, kDkvThreads, grid_k, s, mq, mk, mv, mdo, p);
     }
     return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }
