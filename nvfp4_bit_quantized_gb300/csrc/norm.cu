@@ -48,21 +48,27 @@ template <typename T, int E> struct Chunk;
 template <typename T> struct Chunk<T, 1> {
     T v;
     __device__ __forceinline__ void load(const T* p) { v = *p; }
+    __device__ __forceinline__ void store(T* p) const { *p = v; }
     __device__ __forceinline__ void get(float (&f)[1]) const { f[0] = load1(&v); }
+    __device__ __forceinline__ void set(const float (&f)[1]) { store1(&v, f[0]); }
     __device__ __forceinline__ static void put(T* p, const float (&f)[1]) { store1(p, f[0]); }
 };
 template <> struct Chunk<bf16, 8> {
     uint4 v;
     __device__ __forceinline__ void load(const bf16* p) { v = ld16(p); }
+    __device__ __forceinline__ void store(bf16* p) const { *reinterpret_cast<uint4*>(p) = v; }
     __device__ __forceinline__ void get(float (&f)[8]) const { Vec<uint16_t>::unpack(v, f); }
+    __device__ __forceinline__ static uint32_t pack(float lo, float hi) {
+        const __nv_bfloat162 b = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&b);
+    }
+    __device__ __forceinline__ void set(const float (&f)[8]) {
+        v = make_uint4(pack(f[0], f[1]), pack(f[2], f[3]), pack(f[4], f[5]), pack(f[6], f[7]));
+    }
     __device__ __forceinline__ static void put(bf16* p, const float (&f)[8]) {
-        uint32_t w[4];
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const __nv_bfloat162 b = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&b);
-        }
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+        Chunk c;
+        c.set(f);
+        c.store(p);
     }
 };
 template <> struct Chunk<float, 8> {
@@ -71,13 +77,22 @@ template <> struct Chunk<float, 8> {
         a = ld16(p);
         b = ld16(p + 4);
     }
+    __device__ __forceinline__ void store(float* p) const {
+        reinterpret_cast<uint4*>(p)[0] = a;
+        reinterpret_cast<uint4*>(p)[1] = b;
+    }
     __device__ __forceinline__ void get(float (&f)[8]) const {
         Vec<float>::unpack(a, f);
         Vec<float>::unpack(b, f + 4);
     }
+    __device__ __forceinline__ void set(const float (&f)[8]) {
+        a = make_uint4(__float_as_uint(f[0]), __float_as_uint(f[1]), __float_as_uint(f[2]), __float_as_uint(f[3]));
+        b = make_uint4(__float_as_uint(f[4]), __float_as_uint(f[5]), __float_as_uint(f[6]), __float_as_uint(f[7]));
+    }
     __device__ __forceinline__ static void put(float* p, const float (&f)[8]) {
-        reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
-        reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+        Chunk c;
+        c.set(f);
+        c.store(p);
     }
 };
 
@@ -168,21 +183,42 @@ template <int E> __device__ __forceinline__ float vsum(const float (&a)[E]) {
     }
 }
 
-__device__ __forceinline__ float warp_sum(float v) {
+// The sums of N (a power of two) values over the threads of a block, in all of them; `red`: 32 N floats, of their own
+// for consecutive calls.  A warp adds N values together: at each of the first steps a lane gives away half of those
+// it still has, so that N values take 4 + N steps or so and not 5 N.
+template <int N>
+__device__ __forceinline__ float scatter_sum(float (&v)[N]) {
+    const int lane = threadIdx.x & 31;
+    int d = 16;
 #pragma unroll
-    for (int d = 16; d; d >>= 1) v += __shfl_xor_sync(~0u, v, d);
-    return v;
+    for (int n = N / 2; n; n /= 2, d /= 2) {
+        const bool up = lane & d;
+#pragma unroll
+        for (int k = 0; k < n; ++k) {
+            const float give = up ? v[k] : v[k + n], keep = up ? v[k + n] : v[k];
+            v[k] = keep + __shfl_xor_sync(~0u, give, d);
+        }
+    }
+    float s = v[0];
+    for (; d; d /= 2) s += __shfl_xor_sync(~0u, s, d);
+    return s;                                              // value k in lanes 32 k / N ..
 }
-
-// The sum over a block's threads, through `red` (16 floats, 16-byte aligned; each call of a row its own).  At most 16 warps;
-// `red` holds zeros for those that there are not.
-__device__ __forceinline__ float row_sum(float v, float* red) {
-    v = warp_sum(v);
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
+template <int N>
+__device__ __forceinline__ void block_sums(float (&v)[N], float* red) {
+    const int lane = threadIdx.x & 31, warps = blockDim.x >> 5;
+    const float s = scatter_sum(v);
+    if ((lane & (32 / N - 1)) == 0) red[(threadIdx.x >> 5) * N + lane / (32 / N)] = s;
     __syncthreads();
-    const float4* q = reinterpret_cast<const float4*>(red);
-    const float4 a = q[0], b = q[1], c = q[2], d = q[3];
-    return ((a.x + a.y) + (a.z + a.w)) + ((b.x + b.y) + (b.z + b.w)) + (((c.x + c.y) + (c.z + c.w)) + ((d.x + d.y) + (d.z + d.w)));
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = lane < warps ? red[lane * N + k] : 0.0f;
+    const float all = scatter_sum(v);
+#pragma unroll
+    for (int k = 0; k < N; ++k) v[k] = __shfl_sync(~0u, all, k * (32 / N));
+}
+__device__ __forceinline__ float row_sum(float v, float* red) {
+    float a[1] = {v};
+    block_sums(a, red);
+    return a[0];
 }
 
 // One chunk's copy to this thread's own place in shared memory.
@@ -219,39 +255,55 @@ struct FwdParams {
     int w_f32;
 };
 
-// One row's arithmetic after the loads: v (h, or x) in, y's values out; mean and rstd.  `here[i]`: whether the thread has
-// chunk i (its v is 0 where not).  Sum: the sum over the row's threads.
-template <int E, int NC, typename Sum>
-__device__ __forceinline__ void norm_row(float (&v)[NC][E], const bool (&here)[NC], const float (&w)[NC][E],
-                                         const float (&b)[NC][E], float inv_cols, float eps, float& mean, float& rstd,
-                                         Sum&& sum) {
-    float s = 0.0f;
+// The arithmetic of RB rows after the loads: v (h, or x) in, y's values out; mean and rstd.  `here[i]`: whether the thread
+// has chunk i (its v is 0 where not).  Sums: RB sums over the rows' threads.
+template <int E, int NC, int RB, typename Sums>
+__device__ __forceinline__ void norm_rows(float (&v)[RB][NC][E], const bool (&here)[NC], const float (&w)[NC][E],
+                                          const float (&b)[NC][E], float inv_cols, float eps, float (&mean)[RB],
+                                          float (&rstd)[RB], Sums&& sums) {
 #pragma unroll
-    for (int i = 0; i < NC; ++i) s += vsum(v[i]);
-    mean = sum(s, 0) * inv_cols;
-    s = 0.0f;
+    for (int k = 0; k < RB; ++k) {
+        mean[k] = 0.0f;
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        float q[E] = {};
-        vadd(v[i], -mean);
-        vfma(q, v[i], v[i], q);
-        s += here[i] ? vsum(q) : 0.0f;
+        for (int i = 0; i < NC; ++i) mean[k] += vsum(v[k][i]);
     }
-    rstd = rsqrtf(sum(s, 1) * inv_cols + eps);
+    sums(mean, 0);
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        vmul(v[i], rstd);
-        vfma(v[i], v[i], w[i], b[i]);
+    for (int k = 0; k < RB; ++k) {
+        mean[k] *= inv_cols;
+        rstd[k] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            float q[E] = {};
+            vadd(v[k][i], -mean[k]);
+            vfma(q, v[k][i], v[k][i], q);
+            rstd[k] += here[i] ? vsum(q) : 0.0f;
+        }
+    }
+    float s[RB];
+#pragma unroll
+    for (int k = 0; k < RB; ++k) s[k] = rstd[k];
+    sums(s, 1);
+#pragma unroll
+    for (int k = 0; k < RB; ++k) {
+        rstd[k] = rsqrtf(s[k] * inv_cols + eps);
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            vmul(v[k][i], rstd[k]);
+            vfma(v[k][i], v[k][i], w[i], b[i]);
+        }
     }
 }
+// h = v + the chunk, rounded to its type, stored and left in v.
 template <typename X, int E>
 __device__ __forceinline__ void add_residual(const Chunk<X, E>& c, float (&v)[E], X* h) {
     float a[E];
     c.get(a);
     vadd(v, a);
-#pragma unroll
-    for (int e = 0; e < E; ++e) v[e] = round_to(v[e], static_cast<const X*>(nullptr));
-    Chunk<X, E>::put(h, v);
+    Chunk<X, E> r;
+    r.set(v);
+    r.store(h);
+    r.get(v);
 }
 // The thread's chunks of weight and bias (zeros without one, and where it has no chunk).
 template <int E, int NC>
@@ -298,65 +350,71 @@ __global__ void __launch_bounds__(128, NC * E > 16 ? 3 : 4) norm_fwd_warp_kernel
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t r = mine + base + u * groups;
-            float v[NC][E] = {}, mean, rstd;
+            float v[1][NC][E] = {}, mean[1], rstd[1];
 #pragma unroll
             for (int i = 0; i < NC; ++i)
                 if (r < p.rows && here[i]) {
-                    in[u][i].get(v[i]);
-                    if (p.residual) add_residual(add[u][i], v[i], static_cast<X*>(p.h) + r * p.ldh + (t + i * G) * E);
+                    in[u][i].get(v[0][i]);
+                    if (p.residual) add_residual(add[u][i], v[0][i], static_cast<X*>(p.h) + r * p.ldh + (t + i * G) * E);
                 }
-            norm_row(v, here, w, b, inv_cols, p.eps, mean, rstd, [&](float s, int) { return group_sum(s, G); });
+            norm_rows(v, here, w, b, inv_cols, p.eps, mean, rstd, [&](float (&s)[1], int) { s[0] = group_sum(s[0], G); });
             if (r < p.rows) {
 #pragma unroll
                 for (int i = 0; i < NC; ++i)
-                    if (here[i]) Chunk<Y, E>::put(static_cast<Y*>(p.y) + r * p.ldy + (t + i * G) * E, v[i]);
+                    if (here[i]) Chunk<Y, E>::put(static_cast<Y*>(p.y) + r * p.ldy + (t + i * G) * E, v[0][i]);
                 if (t == 0) {
-                    p.mean[r] = mean;
-                    p.rstd[r] = rstd;
+                    p.mean[r] = mean[0];
+                    p.rstd[r] = rstd[0];
                 }
             }
         }
     }
 }
 
-// A block per row, S rows of copies: S - 1 ahead.  Shared memory: [S][x, residual][NC][threads] chunks.
-template <typename X, typename Y, int E, int NC, int S, bool RES>
-__global__ void __maxnreg__(96) norm_fwd_kernel(FwdParams p) {
+// What a block of a wide row takes: RB rows at a time with two and fewer registers a thread from 641 threads on.
+template <int RB> struct Wide {
+    static constexpr int kRegs = RB == 2 ? 96 : 64;
+};
+
+// A block per RB rows, S such batches of copies: S - 1 ahead.  Shared memory: [S][RB][x, residual][NC][threads] chunks.
+template <typename X, typename Y, int E, int NC, int RB, int S, bool RES>
+__global__ void __maxnreg__(Wide<RB>::kRegs) norm_fwd_kernel(FwdParams p) {
     pdl_launch_dependents();
     pdl_wait();
     extern __shared__ __align__(16) uint8_t norm_smem[];
-    __shared__ __align__(16) float red[2][16];
+    __shared__ float red[2][32 * RB];
     constexpr int A = RES ? 2 : 1;
     const int t = threadIdx.x, width = blockDim.x;
     Chunk<X, E>* ring = reinterpret_cast<Chunk<X, E>*>(norm_smem) + t;
-    if (t < 32) red[t >> 4][t & 15] = 0.0f;
-    __syncthreads();
+    auto at = [&](int slot, int k, int a, int i) { return ring + (((slot * RB + k) * A + a) * NC + i) * width; };
     const float inv_cols = 1.0f / (float)p.cols;
     bool here[NC];
     float w[NC][E], b[NC][E];
 #pragma unroll
     for (int i = 0; i < NC; ++i) here[i] = t + i * width < (int)(p.cols / E);
     load_affine<E, NC>(p, here, t, width, w, b);
-    // this thread's first chunk of the row to fetch next, and of the row to store next
-    const int64_t stride = gridDim.x, first = blockIdx.x;
+    const int64_t stride = (int64_t)gridDim.x * RB, first = (int64_t)blockIdx.x * RB;
+    // this thread's first chunk of the next batch to fetch, and of the next to store
     const X *x = static_cast<const X*>(p.x) + first * p.ldx + t * E, *res = static_cast<const X*>(p.residual) + first * p.ldr + t * E;
     X* h = static_cast<X*>(p.h) + first * p.ldh + t * E;
     Y* y = static_cast<Y*>(p.y) + first * p.ldy + t * E;
-    const int64_t dx = stride * p.ldx, dres = stride * p.ldr, dh = stride * p.ldh, dy = stride * p.ldy;
+    const int64_t step_x = stride * p.ldx, step_res = stride * p.ldr, step_h = stride * p.ldh, step_y = stride * p.ldy;
     int64_t ahead = first;
     auto fetch = [&](int slot) {
-        if (ahead < p.rows) {
 #pragma unroll
-            for (int i = 0; i < NC; ++i)
-                if (here[i]) {
-                    copy_chunk(ring + ((slot * A) * NC + i) * width, x + i * width * E);
-                    if constexpr (RES) copy_chunk(ring + ((slot * A + 1) * NC + i) * width, res + i * width * E);
-                }
-        }
+        for (int k = 0; k < RB; ++k)
+            if (ahead + k < p.rows) {
+#pragma unroll
+                for (int i = 0; i < NC; ++i)
+                    if (here[i]) {
+                        copy_chunk(at(slot, k, 0, i), x + k * p.ldx + i * width * E);
+                        if constexpr (RES) copy_chunk(at(slot, k, 1, i), res + k * p.ldr + i * width * E);
+                    }
+            }
         copies_commit();
         ahead += stride;
-        x += dx;
-        if constexpr (RES) res += dres;
+        x += step_x;
+        if constexpr (RES) res += step_res;
     };
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) fetch(k);
@@ -364,23 +422,30 @@ __global__ void __maxnreg__(96) norm_fwd_kernel(FwdParams p) {
     for (int64_t r = first; r < p.rows; r += stride) {
         fetch(slot == 0 ? S - 1 : slot - 1);
         copies_wait<S - 1>();
-        float v[NC][E] = {}, mean, rstd;
+        float v[RB][NC][E] = {}, mean[RB], rstd[RB];
 #pragma unroll
-        for (int i = 0; i < NC; ++i)
-            if (here[i]) {
-                ring[((slot * A) * NC + i) * width].get(v[i]);
-                if constexpr (RES) add_residual(ring[((slot * A + 1) * NC + i) * width], v[i], h + i * width * E);
+        for (int k = 0; k < RB; ++k)
+            if (r + k < p.rows)
+#pragma unroll
+                for (int i = 0; i < NC; ++i)
+                    if (here[i]) {
+                        at(slot, k, 0, i)->get(v[k][i]);
+                        if constexpr (RES) add_residual(*at(slot, k, 1, i), v[k][i], h + k * p.ldh + i * width * E);
+                    }
+        norm_rows(v, here, w, b, inv_cols, p.eps, mean, rstd, [&](float (&s)[RB], int k) { block_sums(s, red[k]); });
+#pragma unroll
+        for (int k = 0; k < RB; ++k)
+            if (r + k < p.rows) {
+#pragma unroll
+                for (int i = 0; i < NC; ++i)
+                    if (here[i]) Chunk<Y, E>::put(y + k * p.ldy + i * width * E, v[k][i]);
+                if (t == 0) {
+                    p.mean[r + k] = mean[k];
+                    p.rstd[r + k] = rstd[k];
+                }
             }
-        norm_row(v, here, w, b, inv_cols, p.eps, mean, rstd, [&](float s, int k) { return row_sum(s, red[k]); });
-#pragma unroll
-        for (int i = 0; i < NC; ++i)
-            if (here[i]) Chunk<Y, E>::put(y + i * width * E, v[i]);
-        if (t == 0) {
-            p.mean[r] = mean;
-            p.rstd[r] = rstd;
-        }
-        y += dy;
-        if constexpr (RES) h += dh;
+        y += step_y;
+        if constexpr (RES) h += step_h;
         slot = slot + 1 == S ? 0 : slot + 1;
     }
 }
@@ -394,33 +459,38 @@ struct BwdParams {
     int w_f32, nparts;
 };
 
-// One row of the backward pass after the loads: xhat = x and g = dy come in (0 where the thread has no chunk), dx
-// without dh goes out in g, the column sums grow.  Sums: both over the row's threads.
-template <int E, int NC, typename Sums>
-__device__ __forceinline__ void grad_row(float (&xhat)[NC][E], float (&g)[NC][E], const float (&w)[NC][E],
-                                         float (&sw)[NC][E], float (&sb)[NC][E], float mean, float rstd, float inv_cols,
-                                         Sums&& sums) {
-    float a[E] = {}, b[E] = {};
+// RB rows of the backward pass after the loads: xhat = x and g = dy come in (0 where the thread has no chunk or there is no
+// row), dx without dh goes out in g, the column sums grow.  Sums: 2 RB sums over the rows' threads.
+template <int E, int NC, int RB, typename Sums>
+__device__ __forceinline__ void grad_rows(float (&xhat)[RB][NC][E], float (&g)[RB][NC][E], const float (&w)[NC][E],
+                                          float (&sw)[NC][E], float (&sb)[NC][E], const float (&mean)[RB],
+                                          const float (&rstd)[RB], float inv_cols, Sums&& sums) {
+    float s[2 * RB];
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        vadd(xhat[i], -mean);
-        vmul(xhat[i], rstd);
-        vfma(sw[i], g[i], xhat[i], sw[i]);
-        vadd(sb[i], g[i]);
-        vmul(g[i], w[i]);
-        vadd(a, g[i]);
-        vfma(b, g[i], xhat[i], b);
-    }
-    float s1 = vsum(a), s2 = vsum(b);
-    sums(s1, s2);
-    s1 *= inv_cols;
-    s2 *= inv_cols;
+    for (int k = 0; k < RB; ++k) {
+        float a[E] = {}, b[E] = {};
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-        vfma(g[i], xhat[i], -s2, g[i]);
-        vadd(g[i], -s1);
-        vmul(g[i], rstd);
+        for (int i = 0; i < NC; ++i) {
+            vadd(xhat[k][i], -mean[k]);
+            vmul(xhat[k][i], rstd[k]);
+            vfma(sw[i], g[k][i], xhat[k][i], sw[i]);
+            vadd(sb[i], g[k][i]);
+            vmul(g[k][i], w[i]);
+            vadd(a, g[k][i]);
+            vfma(b, g[k][i], xhat[k][i], b);
+        }
+        s[2 * k] = vsum(a);
+        s[2 * k + 1] = vsum(b);
     }
+    sums(s);
+#pragma unroll
+    for (int k = 0; k < RB; ++k)
+#pragma unroll
+        for (int i = 0; i < NC; ++i) {
+            vfma(g[k][i], xhat[k][i], -s[2 * k + 1] * inv_cols, g[k][i]);
+            vadd(g[k][i], -s[2 * k] * inv_cols);
+            vmul(g[k][i], rstd[k]);
+        }
 }
 
 // Groups of G lanes, U rows of a group at a time.  Column sums of a block: parts[2 block] (dy xhat) and
@@ -459,16 +529,16 @@ __global__ void __launch_bounds__(128, 3) norm_bwd_warp_kernel(BwdParams p, int 
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             const int64_t r = mine + base + u * groups;
-            float xhat[NC][E] = {}, g[NC][E] = {};
+            float xhat[1][NC][E] = {}, g[1][NC][E] = {}, m[1] = {mean[u]}, rs[1] = {rstd[u]};
 #pragma unroll
             for (int i = 0; i < NC; ++i)
                 if (r < p.rows && t + i * G < chunks) {
-                    x[u][i].get(xhat[i]);
-                    dy[u][i].get(g[i]);
+                    x[u][i].get(xhat[0][i]);
+                    dy[u][i].get(g[0][i]);
                 }
-            grad_row(xhat, g, w, sw, sb, mean[u], rstd[u], inv_cols, [&](float& a, float& b) {
-                a = group_sum(a, G);
-                b = group_sum(b, G);
+            grad_rows(xhat, g, w, sw, sb, m, rs, inv_cols, [&](float (&s)[2]) {
+                s[0] = group_sum(s[0], G);
+                s[1] = group_sum(s[1], G);
             });
 #pragma unroll
             for (int i = 0; i < NC; ++i)
@@ -476,10 +546,9 @@ __global__ void __launch_bounds__(128, 3) norm_bwd_warp_kernel(BwdParams p, int 
                     if (p.dh) {
                         float a[E];
                         dh[u][i].get(a);
-#pragma unroll
-                        for (int e = 0; e < E; ++e) g[i][e] += a[e];
+                        vadd(g[0][i], a);
                     }
-                    Chunk<X, E>::put(static_cast<X*>(p.dx) + r * p.lddx + (t + i * G) * E, g[i]);
+                    Chunk<X, E>::put(static_cast<X*>(p.dx) + r * p.lddx + (t + i * G) * E, g[0][i]);
                 }
         }
     }
@@ -513,21 +582,19 @@ __global__ void __launch_bounds__(128, 3) norm_bwd_warp_kernel(BwdParams p, int 
     for (int c = threadIdx.x; c < 2 * (int)p.cols; c += 128) out[c] = sums[c];
 }
 
-// A block per row, S rows of copies.  Shared memory: [S][x, dy, dh][NC][threads] chunks.
-template <typename X, typename Y, int E, int NC, int S, bool RES>
-__global__ void __maxnreg__(96) norm_bwd_kernel(BwdParams p) {
+// A block per RB rows, S such batches of copies.  Shared memory: [S][RB][x, dy, dh][NC][threads] chunks.
+template <typename X, typename Y, int E, int NC, int RB, int S, bool RES>
+__global__ void __maxnreg__(Wide<RB>::kRegs) norm_bwd_kernel(BwdParams p) {
     pdl_launch_dependents();
     pdl_wait();
     extern __shared__ __align__(16) uint8_t norm_smem[];
-    __shared__ __align__(16) float2 red[2][16];            // both sums of a row; two buffers take turns
+    __shared__ float red[2][64 * RB];                      // two buffers take turns
     const int t = threadIdx.x, width = blockDim.x;
-    if (t < 32) red[t >> 4][t & 15] = make_float2(0.0f, 0.0f);
-    __syncthreads();
     const uint32_t xs = NC * width * sizeof(Chunk<X, E>), ys = NC * width * sizeof(Chunk<Y, E>);
-    const uint32_t slot_bytes = xs + ys + (RES ? xs : 0);
-    auto at_x = [&](uint32_t slot, int i) { return reinterpret_cast<Chunk<X, E>*>(norm_smem + slot) + i * width + t; };
-    auto at_dy = [&](uint32_t slot, int i) { return reinterpret_cast<Chunk<Y, E>*>(norm_smem + slot + xs) + i * width + t; };
-    auto at_dh = [&](uint32_t slot, int i) { return reinterpret_cast<Chunk<X, E>*>(norm_smem + slot + xs + ys) + i * width + t; };
+    const uint32_t row_bytes = xs + ys + (RES ? xs : 0), slot_bytes = RB * row_bytes;
+    auto at_x = [&](uint32_t row, int i) { return reinterpret_cast<Chunk<X, E>*>(norm_smem + row) + i * width + t; };
+    auto at_dy = [&](uint32_t row, int i) { return reinterpret_cast<Chunk<Y, E>*>(norm_smem + row + xs) + i * width + t; };
+    auto at_dh = [&](uint32_t row, int i) { return reinterpret_cast<Chunk<X, E>*>(norm_smem + row + xs + ys) + i * width + t; };
     const float inv_cols = 1.0f / (float)p.cols;
     bool here[NC];
     float w[NC][E] = {}, sw[NC][E] = {}, sb[NC][E] = {};
@@ -536,78 +603,76 @@ __global__ void __maxnreg__(96) norm_bwd_kernel(BwdParams p) {
         here[i] = t + i * width < (int)(p.cols / E);
         if (here[i]) load_vec<E>(p.weight, p.w_f32, (t + i * width) * E, w[i]);
     }
-    const int64_t first = blockIdx.x, stride = gridDim.x;
+    const int64_t first = (int64_t)blockIdx.x * RB, stride = (int64_t)gridDim.x * RB;
     const X *x = static_cast<const X*>(p.x) + first * p.ldx + t * E, *dh = static_cast<const X*>(p.dh) + first * p.lddh + t * E;
     const Y* dy = static_cast<const Y*>(p.dy) + first * p.lddy + t * E;
     X* dx = static_cast<X*>(p.dx) + first * p.lddx + t * E;
+    const int64_t step_x = stride * p.ldx, step_dh = stride * p.lddh, step_dy = stride * p.lddy, step_dx = stride * p.lddx;
     int64_t ahead = first;
     auto fetch = [&](uint32_t slot) {
-        if (ahead < p.rows) {
 #pragma unroll
-            for (int i = 0; i < NC; ++i)
-                if (here[i]) {
-                    copy_chunk(at_x(slot, i), x + i * width * E);
-                    copy_chunk(at_dy(slot, i), dy + i * width * E);
-                    if constexpr (RES) copy_chunk(at_dh(slot, i), dh + i * width * E);
-                }
-        }
+        for (int k = 0; k < RB; ++k)
+            if (ahead + k < p.rows) {
+#pragma unroll
+                for (int i = 0; i < NC; ++i)
+                    if (here[i]) {
+                        copy_chunk(at_x(slot + k * row_bytes, i), x + k * p.ldx + i * width * E);
+                        copy_chunk(at_dy(slot + k * row_bytes, i), dy + k * p.lddy + i * width * E);
+                        if constexpr (RES) copy_chunk(at_dh(slot + k * row_bytes, i), dh + k * p.lddh + i * width * E);
+                    }
+            }
         copies_commit();
         ahead += stride;
-        x += stride * p.ldx;
-        dy += stride * p.lddy;
-        if constexpr (RES) dh += stride * p.lddh;
+        x += step_x;
+        dy += step_dy;
+        if constexpr (RES) dh += step_dh;
     };
 #pragma unroll
     for (int k = 0; k < S - 1; ++k) fetch(k * slot_bytes);
-    float mean = 0.0f, rstd = 0.0f;
-    if (first < p.rows) {
-        mean = p.mean[first];
-        rstd = p.rstd[first];
-    }
+    float mean[RB] = {}, rstd[RB] = {};
+    auto stats = [&](int64_t r) {
+#pragma unroll
+        for (int k = 0; k < RB; ++k)
+            if (r + k < p.rows) {
+                mean[k] = p.mean[r + k];
+                rstd[k] = p.rstd[r + k];
+            }
+    };
+    stats(first);
     uint32_t slot = 0;
     int buf = 0;
     for (int64_t r = first; r < p.rows; r += stride, buf ^= 1) {
         fetch(slot == 0 ? (S - 1) * slot_bytes : slot - slot_bytes);
         copies_wait<S - 1>();
-        const float m = mean, rs = rstd;
-        if (r + stride < p.rows) {
-            mean = p.mean[r + stride];
-            rstd = p.rstd[r + stride];
+        float m[RB], rs[RB], xhat[RB][NC][E] = {}, g[RB][NC][E] = {};
+#pragma unroll
+        for (int k = 0; k < RB; ++k) {
+            m[k] = mean[k];
+            rs[k] = rstd[k];
+            if (r + k < p.rows)
+#pragma unroll
+                for (int i = 0; i < NC; ++i)
+                    if (here[i]) {
+                        at_x(slot + k * row_bytes, i)->get(xhat[k][i]);
+                        at_dy(slot + k * row_bytes, i)->get(g[k][i]);
+                    }
         }
-        float xhat[NC][E] = {}, g[NC][E] = {};
+        stats(r + stride);
+        grad_rows(xhat, g, w, sw, sb, m, rs, inv_cols, [&](float (&s)[2 * RB]) { block_sums(s, red[buf]); });
 #pragma unroll
-        for (int i = 0; i < NC; ++i)
-            if (here[i]) {
-                at_x(slot, i)->get(xhat[i]);
-                at_dy(slot, i)->get(g[i]);
-            }
-        grad_row(xhat, g, w, sw, sb, m, rs, inv_cols, [&](float& a, float& b) {
-            a = warp_sum(a);
-            b = warp_sum(b);
-            if ((t & 31) == 0) red[buf][t >> 5] = make_float2(a, b);
-            __syncthreads();
-            const float4* q = reinterpret_cast<const float4*>(red[buf]);
-            float2 s[4] = {};
+        for (int k = 0; k < RB; ++k)
+            if (r + k < p.rows)
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-                const float4 v = q[k];
-                s[k & 3] = __fadd2_rn(s[k & 3], __fadd2_rn(make_float2(v.x, v.y), make_float2(v.z, v.w)));
-            }
-            s[0] = __fadd2_rn(__fadd2_rn(s[0], s[1]), __fadd2_rn(s[2], s[3]));
-            a = s[0].x;
-            b = s[0].y;
-        });
-#pragma unroll
-        for (int i = 0; i < NC; ++i)
-            if (here[i]) {
-                if constexpr (RES) {
-                    float a[E];
-                    at_dh(slot, i)->get(a);
-                    vadd(g[i], a);
-                }
-                Chunk<X, E>::put(dx + i * width * E, g[i]);
-            }
-        dx += stride * p.lddx;
+                for (int i = 0; i < NC; ++i)
+                    if (here[i]) {
+                        if constexpr (RES) {
+                            float a[E];
+                            at_dh(slot + k * row_bytes, i)->get(a);
+                            vadd(g[k][i], a);
+                        }
+                        Chunk<X, E>::put(dx + k * p.lddx + i * width * E, g[k][i]);
+                    }
+        dx += step_dx;
         slot = slot + slot_bytes == S * slot_bytes ? 0 : slot + slot_bytes;
     }
     float *pw = p.parts + 2 * (int64_t)blockIdx.x * p.cols + t * E, *pb = pw + p.cols;
@@ -619,31 +684,31 @@ __global__ void __maxnreg__(96) norm_bwd_kernel(BwdParams p) {
         }
 }
 
-// dweight and dbias from the parts: a block takes 32 of the 2 cols columns, its warps every eighth part.
-__global__ void __launch_bounds__(256) norm_bwd_join_kernel(BwdParams p) {
+// dweight and dbias from the parts: a block takes 32 of the 2 cols columns (a part's two rows follow one another), its 16
+// warps every sixteenth part, ten loads at a time.
+constexpr int kJoinThreads = 512;
+__global__ void __launch_bounds__(kJoinThreads) norm_bwd_join_kernel(BwdParams p) {
     pdl_launch_dependents();
     pdl_wait();
-    __shared__ float red[8][33];
+    __shared__ float red[16][33];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int64_t c = blockIdx.x * 32ll + lane;
+    const int64_t c = blockIdx.x * 32ll + lane, part = 2 * p.cols;
     float s = 0.0f;
-    if (c < 2 * p.cols) {
-        // a part's two rows follow one another: column c of 2 cols
-        const float* q = p.parts + c;
-        int i = warp;
-        for (; i + 24 < p.nparts; i += 32) {
-            const float a = q[2 * (int64_t)i * p.cols], b = q[2 * (int64_t)(i + 8) * p.cols];
-            const float d = q[2 * (int64_t)(i + 16) * p.cols], e = q[2 * (int64_t)(i + 24) * p.cols];
-            s += (a + b) + (d + e);
+    if (c < part) {
+        for (int i = warp; i < p.nparts; i += 160) {
+            float v[10];
+#pragma unroll
+            for (int k = 0; k < 10; ++k) v[k] = i + 16 * k < p.nparts ? p.parts[(int64_t)(i + 16 * k) * part + c] : 0.0f;
+#pragma unroll
+            for (int k = 0; k < 10; ++k) s += v[k];
         }
-        for (; i < p.nparts; i += 8) s += q[2 * (int64_t)i * p.cols];
     }
     red[warp][lane] = s;
     __syncthreads();
-    if (warp == 0 && c < 2 * p.cols) {
+    if (warp == 0 && c < part) {
         s = 0.0f;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) s += red[k][lane];
+        for (int k = 0; k < 16; ++k) s += red[k][lane];
         if (c < p.cols) p.dweight[c] = s;
         else if (p.dbias) p.dbias[c - p.cols] = s;
     }
@@ -656,7 +721,7 @@ template <typename X, typename Y, int E>
 __global__ void __launch_bounds__(kLoopThreads) norm_fwd_loop_kernel(FwdParams p) {
     pdl_launch_dependents();
     pdl_wait();
-    __shared__ __align__(16) float red[2][16];             // kLoopThreads has all 16 warps
+    __shared__ float red[2][32];
     const float inv_cols = 1.0f / (float)p.cols;
     for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
         const X* x = static_cast<const X*>(p.x) + r * p.ldx;
@@ -742,7 +807,7 @@ template <typename X, typename Y, int E>
 __global__ void __launch_bounds__(kLoopThreads) norm_bwd_rows_loop_kernel(BwdParams p) {
     pdl_launch_dependents();
     pdl_wait();
-    __shared__ __align__(16) float red[2][16];             // kLoopThreads has all 16 warps
+    __shared__ float red[2][32];
     const float inv_cols = 1.0f / (float)p.cols;
     for (int64_t r = blockIdx.x; r < p.rows; r += gridDim.x) {
         const X* x = static_cast<const X*>(p.x) + r * p.ldx;
@@ -788,6 +853,7 @@ __global__ void __launch_bounds__(kLoopThreads) norm_bwd_rows_loop_kernel(BwdPar
 
 // ---- host
 template <typename T> struct Tag { using type = T; };
+template <int N> struct Int { static constexpr int value = N; };
 template <typename F>
 nvfp4_status with_types(int32_t x, int32_t y, F&& f) {
     auto on_y = [&](auto tx) { return y == NVFP4_F32 ? f(tx, Tag<float>{}) : f(tx, Tag<bf16>{}); };
@@ -801,9 +867,9 @@ nvfp4_status to_status(cudaError_t e) { return e == cudaSuccess ? NVFP4_OK : NVF
 // Rows (base and pitch in elements) that can be read 8 elements at a time.
 bool rows16(const void* p, int64_t ld) { return !p || (aligned16(p) && ld % 8 == 0); }
 
-constexpr int kBlock = 512;                    // the most threads of a row
 constexpr int kNarrow = 128;                   // threads of a block of narrow rows
-constexpr int kRingBytes = 100 * 1024;         // shared memory of a block's copies: two blocks on an SM
+constexpr int kRingBytes = 200 * 1024;         // shared memory of an SM for copies
+constexpr int kTwoRows = 640;                  // the most threads that take two rows at a time (96 registers each)
 
 int sms() {
     int dev = 0;
@@ -816,9 +882,25 @@ int group_lanes(int64_t chunks) {
     while (g < 32 && g < chunks) g *= 2;
     return g;
 }
-// Blocks of a persistent grid: as many as run at once, by registers (96 a thread) and shared memory.
-int64_t resident_blocks(int threads, size_t smem) {
-    return sms() * std::max<int64_t>(1, std::min<int64_t>(65536 / (96 * threads), 224 * 1024 / (smem + 1024)));
+// A launch of a wide kernel: `rb` rows at a time where a block's registers allow it and there are rows enough to go
+// round, `stages` batches of copies (as many as let the blocks that the registers allow run at once), the
+// persistent grid.
+struct WidePlan {
+    int threads, rb, stages;
+    size_t smem;
+    int64_t grid;
+};
+WidePlan wide_plan(int64_t rows, int64_t chunks, int nc, size_t row_bytes_of_thread, int most_stages) {
+    WidePlan w;
+    w.threads = block_threads(chunks, nc);
+    w.rb = nc == 1 && w.threads <= kTwoRows && rows > sms() && 4 * w.threads * row_bytes_of_thread <= 216 * 1024 ? 2 : 1;
+    const int regs = w.rb == 2 ? 96 : 64;
+    const int64_t blocks = std::max(1, std::min(65536 / (regs * w.threads), 1536 / w.threads));
+    const size_t slot = (size_t)w.threads * w.rb * row_bytes_of_thread;
+    w.stages = most_stages * slot * blocks <= kRingBytes ? most_stages : 2;
+    w.smem = w.stages * slot;
+    w.grid = std::min<int64_t>((rows + w.rb - 1) / w.rb, sms() * std::max<int64_t>(1, std::min<int64_t>(blocks, 224 * 1024 / (w.smem + 2048))));
+    return w;
 }
 template <typename Kernel, typename P>
 cudaError_t launch_ring(Kernel kern, int64_t grid, int threads, size_t smem, cudaStream_t s, const P& p) {
@@ -829,30 +911,27 @@ cudaError_t launch_ring(Kernel kern, int64_t grid, int threads, size_t smem, cud
 // How the backward pass cuts the rows.  Rows wider than its registers reach go through the loops.
 struct BwdPlan {
     enum { kWarp, kBlock, kLoop } kind;
-    int threads, stages, parts;
-    size_t smem;
+    int parts;
+    WidePlan w;
 };
 BwdPlan bwd_plan(int64_t rows, int64_t cols, bool vec, size_t row_elem_bytes) {
     const int64_t chunks = vec ? cols / 8 : cols;
-    const int nc = vec ? 2 : 8;
+    const int nc = vec ? 1 : 8;
     BwdPlan b = {};
     int64_t parts;
-    if (chunks <= 32 * nc) {
+    if (chunks <= (vec ? 64 : 256)) {
         const int g = group_lanes(chunks);
         b.kind = BwdPlan::kWarp;
-        b.threads = kNarrow;
-        b.smem = 2 * (size_t)cols * sizeof(float);
+        b.w.threads = kNarrow;
+        b.w.smem = 2 * (size_t)cols * sizeof(float);
         parts = std::min<int64_t>((rows + kNarrow / g - 1) / (kNarrow / g), sms() * 4ll);
-    } else if (chunks <= kBlock * nc) {
+    } else if (chunks <= 1024 * nc) {
         b.kind = BwdPlan::kBlock;
-        b.threads = block_threads(chunks, nc);
-        const size_t slot = (size_t)b.threads * nc * (vec ? 8 : 1) * row_elem_bytes;
-        b.stages = 3 * slot <= kRingBytes ? 3 : 2;
-        b.smem = b.stages * slot;
-        parts = std::min<int64_t>(rows, resident_blocks(b.threads, b.smem));
+        b.w = wide_plan(rows, chunks, nc, nc * (vec ? 8 : 1) * row_elem_bytes, 3);
+        parts = b.w.grid;
     } else {
         b.kind = BwdPlan::kLoop;
-        b.threads = kLoopThreads;
+        b.w.threads = kLoopThreads;
         parts = std::min<int64_t>(64, rows / 16);
     }
     b.parts = (int)std::max<int64_t>(1, parts);
@@ -892,27 +971,29 @@ extern "C" nvfp4_status nvfp4_layer_norm_forward(const void* x, int32_t x_dtype,
             const int64_t grid = std::min<int64_t>((rows + kNarrow / g - 1) / (kNarrow / g), sms() * 16ll);
             return to_status(launch_pdl(kern, dim3((unsigned)grid), dim3(kNarrow), 0, s, p, g));
         };
-        auto wide = [&](auto plain4, auto plain2, auto res4, auto res2, int nc, int e) {
-            const int threads = block_threads(chunks, nc);
-            const size_t slot = (size_t)threads * nc * e * sizeof(X) * (residual ? 2 : 1);
-            const int stages = 4 * slot <= kRingBytes ? 4 : 2;
-            const int64_t grid = std::min<int64_t>(rows, resident_blocks(threads, stages * slot));
-            return to_status(launch_ring(residual ? (stages == 4 ? res4 : res2) : (stages == 4 ? plain4 : plain2), grid, threads,
-                                         stages * slot, s, p));
+        // stages 4 or 2, with or without residual, for one shape of a thread's part
+        auto wide = [&](auto e, auto nc, auto rb, const WidePlan& w) {
+            constexpr int E = decltype(e)::value, NC = decltype(nc)::value, RB = decltype(rb)::value;
+            auto kern = residual ? (w.stages == 4 ? norm_fwd_kernel<X, Y, E, NC, RB, 4, true> : norm_fwd_kernel<X, Y, E, NC, RB, 2, true>)
+                                 : (w.stages == 4 ? norm_fwd_kernel<X, Y, E, NC, RB, 4, false> : norm_fwd_kernel<X, Y, E, NC, RB, 2, false>);
+            return to_status(launch_ring(kern, w.grid, w.threads, w.smem, s, p));
         };
+        const size_t elem = sizeof(X) * (residual ? 2 : 1);
         if (vec) {
             if (chunks <= 32) return narrow(norm_fwd_warp_kernel<X, Y, 8, 1, 4>);
             if (chunks <= 64) return narrow(norm_fwd_warp_kernel<X, Y, 8, 2, 2>);
-            if (chunks <= 128) return narrow(norm_fwd_warp_kernel<X, Y, 8, 4, 1>);
-            if (chunks <= kBlock * 2) return wide(norm_fwd_kernel<X, Y, 8, 2, 4, false>, norm_fwd_kernel<X, Y, 8, 2, 2, false>, norm_fwd_kernel<X, Y, 8, 2, 4, true>, norm_fwd_kernel<X, Y, 8, 2, 2, true>, 2, 8);
-            // 16384 fp32 columns with a residual: two rows of copies do not fit
-            if (chunks <= kBlock * 4 && 2 * cols * sizeof(X) * (residual ? 2 : 1) <= 216 * 1024)
-                return wide(norm_fwd_kernel<X, Y, 8, 4, 4, false>, norm_fwd_kernel<X, Y, 8, 4, 2, false>, norm_fwd_kernel<X, Y, 8, 4, 4, true>, norm_fwd_kernel<X, Y, 8, 4, 2, true>, 4, 8);
+            if (chunks <= 1024) {
+                const WidePlan w = wide_plan(rows, chunks, 1, 8 * elem, 4);
+                return w.rb == 2 ? wide(Int<8>{}, Int<1>{}, Int<2>{}, w) : wide(Int<8>{}, Int<1>{}, Int<1>{}, w);
+            }
+            // two rows of 16384 fp32 columns with a residual do not fit shared memory
+            if (chunks <= 2048 && 2 * cols * elem <= 216 * 1024)
+                return wide(Int<8>{}, Int<2>{}, Int<1>{}, wide_plan(rows, chunks, 2, 16 * elem, 4));
             return to_status(launch_pdl(norm_fwd_loop_kernel<X, Y, 8>, dim3((unsigned)std::min<int64_t>(rows, 1 << 30)),
                                         dim3(kLoopThreads), 0, s, p));
         }
         if (chunks <= 32 * 8) return narrow(norm_fwd_warp_kernel<X, Y, 1, 8, 2>);
-        if (chunks <= kBlock * 8) return wide(norm_fwd_kernel<X, Y, 1, 8, 4, false>, norm_fwd_kernel<X, Y, 1, 8, 2, false>, norm_fwd_kernel<X, Y, 1, 8, 4, true>, norm_fwd_kernel<X, Y, 1, 8, 2, true>, 8, 1);
+        if (chunks <= 1024 * 8) return wide(Int<1>{}, Int<8>{}, Int<1>{}, wide_plan(rows, chunks, 8, 8 * elem, 4));
         return to_status(launch_pdl(norm_fwd_loop_kernel<X, Y, 1>, dim3((unsigned)std::min<int64_t>(rows, 1 << 30)),
                                     dim3(kLoopThreads), 0, s, p));
     });
@@ -955,21 +1036,22 @@ extern "C" nvfp4_status nvfp4_layer_norm_backward(const void* dy, int32_t y_dtyp
         using X = typename decltype(tx)::type;
         using Y = typename decltype(ty)::type;
         cudaError_t e;
-        const dim3 grid(plan.parts), block(plan.threads);
+        const dim3 grid(plan.parts), block(plan.w.threads);
         if (plan.kind == BwdPlan::kWarp) {
             const int g = group_lanes(vec ? cols / 8 : cols);
-            if (!vec) e = launch_pdl(norm_bwd_warp_kernel<X, Y, 1, 8, 1>, grid, block, plan.smem, s, p, g);
-            else if (cols <= 256) e = launch_pdl(norm_bwd_warp_kernel<X, Y, 8, 1, 2>, grid, block, plan.smem, s, p, g);
-            else e = launch_pdl(norm_bwd_warp_kernel<X, Y, 8, 2, 1>, grid, block, plan.smem, s, p, g);
+            if (!vec) e = launch_pdl(norm_bwd_warp_kernel<X, Y, 1, 8, 1>, grid, block, plan.w.smem, s, p, g);
+            else if (cols <= 256) e = launch_pdl(norm_bwd_warp_kernel<X, Y, 8, 1, 2>, grid, block, plan.w.smem, s, p, g);
+            else e = launch_pdl(norm_bwd_warp_kernel<X, Y, 8, 2, 1>, grid, block, plan.w.smem, s, p, g);
         } else if (plan.kind == BwdPlan::kBlock) {
-            auto wide = [&](auto plain3, auto plain2, auto res3, auto res2) {
-                e = launch_ring(dh ? (plan.stages == 3 ? res3 : res2) : (plan.stages == 3 ? plain3 : plain2), plan.parts,
-                                plan.threads, plan.smem, s, p);
+            auto wide = [&](auto ee, auto nc, auto rb) {
+                constexpr int E = decltype(ee)::value, NC = decltype(nc)::value, RB = decltype(rb)::value;
+                auto kern = dh ? (plan.w.stages == 3 ? norm_bwd_kernel<X, Y, E, NC, RB, 3, true> : norm_bwd_kernel<X, Y, E, NC, RB, 2, true>)
+                               : (plan.w.stages == 3 ? norm_bwd_kernel<X, Y, E, NC, RB, 3, false> : norm_bwd_kernel<X, Y, E, NC, RB, 2, false>);
+                e = launch_ring(kern, plan.parts, plan.w.threads, plan.w.smem, s, p);
             };
-            if (vec) wide(norm_bwd_kernel<X, Y, 8, 2, 3, false>, norm_bwd_kernel<X, Y, 8, 2, 2, false>,
-                          norm_bwd_kernel<X, Y, 8, 2, 3, true>, norm_bwd_kernel<X, Y, 8, 2, 2, true>);
-            else wide(norm_bwd_kernel<X, Y, 1, 8, 3, false>, norm_bwd_kernel<X, Y, 1, 8, 2, false>,
-                      norm_bwd_kernel<X, Y, 1, 8, 3, true>, norm_bwd_kernel<X, Y, 1, 8, 2, true>);
+            if (!vec) wide(Int<1>{}, Int<8>{}, Int<1>{});
+            else if (plan.w.rb == 2) wide(Int<8>{}, Int<1>{}, Int<2>{});
+            else wide(Int<8>{}, Int<1>{}, Int<1>{});
         } else {
             auto loops = [&](auto cols_kern, auto rows_kern, int per) {
                 const dim3 cut((unsigned)((cols / per + kLoopThreads - 1) / kLoopThreads), plan.parts);
@@ -981,7 +1063,7 @@ extern "C" nvfp4_status nvfp4_layer_norm_backward(const void* dy, int32_t y_dtyp
             else loops(norm_bwd_cols_loop_kernel<X, Y, 1>, norm_bwd_rows_loop_kernel<X, Y, 1>, 1);
         }
         if (e == cudaSuccess)
-            e = launch_pdl(norm_bwd_join_kernel, dim3((unsigned)((2 * cols + 31) / 32)), dim3(256), 0, s, p);
+            e = launch_pdl(norm_bwd_join_kernel, dim3((unsigned)((2 * cols + 31) / 32)), dim3(kJoinThreads), 0, s, p);
         return to_status(e);
     });
 }
