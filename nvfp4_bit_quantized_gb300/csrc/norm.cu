@@ -257,10 +257,9 @@ struct FwdParams {
 
 // The arithmetic of RB rows after the loads: v (h, or x) in, y's values out; mean and rstd.  `here[i]`: whether the thread
 // has chunk i (its v is 0 where not).  Sums: RB sums over the rows' threads.
-template <int E, int NC, int RB, typename Sums>
-__device__ __forceinline__ void norm_rows(float (&v)[RB][NC][E], const bool (&here)[NC], const float (&w)[NC][E],
-                                          const float (&b)[NC][E], float inv_cols, float eps, float (&mean)[RB],
-                                          float (&rstd)[RB], Sums&& sums) {
+template <int E, int NC, int RB, typename Affine, typename Sums>
+__device__ __forceinline__ void norm_rows(float (&v)[RB][NC][E], const bool (&here)[NC], Affine&& affine, float inv_cols,
+                                          float eps, float (&mean)[RB], float (&rstd)[RB], Sums&& sums) {
 #pragma unroll
     for (int k = 0; k < RB; ++k) {
         mean[k] = 0.0f;
@@ -285,12 +284,15 @@ __device__ __forceinline__ void norm_rows(float (&v)[RB][NC][E], const bool (&he
     for (int k = 0; k < RB; ++k) s[k] = rstd[k];
     sums(s, 1);
 #pragma unroll
-    for (int k = 0; k < RB; ++k) {
-        rstd[k] = rsqrtf(s[k] * inv_cols + eps);
+    for (int k = 0; k < RB; ++k) rstd[k] = rsqrtf(s[k] * inv_cols + eps);
 #pragma unroll
-        for (int i = 0; i < NC; ++i) {
+    for (int i = 0; i < NC; ++i) {
+        float w[E], b[E];
+        affine(i, w, b);
+#pragma unroll
+        for (int k = 0; k < RB; ++k) {
             vmul(v[k][i], rstd[k]);
-            vfma(v[k][i], v[k][i], w[i], b[i]);
+            vfma(v[k][i], v[k][i], w, b);
         }
     }
 }
@@ -305,18 +307,14 @@ __device__ __forceinline__ void add_residual(const Chunk<X, E>& c, float (&v)[E]
     r.store(h);
     r.get(v);
 }
-// The thread's chunks of weight and bias (zeros without one, and where it has no chunk).
-template <int E, int NC>
-__device__ __forceinline__ void load_affine(const FwdParams& p, const bool (&here)[NC], int t, int width, float (&w)[NC][E],
-                                            float (&b)[NC][E]) {
+// A chunk of weight and bias (zeros without one, and where the thread has no chunk).
+template <int E>
+__device__ __forceinline__ void load_affine(const FwdParams& p, bool here, int64_t at, float (&w)[E], float (&b)[E]) {
 #pragma unroll
-    for (int i = 0; i < NC; ++i) {
-#pragma unroll
-        for (int e = 0; e < E; ++e) w[i][e] = b[i][e] = 0.0f;
-        if (here[i]) {
-            load_vec<E>(p.weight, p.w_f32, (t + i * width) * E, w[i]);
-            if (p.bias) load_vec<E>(p.bias, p.w_f32, (t + i * width) * E, b[i]);
-        }
+    for (int e = 0; e < E; ++e) w[e] = b[e] = 0.0f;
+    if (here) {
+        load_vec<E>(p.weight, p.w_f32, at, w);
+        if (p.bias) load_vec<E>(p.bias, p.w_f32, at, b);
     }
 }
 
@@ -331,8 +329,17 @@ __global__ void __launch_bounds__(128, NC * E > 16 ? 3 : 4) norm_fwd_warp_kernel
     bool here[NC];
     float w[NC][E], b[NC][E];
 #pragma unroll
-    for (int i = 0; i < NC; ++i) here[i] = t + i * G < chunks;
-    load_affine<E, NC>(p, here, t, G, w, b);
+    for (int i = 0; i < NC; ++i) {
+        here[i] = t + i * G < chunks;
+        load_affine<E>(p, here[i], (t + i * G) * E, w[i], b[i]);
+    }
+    auto affine = [&](int i, float (&wi)[E], float (&bi)[E]) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+            wi[e] = w[i][e];
+            bi[e] = b[i][e];
+        }
+    };
     // whole warps stay together (the sums are shuffles): the loop's bounds are the warp's first group's
     const int64_t mine = blockIdx.x * (int64_t)(128 / G) + threadIdx.x / G, lead = mine - (threadIdx.x & 31) / G;
     for (int64_t base = 0; lead + base < p.rows; base += U * groups) {
@@ -357,7 +364,7 @@ __global__ void __launch_bounds__(128, NC * E > 16 ? 3 : 4) norm_fwd_warp_kernel
                     in[u][i].get(v[0][i]);
                     if (p.residual) add_residual(add[u][i], v[0][i], static_cast<X*>(p.h) + r * p.ldh + (t + i * G) * E);
                 }
-            norm_rows(v, here, w, b, inv_cols, p.eps, mean, rstd, [&](float (&s)[1], int) { s[0] = group_sum(s[0], G); });
+            norm_rows(v, here, affine, inv_cols, p.eps, mean, rstd, [&](float (&s)[1], int) { s[0] = group_sum(s[0], G); });
             if (r < p.rows) {
 #pragma unroll
                 for (int i = 0; i < NC; ++i)
@@ -371,14 +378,15 @@ __global__ void __launch_bounds__(128, NC * E > 16 ? 3 : 4) norm_fwd_warp_kernel
     }
 }
 
-// What a block of a wide row takes: RB rows at a time with two and fewer registers a thread from 641 threads on.
-template <int RB> struct Wide {
-    static constexpr int kRegs = RB == 2 ? 96 : 64;
-};
+// Registers of a thread of the wide kernels.  Two rows at a time with a residual, forward: 48, with weight and bias read
+// for each batch, so that two blocks of 640 threads share an SM (8192 x 5120, fp32 x: 89 us, 101 us with 96 and one block).
+// Without a residual, and backward with its column sums, 96 with weight and bias kept (bf16: 38 us, 42 us with 48).
+// Blocks of more threads take one row at a time.
+constexpr int kFewRegs = 48, kRegs = 96, kManyThreadsRegs = 64;
 
 // A block per RB rows, S such batches of copies: S - 1 ahead.  Shared memory: [S][RB][x, residual][NC][threads] chunks.
 template <typename X, typename Y, int E, int NC, int RB, int S, bool RES>
-__global__ void __maxnreg__(Wide<RB>::kRegs) norm_fwd_kernel(FwdParams p) {
+__global__ void __maxnreg__(RB == 1 ? kManyThreadsRegs : RES ? kFewRegs : kRegs) norm_fwd_kernel(FwdParams p) {
     pdl_launch_dependents();
     pdl_wait();
     extern __shared__ __align__(16) uint8_t norm_smem[];
@@ -388,11 +396,25 @@ __global__ void __maxnreg__(Wide<RB>::kRegs) norm_fwd_kernel(FwdParams p) {
     Chunk<X, E>* ring = reinterpret_cast<Chunk<X, E>*>(norm_smem) + t;
     auto at = [&](int slot, int k, int a, int i) { return ring + (((slot * RB + k) * A + a) * NC + i) * width; };
     const float inv_cols = 1.0f / (float)p.cols;
+    constexpr bool KEEP = !(RB == 2 && RES);               // weight and bias stay in registers
     bool here[NC];
-    float w[NC][E], b[NC][E];
+    float wk[KEEP ? NC : 1][E], bk[KEEP ? NC : 1][E];
 #pragma unroll
-    for (int i = 0; i < NC; ++i) here[i] = t + i * width < (int)(p.cols / E);
-    load_affine<E, NC>(p, here, t, width, w, b);
+    for (int i = 0; i < NC; ++i) {
+        here[i] = t + i * width < (int)(p.cols / E);
+        if constexpr (KEEP) load_affine<E>(p, here[i], (t + i * width) * E, wk[i], bk[i]);
+    }
+    auto affine = [&](int i, float (&w)[E], float (&b)[E]) {
+        if constexpr (KEEP) {
+#pragma unroll
+            for (int e = 0; e < E; ++e) {
+                w[e] = wk[i][e];
+                b[e] = bk[i][e];
+            }
+        } else {
+            load_affine<E>(p, here[i], (t + i * width) * E, w, b);
+        }
+    };
     const int64_t stride = (int64_t)gridDim.x * RB, first = (int64_t)blockIdx.x * RB;
     // this thread's first chunk of the next batch to fetch, and of the next to store
     const X *x = static_cast<const X*>(p.x) + first * p.ldx + t * E, *res = static_cast<const X*>(p.residual) + first * p.ldr + t * E;
@@ -432,7 +454,7 @@ __global__ void __maxnreg__(Wide<RB>::kRegs) norm_fwd_kernel(FwdParams p) {
                         at(slot, k, 0, i)->get(v[k][i]);
                         if constexpr (RES) add_residual(*at(slot, k, 1, i), v[k][i], h + k * p.ldh + i * width * E);
                     }
-        norm_rows(v, here, w, b, inv_cols, p.eps, mean, rstd, [&](float (&s)[RB], int k) { block_sums(s, red[k]); });
+        norm_rows(v, here, affine, inv_cols, p.eps, mean, rstd, [&](float (&s)[RB], int k) { block_sums(s, red[k]); });
 #pragma unroll
         for (int k = 0; k < RB; ++k)
             if (r + k < p.rows) {
@@ -584,7 +606,7 @@ __global__ void __launch_bounds__(128, 3) norm_bwd_warp_kernel(BwdParams p, int 
 
 // A block per RB rows, S such batches of copies.  Shared memory: [S][RB][x, dy, dh][NC][threads] chunks.
 template <typename X, typename Y, int E, int NC, int RB, int S, bool RES>
-__global__ void __maxnreg__(Wide<RB>::kRegs) norm_bwd_kernel(BwdParams p) {
+__global__ void __maxnreg__(RB == 1 ? kManyThreadsRegs : kRegs) norm_bwd_kernel(BwdParams p) {
     pdl_launch_dependents();
     pdl_wait();
     extern __shared__ __align__(16) uint8_t norm_smem[];
@@ -890,12 +912,12 @@ struct WidePlan {
     size_t smem;
     int64_t grid;
 };
-WidePlan wide_plan(int64_t rows, int64_t chunks, int nc, size_t row_bytes_of_thread, int most_stages) {
+WidePlan wide_plan(int64_t rows, int64_t chunks, int nc, size_t row_bytes_of_thread, int most_stages, int two_row_regs) {
     WidePlan w;
     w.threads = block_threads(chunks, nc);
     w.rb = nc == 1 && w.threads <= kTwoRows && rows > sms() && 4 * w.threads * row_bytes_of_thread <= 216 * 1024 ? 2 : 1;
-    const int regs = w.rb == 2 ? 96 : 64;
-    const int64_t blocks = std::max(1, std::min(65536 / (regs * w.threads), 1536 / w.threads));
+    const int regs = w.rb == 2 ? two_row_regs : kManyThreadsRegs;
+    const int64_t blocks = std::max(1, std::min(65536 / (regs * w.threads), 2048 / w.threads));
     const size_t slot = (size_t)w.threads * w.rb * row_bytes_of_thread;
     w.stages = most_stages * slot * blocks <= kRingBytes ? most_stages : 2;
     w.smem = w.stages * slot;
@@ -927,7 +949,7 @@ BwdPlan bwd_plan(int64_t rows, int64_t cols, bool vec, size_t row_elem_bytes) {
         parts = std::min<int64_t>((rows + kNarrow / g - 1) / (kNarrow / g), sms() * 4ll);
     } else if (chunks <= 1024 * nc) {
         b.kind = BwdPlan::kBlock;
-        b.w = wide_plan(rows, chunks, nc, nc * (vec ? 8 : 1) * row_elem_bytes, 3);
+        b.w = wide_plan(rows, chunks, nc, nc * (vec ? 8 : 1) * row_elem_bytes, 3, kRegs);
         parts = b.w.grid;
     } else {
         b.kind = BwdPlan::kLoop;
@@ -983,17 +1005,17 @@ extern "C" nvfp4_status nvfp4_layer_norm_forward(const void* x, int32_t x_dtype,
             if (chunks <= 32) return narrow(norm_fwd_warp_kernel<X, Y, 8, 1, 4>);
             if (chunks <= 64) return narrow(norm_fwd_warp_kernel<X, Y, 8, 2, 2>);
             if (chunks <= 1024) {
-                const WidePlan w = wide_plan(rows, chunks, 1, 8 * elem, 4);
+                const WidePlan w = wide_plan(rows, chunks, 1, 8 * elem, 4, residual ? kFewRegs : kRegs);
                 return w.rb == 2 ? wide(Int<8>{}, Int<1>{}, Int<2>{}, w) : wide(Int<8>{}, Int<1>{}, Int<1>{}, w);
             }
             // two rows of 16384 fp32 columns with a residual do not fit shared memory
             if (chunks <= 2048 && 2 * cols * elem <= 216 * 1024)
-                return wide(Int<8>{}, Int<2>{}, Int<1>{}, wide_plan(rows, chunks, 2, 16 * elem, 4));
+                return wide(Int<8>{}, Int<2>{}, Int<1>{}, wide_plan(rows, chunks, 2, 16 * elem, 4, residual ? kFewRegs : kRegs));
             return to_status(launch_pdl(norm_fwd_loop_kernel<X, Y, 8>, dim3((unsigned)std::min<int64_t>(rows, 1 << 30)),
                                         dim3(kLoopThreads), 0, s, p));
         }
         if (chunks <= 32 * 8) return narrow(norm_fwd_warp_kernel<X, Y, 1, 8, 2>);
-        if (chunks <= 1024 * 8) return wide(Int<1>{}, Int<8>{}, Int<1>{}, wide_plan(rows, chunks, 8, 8 * elem, 4));
+        if (chunks <= 1024 * 8) return wide(Int<1>{}, Int<8>{}, Int<1>{}, wide_plan(rows, chunks, 8, 8 * elem, 4, residual ? kFewRegs : kRegs));
         return to_status(launch_pdl(norm_fwd_loop_kernel<X, Y, 1>, dim3((unsigned)std::min<int64_t>(rows, 1 << 30)),
                                     dim3(kLoopThreads), 0, s, p));
     });
