@@ -938,7 +938,7 @@ struct BwdPlan {
 };
 BwdPlan bwd_plan(int64_t rows, int64_t cols, bool vec, size_t row_elem_bytes) {
     const int64_t chunks = vec ? cols / 8 : cols;
-    const int nc = vec ? 1 : 8;
+    const int nc = vec ? 1 : chunks <= 4096 ? 4 : 8;
     BwdPlan b = {};
     int64_t parts;
     if (chunks <= (vec ? 64 : 256)) {
@@ -950,6 +950,7 @@ BwdPlan bwd_plan(int64_t rows, int64_t cols, bool vec, size_t row_elem_bytes) {
     } else if (chunks <= 1024 * nc) {
         b.kind = BwdPlan::kBlock;
         b.w = wide_plan(rows, chunks, nc, nc * (vec ? 8 : 1) * row_elem_bytes, 3, kRegs);
+        b.w.grid = std::min<int64_t>(b.w.grid, 3 * sms());     // each block's part is written and read once more
         parts = b.w.grid;
     } else {
         b.kind = BwdPlan::kLoop;
@@ -990,7 +991,7 @@ extern "C" nvfp4_status nvfp4_layer_norm_forward(const void* x, int32_t x_dtype,
         using Y = typename decltype(ty)::type;
         auto narrow = [&](auto kern) {
             const int g = group_lanes(chunks);
-            const int64_t grid = std::min<int64_t>((rows + kNarrow / g - 1) / (kNarrow / g), sms() * 16ll);
+            const int64_t grid = std::min<int64_t>((rows + kNarrow / g - 1) / (kNarrow / g), sms() * 5ll);
             return to_status(launch_pdl(kern, dim3((unsigned)grid), dim3(kNarrow), 0, s, p, g));
         };
         // stages 4 or 2, with or without residual, for one shape of a thread's part
@@ -1071,7 +1072,8 @@ extern "C" nvfp4_status nvfp4_layer_norm_backward(const void* dy, int32_t y_dtyp
                                : (plan.w.stages == 3 ? norm_bwd_kernel<X, Y, E, NC, RB, 3, false> : norm_bwd_kernel<X, Y, E, NC, RB, 2, false>);
                 e = launch_ring(kern, plan.parts, plan.w.threads, plan.w.smem, s, p);
             };
-            if (!vec) wide(Int<1>{}, Int<8>{}, Int<1>{});
+            if (!vec && cols <= 4096) wide(Int<1>{}, Int<4>{}, Int<1>{});
+            else if (!vec) wide(Int<1>{}, Int<8>{}, Int<1>{});
             else if (plan.w.rb == 2) wide(Int<8>{}, Int<1>{}, Int<2>{});
             else wide(Int<8>{}, Int<1>{}, Int<1>{});
         } else {

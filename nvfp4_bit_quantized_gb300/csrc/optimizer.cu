@@ -1,4 +1,4 @@
-// optimizer.cu -- AdamW over many tensors, with the two states in fp32 or in 8 bits (include/nvfp4.h
+// optimizer.cu -- AdamW over many tensors, with the two moments in fp32 or in 8 bits (include/nvfp4.h
 // has the formulas).  Every line of the update is one IEEE fp32 operation after another, so a result
 // does not depend on how the compiler contracts it.
 //
@@ -8,6 +8,12 @@
 // stochastically it follows in expectation, with a spread of about 0.018 / sqrt(1 - beta2) .. 0.036 /
 // sqrt(1 - beta2) of the value (step^2 / 6 a step against a pull of 1 - beta2).  v's code is kept off
 // zero: a denominator rounded to zero would blow the next step up.
+//
+// One launch for many tensors: their descriptors are the kernel's parameter (no table to copy to the
+// device), a block takes 4096 neighbouring elements of one tensor and finds it by bisection.  Bound by
+// memory: 26 bytes an element with fp32 parameters and states and bf16 gradients, 14.1 with 8-bit
+// states.  A thread takes 8 neighbouring elements with 16-byte accesses, 16 threads an 8-bit state's
+// block; tensors that do not lie on 16 bytes, and a tensor's last elements, go one by one.
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
 #include <cmath>
@@ -19,7 +25,13 @@
 namespace nvfp4 {
 namespace {
 
+using bf16 = __nv_bfloat16;
+
 constexpr int kBlock = 128;                    // elements with one scale
+constexpr int kThreads = 256, kPer = 8;        // a thread's elements at a time
+constexpr int kRounds = 2;
+constexpr int kSlice = kThreads * kPer * kRounds;      // elements of a CUDA block
+static_assert(kSlice % kBlock == 0 && kBlock == 16 * kPer, "an 8-bit block is 16 threads' elements");
 
 struct AdamwConsts {
     float b1, c1, b2, c2;                      // beta, 1 - beta
@@ -38,30 +50,78 @@ struct AdamwTensor {
     int64_t n;
     float keep;                                // 1 - lr * weight_decay
     uint32_t id;
+    uint32_t first_slice;
+    uint32_t vec;                              // all of it on 16 bytes
+};
+
+// The descriptors of one launch: two sizes, so that few tensors do not carry a large parameter.
+template <int MAX> struct Batch {
+    AdamwTensor t[MAX];
+    AdamwConsts k;
+    int count;
 };
 
 __device__ __forceinline__ float load1(const float* p) { return *p; }
-__device__ __forceinline__ float load1(const __nv_bfloat16* p) { return __bfloat162float(*p); }
+__device__ __forceinline__ float load1(const bf16* p) { return __bfloat162float(*p); }
+
+__device__ __forceinline__ uint4 ld16(const void* p) {
+    uint4 v;
+    asm volatile("ld.global.L1::no_allocate.v4.u32 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+    return v;
+}
+template <int N> struct Raw;
+template <> struct Raw<8> {                    // 8 bytes
+    uint2 a;
+    __device__ __forceinline__ void load(const void* p) {
+        asm volatile("ld.global.L1::no_allocate.v2.u32 {%0, %1}, [%2];" : "=r"(a.x), "=r"(a.y) : "l"(p) : "memory");
+    }
+};
+template <> struct Raw<16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const void* p) { a = ld16(p); }
+};
+template <> struct Raw<32> {
+    uint4 a, b;
+    __device__ __forceinline__ void load(const void* p) {
+        a = ld16(p);
+        b = ld16(static_cast<const uint4*>(p) + 1);
+    }
+};
+__device__ __forceinline__ void get8(const Raw<16>& r, float (&f)[8]) { Vec<uint16_t>::unpack(r.a, f); }      // bf16
+__device__ __forceinline__ void get8(const Raw<32>& r, float (&f)[8]) {
+    Vec<float>::unpack(r.a, f);
+    Vec<float>::unpack(r.b, f + 4);
+}
+__device__ __forceinline__ void put8(float* p, const float (&f)[8]) {
+    reinterpret_cast<float4*>(p)[0] = make_float4(f[0], f[1], f[2], f[3]);
+    reinterpret_cast<float4*>(p)[1] = make_float4(f[4], f[5], f[6], f[7]);
+}
+__device__ __forceinline__ void put8(bf16* p, const float (&f)[8]) {       // values that bf16 holds
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) w[i] = __byte_perm(__float_as_uint(f[2 * i]), __float_as_uint(f[2 * i + 1]), 0x7632);
+    *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+}
 
 __device__ __forceinline__ Philox4 words_of(const AdamwConsts& k, int64_t i, uint32_t stream) {
     return philox4x32_10((uint32_t)(i >> 2), (uint32_t)(i >> 34), stream, k.step, k.key);
 }
 
-// bf16 from fp32 bits: to nearest even, or up where the low half plus rand16 carries.
-__device__ __forceinline__ float to_bf16(float v, bool sr, uint32_t rand16) {
-    if (!sr) return __bfloat162float(__float2bfloat16_rn(v));
+// The nearest-even or stochastic bf16 value (up where the low half plus rand16 carries).
+template <bool SR> __device__ __forceinline__ float to_bf16(float v, uint32_t rand16) {
+    if constexpr (!SR) return __bfloat162float(__float2bfloat16_rn(v));
     uint32_t b = __float_as_uint(v);
     if ((b & 0x7F800000u) != 0x7F800000u) b += rand16;
     return __uint_as_float(b & 0xFFFF0000u);
 }
 
-// E4M3 code of x.  2^-120 x has the grid's exponents, subnormals included, as fp32's own: the code
-// is the word's top bits, 20 bits below them deciding the rounding.
-__device__ __forceinline__ uint32_t to_e4m3(float x, bool sr, uint32_t rand16) {
-    const uint32_t sign = (__float_as_uint(x) >> 24) & 0x80u;
+// E4M3 code of x, without its sign.  2^-120 x has the grid's exponents, subnormals included, as fp32's
+// own: the code is the word's top bits, 20 bits below them deciding the rounding.
+template <bool SR> __device__ __forceinline__ uint32_t to_e4m3(float x, uint32_t rand16) {
     const uint32_t b = __float_as_uint(__fmul_rn(fabsf(x), 0x1p-120f));
-    const uint32_t up = sr ? rand16 << 4 : 0x7FFFFu + ((b >> 20) & 1u);
-    return sign | min((b + up) >> 20, 126u);
+    const uint32_t up = SR ? rand16 << 4 : 0x7FFFFu + ((b >> 20) & 1u);
+    return min((b + up) >> 20, 126u);
 }
 __device__ __forceinline__ float from_e4m3(uint32_t code) {
     return __fmul_rn(__uint_as_float(((code & 0x80u) << 24) | ((code & 0x7Fu) << 20)), 0x1p120f);
@@ -74,98 +134,235 @@ __device__ __forceinline__ void update(const AdamwConsts& k, float g, float keep
                   __fdiv_rn(__fmul_rn(m, k.size), __fadd_rn(__fmul_rn(__fsqrt_rn(v), k.unbias), k.eps)));
 }
 
-template <typename P>
-__device__ __forceinline__ void store_param(const AdamwConsts& k, P* p, int64_t i, float v, bool sr, uint32_t id) {
-    if constexpr (sizeof(P) == 4) p[i] = v;
-    else {
-        const uint32_t r = sr ? words_of(k, i, 2 * id + 1).w[i & 3] & 0xFFFFu : 0u;
-        p[i] = __float2bfloat16_rn(to_bf16(v, sr, r));
-    }
+__device__ __forceinline__ float inverse_of(float top) {
+    return top > 0.0f ? fminf(__fdiv_rn(448.0f, top), FLT_MAX) : 0.0f;
+}
+// max of non-negative values by their bits (NaN above all others) over the 16 threads of a block
+__device__ __forceinline__ uint32_t max16(uint32_t v) {
+#pragma unroll
+    for (int d = 8; d; d >>= 1) v = max(v, __shfl_xor_sync(~0u, v, d));
+    return v;
 }
 
-template <typename P, typename G>
-__global__ void __launch_bounds__(256) adamw32_kernel(AdamwTensor t, AdamwConsts k, int sr) {
+template <typename P, typename G, int BITS, bool SR, int MAX>
+__global__ void __launch_bounds__(kThreads, BITS == 32 ? 4 : 3) adamw_kernel(const __grid_constant__ Batch<MAX> batch) {
     pdl_launch_dependents();
     pdl_wait();
-    const float gs = k.grad_scale ? *k.grad_scale : 1.0f;
-    P* p = static_cast<P*>(t.param);
-    float *m = static_cast<float*>(t.m), *v = static_cast<float*>(t.v);
-    for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < t.n; i += gridDim.x * 256ll) {
-        const float g = __fmul_rn(load1(static_cast<const G*>(t.grad) + i), gs);
-        if (!isfinite(g)) set_status(k.dev_status, NVFP4_ERR_NONFINITE);
-        float pv = load1(p + i), mv = m[i], vv = v[i];
-        update(k, g, t.keep, pv, mv, vv);
-        m[i] = mv;
-        v[i] = vv;
-        store_param(k, p, i, pv, sr, t.id);
+    // the tensor of this slice: the last that begins at or before it
+    int lo = 0, hi = batch.count - 1;
+    while (lo < hi) {
+        const int mid = (lo + hi + 1) >> 1;
+        if (batch.t[mid].first_slice <= blockIdx.x) lo = mid;
+        else hi = mid - 1;
     }
-}
-
-// max over a block's 128 threads, on the bits of non-negative values (NaN above all others).
-__device__ __forceinline__ uint32_t block_max(uint32_t v, uint32_t* red) {
-    v = __reduce_max_sync(~0u, v);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) red[threadIdx.x >> 5] = v;
-    __syncthreads();
-    return max(max(red[0], red[1]), max(red[2], red[3]));
-}
-
-__device__ __forceinline__ uint8_t encode(float x, uint32_t top_bits, float* scale, bool sr, uint32_t rand16,
-                                          bool floor1) {
-    const float top = __uint_as_float(top_bits);
-    const float inv = top > 0.0f ? fminf(__fdiv_rn(448.0f, top), FLT_MAX) : 0.0f;
-    if (threadIdx.x == 0) *scale = __fmul_rn(top, 1.0f / 448.0f);
-    uint32_t c = to_e4m3(__fmul_rn(x, inv), sr, rand16);
-    if (floor1 && x > 0.0f) c = max(c, 1u);
-    return (uint8_t)c;
-}
-
-template <typename P, typename G>
-__global__ void __launch_bounds__(kBlock) adamw8_kernel(AdamwTensor t, AdamwConsts k, int sr) {
-    pdl_launch_dependents();
-    pdl_wait();
-    __shared__ uint32_t red[4];
+    const AdamwTensor& t = batch.t[lo];
+    const AdamwConsts& k = batch.k;
     const float gs = k.grad_scale ? *k.grad_scale : 1.0f;
-    P* p = static_cast<P*>(t.param);
+    P* param = static_cast<P*>(t.param);
+    const G* grad = static_cast<const G*>(t.grad);
+    constexpr int SB = BITS == 32 ? 32 : 8;                // bytes of eight elements of a state
+    constexpr int PB = 8 * sizeof(P), GB = 8 * sizeof(G);
+    const int64_t n = t.n;
+    const float keep = t.keep;
+    const int64_t base = (int64_t)(blockIdx.x - t.first_slice) * kSlice + threadIdx.x * kPer;
     uint8_t *mc = static_cast<uint8_t*>(t.m), *vc = static_cast<uint8_t*>(t.v);
-    const int64_t blocks = (t.n + kBlock - 1) / kBlock;
-    for (int64_t b = blockIdx.x; b < blocks; b += gridDim.x) {
-        const int64_t i = b * kBlock + threadIdx.x;
-        const bool in = i < t.n;
-        float pv = 0.0f, mv = 0.0f, vv = 0.0f, g = 0.0f;
-        if (in) {
-            g = __fmul_rn(load1(static_cast<const G*>(t.grad) + i), gs);
-            pv = load1(p + i);
-            mv = __fmul_rn(from_e4m3(mc[i]), t.m_scale[b]);
-            vv = __fmul_rn(from_e4m3(vc[i]), t.v_scale[b]);
-        }
-        if (!isfinite(g)) set_status(k.dev_status, NVFP4_ERR_NONFINITE);
-        update(k, g, t.keep, pv, mv, vv);
-        const uint32_t mt = block_max(__float_as_uint(fabsf(mv)), red);   // its barriers follow the scale reads
-        const uint32_t vt = block_max(__float_as_uint(fabsf(vv)), red);
-        const uint32_t w = sr ? words_of(k, i, 2 * t.id).w[i & 3] : 0u;
-        const uint8_t cm = encode(mv, mt, t.m_scale + b, sr, w & 0xFFFFu, false);
-        const uint8_t cv = encode(vv, vt, t.v_scale + b, sr, w >> 16, true);
-        if (in) {
-            mc[i] = cm;
-            vc[i] = cv;
-            store_param(k, p, i, pv, sr, t.id);
-        }
-    }
-}
 
-template <typename P, typename G>
-cudaError_t launch_one(const AdamwTensor& t, const AdamwConsts& k, int bits, int sr, cudaStream_t s) {
-    if (bits == 32) {
-        const int grid = (int)std::min<int64_t>((t.n + 255) / 256, 152 * 32);
-        return launch_pdl(adamw32_kernel<P, G>, dim3(grid), dim3(256), 0, s, t, k, sr);
+    // all rounds' loads first
+    Raw<PB> rp[kRounds];
+    Raw<GB> rg[kRounds];
+    Raw<SB> rm[kRounds], rv[kRounds];
+    float sm[kRounds], sv[kRounds];
+#pragma unroll
+    for (int q = 0; q < kRounds; ++q) {
+        const int64_t i = base + q * (kThreads * kPer);
+        if (t.vec && i + kPer <= n) {
+            rp[q].load(param + i);
+            rg[q].load(grad + i);
+            rm[q].load(mc + i * (SB / 8));
+            rv[q].load(vc + i * (SB / 8));
+        }
+        if (BITS == 8 && i < n) {
+            sm[q] = t.m_scale[i / kBlock];
+            sv[q] = t.v_scale[i / kBlock];
+        }
     }
-    const int grid = (int)std::min<int64_t>((t.n + kBlock - 1) / kBlock, 152 * 64);
-    return launch_pdl(adamw8_kernel<P, G>, dim3(grid), dim3(kBlock), 0, s, t, k, sr);
+    uint32_t worst = 0;                                    // the largest gradient, for the finite check
+#pragma unroll
+    for (int q = 0; q < kRounds; ++q) {
+        const int64_t i = base + q * (kThreads * kPer);
+        const bool full = t.vec && i + kPer <= n;
+        float p[8] = {}, g[8] = {}, m[8] = {}, v[8] = {};
+        uint32_t cm[2], cv[2];
+        if (full) {
+            get8(rp[q], p);
+            get8(rg[q], g);
+            if constexpr (BITS == 32) {
+                get8(rm[q], m);
+                get8(rv[q], v);
+            } else {
+                cm[0] = rm[q].a.x; cm[1] = rm[q].a.y;
+                cv[0] = rv[q].a.x; cv[1] = rv[q].a.y;
+            }
+        } else {
+            cm[0] = cm[1] = cv[0] = cv[1] = 0u;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (i + e < n) {
+                    p[e] = load1(param + i + e);
+                    g[e] = load1(grad + i + e);
+                    if constexpr (BITS == 32) {
+                        m[e] = static_cast<float*>(t.m)[i + e];
+                        v[e] = static_cast<float*>(t.v)[i + e];
+                    } else {
+                        cm[e >> 2] |= (uint32_t)mc[i + e] << (8 * (e & 3));
+                        cv[e >> 2] |= (uint32_t)vc[i + e] << (8 * (e & 3));
+                    }
+                }
+        }
+        if constexpr (BITS == 8) {
+            const float a = i < n ? sm[q] : 0.0f, b = i < n ? sv[q] : 0.0f;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                m[e] = __fmul_rn(from_e4m3(cm[e >> 2] >> (8 * (e & 3))), a);
+                v[e] = __fmul_rn(from_e4m3(cv[e >> 2] >> (8 * (e & 3))), b);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            g[e] = __fmul_rn(g[e], gs);
+            worst = max(worst, __float_as_uint(g[e]) & 0x7FFFFFFFu);
+            update(k, g[e], keep, p[e], m[e], v[e]);
+        }
+        // a bf16 parameter's random words, stream 1; words of elements 4 j .. 4 j + 3 from one call
+        if constexpr (sizeof(P) == 2) {
+            Philox4 w[2] = {};
+            if constexpr (SR) {
+                w[0] = words_of(k, i, 2 * t.id + 1);
+                w[1] = words_of(k, i + 4, 2 * t.id + 1);
+            }
+#pragma unroll
+            for (int e = 0; e < 8; ++e) p[e] = to_bf16<SR>(p[e], w[e >> 2].w[e & 3] & 0xFFFFu);
+        }
+        if constexpr (BITS == 8) {
+            uint32_t tm = 0, tv = 0;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                // past the tensor's end everything is zero: it takes no part in the largest value
+                tm = max(tm, __float_as_uint(m[e]) & 0x7FFFFFFFu);
+                tv = max(tv, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+            }
+            const float topm = __uint_as_float(max16(tm)), topv = __uint_as_float(max16(tv));
+            if ((threadIdx.x & 15) == 0 && i < n) {
+                t.m_scale[i / kBlock] = __fmul_rn(topm, 1.0f / 448.0f);
+                t.v_scale[i / kBlock] = __fmul_rn(topv, 1.0f / 448.0f);
+            }
+            const float im = inverse_of(topm), iv = inverse_of(topv);
+            Philox4 w[2] = {};
+            if constexpr (SR) {
+                w[0] = words_of(k, i, 2 * t.id);
+                w[1] = words_of(k, i + 4, 2 * t.id);
+            }
+            cm[0] = cm[1] = cv[0] = cv[1] = 0u;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const uint32_t r = w[e >> 2].w[e & 3], sign = __float_as_uint(m[e]) >> 31;
+                const uint32_t a = to_e4m3<SR>(__fmul_rn(m[e], im), r & 0xFFFFu) | sign << 7;
+                uint32_t b = to_e4m3<SR>(__fmul_rn(v[e], iv), r >> 16);
+                if (v[e] > 0.0f) b = max(b, 1u);
+                cm[e >> 2] |= a << (8 * (e & 3));
+                cv[e >> 2] |= b << (8 * (e & 3));
+            }
+        }
+        if (full) {
+            put8(param + i, p);
+            if constexpr (BITS == 32) {
+                put8(static_cast<float*>(t.m) + i, m);
+                put8(static_cast<float*>(t.v) + i, v);
+            } else {
+                *reinterpret_cast<uint2*>(mc + i) = make_uint2(cm[0], cm[1]);
+                *reinterpret_cast<uint2*>(vc + i) = make_uint2(cv[0], cv[1]);
+            }
+        } else {
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (i + e < n) {
+                    if constexpr (sizeof(P) == 4) param[i + e] = p[e];
+                    else param[i + e] = __float2bfloat16_rn(p[e]);
+                    if constexpr (BITS == 32) {
+                        static_cast<float*>(t.m)[i + e] = m[e];
+                        static_cast<float*>(t.v)[i + e] = v[e];
+                    } else {
+                        mc[i + e] = (uint8_t)(cm[e >> 2] >> (8 * (e & 3)));
+                        vc[i + e] = (uint8_t)(cv[e >> 2] >> (8 * (e & 3)));
+                    }
+                }
+        }
+    }
+    if (worst >= 0x7F800000u) set_status(k.dev_status, NVFP4_ERR_NONFINITE);
 }
 
 bool known(int32_t t) { return t == NVFP4_F32 || t == NVFP4_BF16; }
 bool aligned_to(const void* p, size_t n) { return reinterpret_cast<uintptr_t>(p) % n == 0; }
+
+constexpr int kFew = 24, kMany = 400;
+static_assert(sizeof(Batch<kMany>) <= 32764, "kernel parameters");
+
+template <typename P, typename G, int MAX>
+cudaError_t launch(const Batch<MAX>& b, int bits, bool sr, unsigned slices, cudaStream_t s) {
+    auto kern = bits == 32 ? (sr && sizeof(P) == 2 ? adamw_kernel<P, G, 32, true, MAX> : adamw_kernel<P, G, 32, false, MAX>)
+                           : (sr ? adamw_kernel<P, G, 8, true, MAX> : adamw_kernel<P, G, 8, false, MAX>);
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(slices);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    void* args[1] = {const_cast<Batch<MAX>*>(&b)};         // by address: the batch is not copied on the way
+    return cudaLaunchKernelExC(&cfg, reinterpret_cast<const void*>(kern), args);
+}
+
+// The tensors of one pair of types, at most MAX a launch.
+template <typename P, typename G, int MAX>
+cudaError_t step_types(const nvfp4_adamw_tensor* ts, int count, const nvfp4_adamw_params& hp, const AdamwConsts& k,
+                       int32_t pt, int32_t gt, cudaStream_t s) {
+    Batch<MAX> b;
+    b.k = k;
+    b.count = 0;
+    int64_t slices = 0;
+    cudaError_t e = cudaSuccess;
+    auto flush = [&] {
+        if (b.count && e == cudaSuccess) e = launch<P, G, MAX>(b, hp.bits, hp.round == NVFP4_ROUND_SR, (unsigned)slices, s);
+        b.count = 0;
+        slices = 0;
+    };
+    for (int i = 0; i < count; ++i) {
+        const nvfp4_adamw_tensor& a = ts[i];
+        if (a.n == 0 || !a.grad || a.param_dtype != pt || a.grad_dtype != gt) continue;
+        const int64_t mine = (a.n + kSlice - 1) / kSlice;  // at most 2^28
+        if (b.count == MAX || slices + mine > (1ll << 30)) flush();
+        const size_t state = hp.bits == 32 ? 16 : 8;
+        const bool vec = aligned16(a.param) && aligned16(a.grad) && aligned_to(a.m, state) && aligned_to(a.v, state);
+        b.t[b.count++] = AdamwTensor{a.param, a.grad, a.m, a.v, a.m_scale, a.v_scale, a.n, (float)(1.0 - hp.lr * a.weight_decay),
+                                     (uint32_t)a.id, (uint32_t)slices, vec};
+        slices += mine;
+    }
+    flush();
+    return e;
+}
+
+template <int MAX>
+cudaError_t step_all(const nvfp4_adamw_tensor* ts, int count, const nvfp4_adamw_params& hp, const AdamwConsts& k,
+                     const bool (&seen)[2][2], cudaStream_t s) {
+    cudaError_t e = cudaSuccess;
+    if (seen[0][0]) e = step_types<float, float, MAX>(ts, count, hp, k, NVFP4_F32, NVFP4_F32, s);
+    if (seen[0][1] && e == cudaSuccess) e = step_types<float, bf16, MAX>(ts, count, hp, k, NVFP4_F32, NVFP4_BF16, s);
+    if (seen[1][0] && e == cudaSuccess) e = step_types<bf16, float, MAX>(ts, count, hp, k, NVFP4_BF16, NVFP4_F32, s);
+    if (seen[1][1] && e == cudaSuccess) e = step_types<bf16, bf16, MAX>(ts, count, hp, k, NVFP4_BF16, NVFP4_BF16, s);
+    return e;
+}
 
 }  // namespace
 }  // namespace nvfp4
@@ -183,6 +380,7 @@ extern "C" nvfp4_status nvfp4_adamw_step(const nvfp4_adamw_tensor* tensors, int3
         !std::isfinite(hp->eps) || !std::isfinite(hp->lr))
         return NVFP4_ERR_INVALID_ARG;
     if (!aligned_to(grad_scale, 4)) return NVFP4_ERR_ALIGNMENT;
+    bool seen[2][2] = {};
     for (int i = 0; i < count; ++i) {
         const nvfp4_adamw_tensor& t = tensors[i];
         if (t.n < 0 || t.n > (1ll << 40)) return NVFP4_ERR_SHAPE;
@@ -196,6 +394,7 @@ extern "C" nvfp4_status nvfp4_adamw_step(const nvfp4_adamw_tensor* tensors, int3
             (hp->bits == 32 ? !aligned_to(t.m, 4) || !aligned_to(t.v, 4)
                             : !aligned_to(t.m_scale, 4) || !aligned_to(t.v_scale, 4)))
             return NVFP4_ERR_ALIGNMENT;
+        seen[t.param_dtype][t.grad_dtype] = true;
     }
     AdamwConsts k;
     k.b1 = (float)hp->beta1;
@@ -209,19 +408,8 @@ extern "C" nvfp4_status nvfp4_adamw_step(const nvfp4_adamw_tensor* tensors, int3
     k.grad_scale = grad_scale;
     k.dev_status = dev_status;
     k.key = philox_key(hp->sr_seed);
-    const int sr = hp->round == NVFP4_ROUND_SR;
-    for (int i = 0; i < count; ++i) {
-        const nvfp4_adamw_tensor& a = tensors[i];
-        if (a.n == 0 || !a.grad) continue;
-        const AdamwTensor t{a.param, a.grad, a.m, a.v, a.m_scale, a.v_scale, a.n,
-                            (float)(1.0 - hp->lr * a.weight_decay), (uint32_t)a.id};
-        const cudaStream_t s = static_cast<cudaStream_t>(stream);
-        const bool pf = a.param_dtype == NVFP4_F32, gf = a.grad_dtype == NVFP4_F32;
-        const cudaError_t e = pf ? (gf ? launch_one<float, float>(t, k, hp->bits, sr, s)
-                                       : launch_one<float, __nv_bfloat16>(t, k, hp->bits, sr, s))
-                                 : (gf ? launch_one<__nv_bfloat16, float>(t, k, hp->bits, sr, s)
-                                       : launch_one<__nv_bfloat16, __nv_bfloat16>(t, k, hp->bits, sr, s));
-        if (e != cudaSuccess) return NVFP4_ERR_CUDA;
-    }
-    return NVFP4_OK;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    const cudaError_t e = count <= kFew ? step_all<kFew>(tensors, count, *hp, k, seen, s)
+                                        : step_all<kMany>(tensors, count, *hp, k, seen, s);
+    return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }

@@ -13,37 +13,68 @@ import torch
 
 from . import _lib as L
 from ._lib import NVFP4Error
-from .api import _DT, _check_2d, _ptr, _stream, _workspace, dev_status
+from . import api
+from .api import _DT, _check_2d, _ptr, dev_status
 
 
 def _invalid(what: str) -> NVFP4Error:
     return NVFP4Error(L.ERR_INVALID_ARG, what)
 
 
-def _on_current_device(t: torch.Tensor, name: str) -> None:
-    if not t.is_cuda or t.device.index != torch.cuda.current_device():
-        raise _invalid(f"{name} must be a tensor on the current CUDA device")
+# The calls here are short; what a wrapper costs on the host shows.  So arguments are compared against what they
+# have to be in one go, and looked at one by one only when something is wrong.
+
+def _here(dev: int) -> int:
+    """The current stream of device ``dev``, which has to be the current device."""
+    if dev != torch.cuda.current_device():
+        raise _invalid("the tensors must be on the current CUDA device")
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
-def _rows(t: torch.Tensor, name: str, shape, dtype) -> int:
-    """Row pitch of a [rows, cols] operand that has to match ``shape`` and ``dtype``."""
-    _check_2d(t, name)
-    _on_current_device(t, name)
-    if t.dtype != dtype:
-        raise _invalid(f"{name} must be {dtype}")
-    if tuple(t.shape) != tuple(shape):
+def _on(t: torch.Tensor, name: str, dev: int) -> None:
+    if not t.is_cuda or t.get_device() != dev:
+        raise _invalid(f"{name} must be on CUDA device {dev}")
+
+
+def _matrix(t: torch.Tensor, name: str, shape, dtype, dev: int) -> int:
+    """Row pitch of a [rows, cols] operand of ``shape``, ``dtype`` and device ``dev``."""
+    if t.shape != shape or t.dtype is not dtype or t.get_device() != dev:
+        _check_2d(t, name)
+        _on(t, name, dev)
+        if t.dtype != dtype:
+            raise _invalid(f"{name} must be {dtype}")
         raise NVFP4Error(L.ERR_SHAPE, f"{name} must be {list(shape)}")
-    return t.stride(0) if t.shape[0] > 1 else max(t.shape[1], 1)
+    pitch, unit = t.stride()
+    if unit != 1 and shape[1] > 1:
+        raise _invalid(f"{name} must have unit column stride")
+    return pitch if shape[0] > 1 else max(shape[1], 1)
 
 
-def _vector(t: torch.Tensor, name: str, n: int, dtypes) -> None:
-    _on_current_device(t, name)
+def _vector(t: torch.Tensor, name: str, n: int, dtypes, dev: int) -> int:
+    """Address of a contiguous [n] operand."""
     if t.dtype not in dtypes:
         raise _invalid(f"{name} must be one of {[str(d) for d in dtypes]}")
     if t.dim() != 1 or t.shape[0] != n:
         raise NVFP4Error(L.ERR_SHAPE, f"{name} must be [{n}]")
-    if n > 1 and t.stride(0) != 1:
+    if not t.is_contiguous():
         raise _invalid(f"{name} must be contiguous")
+    if t.get_device() != dev:
+        _on(t, name, dev)
+    return t.data_ptr()
+
+
+def _workspace(nbytes: int, dev: int, stream: int) -> torch.Tensor:
+    """The module's workspace of this device and stream (the one the quantizers use), grown to ``nbytes``."""
+    t = api._ws.get((dev, stream))
+    return t if t is not None and t.numel() >= nbytes else api._workspace(nbytes)
+
+
+def _status_ptr(dev: int) -> int:
+    t = api._status.get(dev)
+    return (dev_status(dev) if t is None else t).data_ptr()
+
+
+_F32_ONLY = (torch.float32,)
 
 
 # ----------------------------------------------------------------------------- layer norm
@@ -55,28 +86,30 @@ def layer_norm_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[tor
     x: float32 / bfloat16 with unit column stride; weight, bias: [cols], one type; the result is
     of ``out_dtype`` (x's type by default).  Returns (y, mean, rstd, h), h being x itself without
     a residual: mean, rstd and h are what :func:`layer_norm_backward` needs."""
-    _check_2d(x, "x")
-    R, C = x.shape
+    dtype, dev = x.dtype, x.get_device()
+    if dtype not in _DT or x.dim() != 2 or dev < 0:
+        _check_2d(x, "x")
+    R, C = shape = x.shape
     if C < 1:
         raise NVFP4Error(L.ERR_SHAPE, "x has no columns")
-    ldx = _rows(x, "x", (R, C), x.dtype)
-    _vector(weight, "weight", C, tuple(_DT))
-    if bias is not None:
-        _vector(bias, "bias", C, (weight.dtype,))
-    out_dtype = x.dtype if out_dtype is None else out_dtype
+    ldx = _matrix(x, "x", shape, dtype, dev)
+    w = _vector(weight, "weight", C, _DT, dev)
+    b = None if bias is None else _vector(bias, "bias", C, (weight.dtype,), dev)
+    out_dtype = dtype if out_dtype is None else out_dtype
     if out_dtype not in _DT:
         raise _invalid("out_dtype must be float32 or bfloat16")
+    stream = _here(dev)
     h, ldr = None, 0
     if residual is not None:
-        ldr = _rows(residual, "residual", (R, C), x.dtype)
-        h = torch.empty((R, C), dtype=x.dtype, device=x.device)
-    y = torch.empty((R, C), dtype=out_dtype, device=x.device)
-    mean = torch.empty(R, dtype=torch.float32, device=x.device)
-    rstd = torch.empty(R, dtype=torch.float32, device=x.device)
-    st = L.lib().nvfp4_layer_norm_forward(_ptr(x), _DT[x.dtype], R, C, ldx, _ptr(residual), ldr, _ptr(weight),
-                                          _ptr(bias), _DT[weight.dtype], eps, _ptr(y), _DT[out_dtype], C, _ptr(h), C,
-                                          _ptr(mean), _ptr(rstd), _stream())
-    L.check(st, "nvfp4_layer_norm_forward")
+        ldr = _matrix(residual, "residual", shape, dtype, dev)
+        h = x.new_empty(shape)
+    y = x.new_empty(shape, dtype=out_dtype)
+    mean, rstd = x.new_empty(R, dtype=torch.float32), x.new_empty(R, dtype=torch.float32)
+    st = L.lib().nvfp4_layer_norm_forward(x.data_ptr(), _DT[dtype], R, C, ldx, _ptr(residual), ldr, w, b, _DT[weight.dtype],
+                                          eps, y.data_ptr(), _DT[out_dtype], C, _ptr(h), C, mean.data_ptr(),
+                                          rstd.data_ptr(), stream)
+    if st:
+        L.check(st, "nvfp4_layer_norm_forward")
     return y, mean, rstd, x if h is None else h
 
 
@@ -86,64 +119,66 @@ def layer_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
     """Gradients of :func:`layer_norm_forward`: (dx, dweight, dbias), dx in h's type, the vectors in
     float32, dbias None unless ``bias``.  ``dh`` (h's type) is the gradient that reaches h along
     the residual path; it is added to dx, which then is the gradient of x and of the residual."""
-    _check_2d(h, "h")
-    R, C = h.shape
+    dtype, dev = h.dtype, h.get_device()
+    if dtype not in _DT or h.dim() != 2 or dev < 0:
+        _check_2d(h, "h")
+    R, C = shape = h.shape
     if C < 1:
         raise NVFP4Error(L.ERR_SHAPE, "h has no columns")
-    ldx = _rows(h, "h", (R, C), h.dtype)
-    _check_2d(dy, "dy")
-    lddy = _rows(dy, "dy", (R, C), dy.dtype)
-    lddh = 0 if dh is None else _rows(dh, "dh", (R, C), h.dtype)
-    _vector(weight, "weight", C, tuple(_DT))
-    _vector(mean, "mean", R, (torch.float32,))
-    _vector(rstd, "rstd", R, (torch.float32,))
-    dx = torch.empty((R, C), dtype=h.dtype, device=h.device)
-    dw = torch.empty(C, dtype=torch.float32, device=h.device)
-    db = torch.empty(C, dtype=torch.float32, device=h.device) if bias else None
+    if dy.dtype not in _DT:
+        raise _invalid("dy must be float32 or bfloat16")
+    ldx, lddy = _matrix(h, "h", shape, dtype, dev), _matrix(dy, "dy", shape, dy.dtype, dev)
+    lddh = 0 if dh is None else _matrix(dh, "dh", shape, dtype, dev)
+    w = _vector(weight, "weight", C, _DT, dev)
+    m, s = _vector(mean, "mean", R, _F32_ONLY, dev), _vector(rstd, "rstd", R, _F32_ONLY, dev)
+    stream = _here(dev)
+    dx = h.new_empty(shape)
+    dw = h.new_empty(C, dtype=torch.float32)
+    db = h.new_empty(C, dtype=torch.float32) if bias else None
     lib = L.lib()
-    ws = _workspace(int(lib.nvfp4_layer_norm_backward_workspace_bytes(R, C)))
-    st = lib.nvfp4_layer_norm_backward(_ptr(dy), _DT[dy.dtype], lddy, _ptr(h), _DT[h.dtype], R, C, ldx, _ptr(weight),
-                                       _DT[weight.dtype], _ptr(mean), _ptr(rstd), _ptr(dh), lddh, _ptr(dx), C,
-                                       _ptr(dw), _ptr(db), ws.data_ptr(), ws.numel(), _stream())
-    L.check(st, "nvfp4_layer_norm_backward")
+    ws = _workspace(lib.nvfp4_layer_norm_backward_workspace_bytes(R, C), dev, stream)
+    st = lib.nvfp4_layer_norm_backward(dy.data_ptr(), _DT[dy.dtype], lddy, h.data_ptr(), _DT[dtype], R, C, ldx, w,
+                                       _DT[weight.dtype], m, s, _ptr(dh), lddh, dx.data_ptr(), C, dw.data_ptr(), _ptr(db),
+                                       ws.data_ptr(), ws.numel(), stream)
+    if st:
+        L.check(st, "nvfp4_layer_norm_backward")
     return dx, dw, db
 
 
 # ----------------------------------------------------------------------------- attention
 
-def _heads(t: torch.Tensor, name: str, tokens: Optional[int] = None, heads: Optional[int] = None,
-           dim: Optional[int] = None) -> L.HeadsC:
-    if not isinstance(t, torch.Tensor) or t.dim() != 3:
-        raise NVFP4Error(L.ERR_SHAPE, f"{name} must be [tokens, heads, dim]")
-    _on_current_device(t, name)
-    if t.dtype != torch.bfloat16:
-        raise NVFP4Error(L.ERR_UNSUPPORTED, f"{name} must be bfloat16")
-    T, H, D = t.shape
-    if (tokens is not None and T != tokens) or (heads is not None and H != heads) or (dim is not None and D != dim):
-        raise NVFP4Error(L.ERR_SHAPE, f"{name} is {list(t.shape)}, expected {[tokens, heads, dim]}")
-    if D > 1 and t.stride(2) != 1:
+def _heads(t: torch.Tensor, name: str, shape, dev: int) -> L.HeadsC:
+    if t.shape != shape or t.dtype is not torch.bfloat16 or t.get_device() != dev:
+        if t.dim() != 3:
+            raise NVFP4Error(L.ERR_SHAPE, f"{name} must be [tokens, heads, dim]")
+        _on(t, name, dev)
+        if t.dtype != torch.bfloat16:
+            raise NVFP4Error(L.ERR_UNSUPPORTED, f"{name} must be bfloat16")
+        raise NVFP4Error(L.ERR_SHAPE, f"{name} is {list(t.shape)}, expected {list(shape)}")
+    tokens, heads, unit = t.stride()
+    if unit != 1 and shape[2] > 1:
         raise _invalid(f"{name} must be contiguous along dim")
-    return L.HeadsC(t.data_ptr() if T else None, t.stride(0), t.stride(1))
+    return L.HeadsC(t.data_ptr() or None, tokens, heads)
 
 
-def _attention_shape(q, k, causal, scale, cu_q, cu_k) -> L.AttentionShapeC:
+def _attention_shape(q, k, causal, scale, cu_q, cu_k, dev) -> L.AttentionShapeC:
     if q.dim() != 3 or k.dim() != 3:
         raise NVFP4Error(L.ERR_SHAPE, "q and k must be [tokens, heads, dim]")
-    if (cu_q is None) and (cu_k is not None):
-        raise _invalid("cu_k needs cu_q")
-    cu_k = cu_q if cu_k is None else cu_k
     nseq = 1
-    for cu, name in ((cu_q, "cu_q"), (cu_k, "cu_k")):
-        if cu is None:
-            continue
-        _on_current_device(cu, name)
-        if cu.dtype != torch.int32 or cu.dim() != 1 or not cu.is_contiguous() or cu.shape[0] < 2:
-            raise _invalid(f"{name} must be a contiguous int32 vector of at least two offsets")
-        if cu.shape != cu_q.shape:
+    if cu_q is None:
+        if cu_k is not None:
+            raise _invalid("cu_k needs cu_q")
+    else:
+        cu_k = cu_q if cu_k is None else cu_k
+        for cu, name in ((cu_q, "cu_q"), (cu_k, "cu_k")):
+            if cu.dtype != torch.int32 or cu.dim() != 1 or not cu.is_contiguous() or cu.shape[0] < 2:
+                raise _invalid(f"{name} must be a contiguous int32 vector of at least two offsets")
+            _on(cu, name, dev)
+        if cu_k.shape != cu_q.shape:
             raise NVFP4Error(L.ERR_SHAPE, "cu_q and cu_k differ in length")
-        nseq = cu.shape[0] - 1
-    scale = q.shape[2] ** -0.5 if scale is None else float(scale)
-    return L.AttentionShapeC(q.shape[0], k.shape[0], q.shape[1], k.shape[1], q.shape[2], int(bool(causal)), scale, nseq,
+        nseq = cu_q.shape[0] - 1
+    T, H, D = q.shape
+    return L.AttentionShapeC(T, k.shape[0], H, k.shape[1], D, bool(causal), D ** -0.5 if scale is None else scale, nseq,
                              _ptr(cu_q), _ptr(cu_k))
 
 
@@ -157,15 +192,19 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal:
     sequences (``cu_k`` defaults to ``cu_q``); None: one sequence.  ``causal`` masks are aligned at
     the sequences' ends.  ``scale`` defaults to dim ** -0.5.  Returns (out [tq, heads, dim], lse
     [heads, tq] float32); a query that sees no key gets 0 and -inf."""
-    shape = _attention_shape(q, k, causal, scale, cu_q, cu_k)
-    T, H, D = q.shape
+    dev = q.get_device()
+    shape = _attention_shape(q, k, causal, scale, cu_q, cu_k, dev)
+    T, H, D = qs = q.shape
+    ks = (k.shape[0], k.shape[1], D)
+    a, b, c = _heads(q, "q", qs, dev), _heads(k, "k", ks, dev), _heads(v, "v", ks, dev)
+    stream = _here(dev)
     if out is None:
-        out = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device)
-    args = [_heads(q, "q"), _heads(k, "k", dim=D), _heads(v, "v", k.shape[0], k.shape[1], D), _heads(out, "out", T, H, D)]
-    lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
-    st = L.lib().nvfp4_attention_forward(ctypes.byref(shape), *(ctypes.byref(a) for a in args), _ptr(lse),
-                                         dev_status(q.device).data_ptr(), _stream())
-    L.check(st, "nvfp4_attention_forward")
+        out = q.new_empty(qs)
+    d = _heads(out, "out", qs, dev)
+    lse = q.new_empty((H, T), dtype=torch.float32)
+    st = L.lib().nvfp4_attention_forward(shape, a, b, c, d, lse.data_ptr(), _status_ptr(dev), stream)
+    if st:
+        L.check(st, "nvfp4_attention_forward")
     return out, lse
 
 
@@ -177,24 +216,25 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     """Gradients (dq, dk, dv) of :func:`attention_forward`, the probabilities recomputed from q, k and
     lse.  dq, dk, dv may be given as strided views, such as the slices of one buffer that is the
     fused projection's dY.  Deterministic."""
-    shape = _attention_shape(q, k, causal, scale, cu_q, cu_k)
-    T, H, D = q.shape
-    S, G = k.shape[0], k.shape[1]
-    dq = torch.empty((T, H, D), dtype=torch.bfloat16, device=q.device) if dq is None else dq
-    dk = torch.empty((S, G, D), dtype=torch.bfloat16, device=q.device) if dk is None else dk
-    dv = torch.empty((S, G, D), dtype=torch.bfloat16, device=q.device) if dv is None else dv
-    ins = [_heads(dout, "dout", T, H, D), _heads(q, "q"), _heads(k, "k", dim=D), _heads(v, "v", S, G, D),
-           _heads(out, "out", T, H, D)]
-    outs = [_heads(dq, "dq", T, H, D), _heads(dk, "dk", S, G, D), _heads(dv, "dv", S, G, D)]
-    _on_current_device(lse, "lse")
-    if lse.dtype != torch.float32 or tuple(lse.shape) != (H, T) or not lse.is_contiguous():
+    dev = q.get_device()
+    shape = _attention_shape(q, k, causal, scale, cu_q, cu_k, dev)
+    T, H, D = qs = q.shape
+    ks = (k.shape[0], k.shape[1], D)
+    ins = [_heads(dout, "dout", qs, dev), _heads(q, "q", qs, dev), _heads(k, "k", ks, dev), _heads(v, "v", ks, dev),
+           _heads(out, "out", qs, dev)]
+    if lse.dtype != torch.float32 or lse.shape != (H, T) or not lse.is_contiguous():
         raise _invalid(f"lse must be contiguous float32 [{H}, {T}]")
+    _on(lse, "lse", dev)
+    stream = _here(dev)
+    dq = q.new_empty(qs) if dq is None else dq
+    dk = q.new_empty(ks) if dk is None else dk
+    dv = q.new_empty(ks) if dv is None else dv
     lib = L.lib()
-    ws = _workspace(int(lib.nvfp4_attention_backward_workspace_bytes(ctypes.byref(shape))))
-    st = lib.nvfp4_attention_backward(ctypes.byref(shape), *(ctypes.byref(a) for a in ins), _ptr(lse),
-                                      *(ctypes.byref(a) for a in outs), ws.data_ptr(), ws.numel(),
-                                      dev_status(q.device).data_ptr(), _stream())
-    L.check(st, "nvfp4_attention_backward")
+    ws = _workspace(lib.nvfp4_attention_backward_workspace_bytes(shape), dev, stream)
+    st = lib.nvfp4_attention_backward(shape, *ins, lse.data_ptr(), _heads(dq, "dq", qs, dev), _heads(dk, "dk", ks, dev),
+                                      _heads(dv, "dv", ks, dev), ws.data_ptr(), ws.numel(), _status_ptr(dev), stream)
+    if st:
+        L.check(st, "nvfp4_attention_backward")
     return dq, dk, dv
 
 
@@ -227,7 +267,7 @@ class AdamW:
         if len(decay) != n:
             raise NVFP4Error(L.ERR_SHAPE, "weight_decay must be one number or one per parameter")
         for i, p in enumerate(self.params):
-            _on_current_device(p, f"params[{i}]")
+            _on(p, f"params[{i}]", torch.cuda.current_device())
             if p.dtype not in _DT or not p.is_contiguous():
                 raise _invalid(f"params[{i}] must be contiguous float32 or bfloat16")
         if self.params and any(p.device != self.params[0].device for p in self.params):
@@ -258,6 +298,13 @@ class AdamW:
                 p.data_ptr(), None, self.state["m"][i].data_ptr(), self.state["v"][i].data_ptr(),
                 self.state["m_scale"][i].data_ptr() if bits == 8 else None,
                 self.state["v_scale"][i].data_ptr() if bits == 8 else None, p.numel(), _DT[p.dtype], 0, d, i)
+        # the descriptors' fields that change from step to step, as words of the same memory
+        words = (ctypes.c_uint64 * (ctypes.sizeof(self._tensors) // 8)).from_buffer(self._tensors)
+        halves = (ctypes.c_int32 * (ctypes.sizeof(self._tensors) // 4)).from_buffer(self._tensors)
+        size, T = ctypes.sizeof(L.AdamWTensorC), L.AdamWTensorC
+        self._words, self._halves = words, halves
+        self._grad_at = [(i * size + T.grad.offset) // 8 for i in range(n)]
+        self._dtype_at = [(i * size + T.grad_dtype.offset) // 4 for i in range(n)]
 
     def step(self, grads: Sequence[Optional[torch.Tensor]], lr: float, betas: Tuple[float, float] = (0.9, 0.95),
              eps: float = 1e-8, grad_scale: Optional[torch.Tensor] = None, round: int = L.SR, sr_seed: int = 0) -> None:
@@ -265,27 +312,29 @@ class AdamW:
         (None leaves that parameter and its state alone).  ``grad_scale``: a one-element float32 CUDA tensor
         that multiplies every gradient (loss scale, clipping) without a host read.  ``round`` (RNE
         or SR with ``sr_seed``) is how 8-bit states and bfloat16 parameters are rounded."""
-        if len(grads) != len(self.params):
-            raise NVFP4Error(L.ERR_SHAPE, f"{len(grads)} gradients for {len(self.params)} parameters")
-        if not self.params:
+        params = self._kept[0]
+        if len(grads) != len(params):
+            raise NVFP4Error(L.ERR_SHAPE, f"{len(grads)} gradients for {len(params)} parameters")
+        if not params:
             return
-        dev = self.params[0].device
-        if torch.cuda.current_device() != dev.index:
-            raise _invalid("the parameters are not on the current CUDA device")
-        if grad_scale is not None and (grad_scale.device != dev or grad_scale.dtype != torch.float32
+        dev = params[0].get_device()
+        stream = _here(dev)
+        if grad_scale is not None and (grad_scale.get_device() != dev or grad_scale.dtype != torch.float32
                                        or grad_scale.numel() != 1):
             raise _invalid("grad_scale must be one float32 on the parameters' device")
-        for i, (g, p, ptr, t, shape) in enumerate(zip(grads, self._kept[0], self._ptrs, self._tensors, self._shapes)):
-            if p.data_ptr() != ptr:
-                raise _invalid(f"params[{i}] has other storage than when the optimizer was made")
+        if [p.data_ptr() for p in params] != self._ptrs:
+            raise _invalid("a parameter has other storage than when the optimizer was made")
+        words, halves = self._words, self._halves
+        for i, (g, shape, at, kind) in enumerate(zip(grads, self._shapes, self._grad_at, self._dtype_at)):
             if g is None:
-                t.grad = None
+                words[at] = 0
                 continue
-            if g.shape != shape or g.dtype not in _DT or g.device != dev or not g.is_contiguous():
+            code = _DT.get(g.dtype)
+            if code is None or g.shape != shape or g.get_device() != dev or not g.is_contiguous():
                 raise _invalid(f"grads[{i}] must be contiguous float32 or bfloat16 {list(shape)} beside its parameter")
-            t.grad, t.grad_dtype = g.data_ptr(), _DT[g.dtype]
+            words[at] = g.data_ptr()
+            halves[kind] = code
         hp = L.AdamWParams(self.bits, round, self.steps + 1, lr, betas[0], betas[1], eps, sr_seed & (2**64 - 1))
-        st = L.lib().nvfp4_adamw_step(self._tensors, len(self.params), ctypes.byref(hp), _ptr(grad_scale),
-                                      dev_status(dev).data_ptr(), _stream())
+        st = L.lib().nvfp4_adamw_step(self._tensors, len(params), hp, _ptr(grad_scale), _status_ptr(dev), stream)
         L.check(st, "nvfp4_adamw_step")
         self.steps += 1
