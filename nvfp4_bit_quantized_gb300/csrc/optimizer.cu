@@ -37,6 +37,7 @@ struct AdamwConsts {
     float b1, c1, b2, c2;                      // beta, 1 - beta
     float size, unbias, eps;                   // lr / (1 - b1^t), 1 / sqrt(1 - b2^t)
     uint32_t step;
+    float one;                                 // 1, where the compiler must not know it
     const float* grad_scale;
     uint32_t* dev_status;
     PhiloxKey key;
@@ -116,31 +117,55 @@ template <bool SR> __device__ __forceinline__ float to_bf16(float v, uint32_t ra
     return __uint_as_float(b & 0xFFFF0000u);
 }
 
-// E4M3 code of x, without its sign.  2^-120 x has the grid's exponents, subnormals included, as fp32's
-// own: the code is the word's top bits, 20 bits below them deciding the rounding.
-template <bool SR> __device__ __forceinline__ uint32_t to_e4m3(float x, uint32_t rand16) {
-    const uint32_t b = __float_as_uint(__fmul_rn(fabsf(x), 0x1p-120f));
-    const uint32_t up = SR ? rand16 << 4 : 0x7FFFFu + ((b >> 20) & 1u);
-    return min((b + up) >> 20, 126u);
-}
-__device__ __forceinline__ float from_e4m3(uint32_t code) {
-    return __fmul_rn(__uint_as_float(((code & 0x80u) << 24) | ((code & 0x7Fu) << 20)), 0x1p120f);
+// Two fp32 operations at once.  The assembler contracts a packed product with a packed sum that follows it, both
+// marked .rn or not (61660 of 262144 random pairs came out as fused ones), so a sum is written as a * 1 + b with a 1
+// that it does not know.
+__device__ __forceinline__ float2 mul2(float2 a, float b) { return __fmul2_rn(a, make_float2(b, b)); }
+__device__ __forceinline__ float2 add2(const float one, float2 a, float2 b) { return __ffma2_rn(a, make_float2(one, one), b); }
+
+// max of magnitudes; NaN wins
+__device__ __forceinline__ float max_abs(float a, float b) {
+    float r;
+    asm("{\n\t.reg .f32 t;\n\tabs.f32 t, %2;\n\tmax.NaN.f32 %0, %1, t;\n\t}" : "=f"(r) : "f"(a), "f"(b));
+    return r;
 }
 
-__device__ __forceinline__ void update(const AdamwConsts& k, float g, float keep, float& p, float& m, float& v) {
-    m = __fadd_rn(__fmul_rn(m, k.b1), __fmul_rn(g, k.c1));
-    v = __fadd_rn(__fmul_rn(v, k.b2), __fmul_rn(__fmul_rn(g, g), k.c2));
-    p = __fsub_rn(__fmul_rn(p, keep),
-                  __fdiv_rn(__fmul_rn(m, k.size), __fadd_rn(__fmul_rn(__fsqrt_rn(v), k.unbias), k.eps)));
+// Two E4M3 codes (the low 16 bits) as values.
+__device__ __forceinline__ float2 from_e4m3x2(uint32_t codes) {
+    uint32_t h;
+    const uint16_t in = (uint16_t)codes;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(in));
+    return __half22float2(*reinterpret_cast<const __half2*>(&h));
+}
+// The E4M3 code of a magnitude x >= 0 in the top byte.  2^-120 x has the grid's exponents, subnormals
+// included, as fp32's own: the code is the word's bits 20 .. 27, the 20 bits below them deciding the rounding.
+// `scaled`: 2^-120 x; rand: 16 random bits at bits 4 .. 19.
+template <bool SR> __device__ __forceinline__ uint32_t to_e4m3_top(float scaled, uint32_t rand, uint32_t least) {
+    const uint32_t b = __float_as_uint(scaled) & 0x7FFFFFFFu;
+    const uint32_t up = SR ? rand : 0x7FFFFu + ((b >> 20) & 1u);
+    return max(min(b + up, (126u << 20) | 0xFFFFFu), least) << 4;
+}
+// The top bytes of four words, first in the lowest byte.
+__device__ __forceinline__ uint32_t top_bytes(uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
+    return __byte_perm(__byte_perm(a, b, 0x0073), __byte_perm(c, d, 0x0073), 0x5410);
+}
+
+__device__ __forceinline__ void update2(const AdamwConsts& k, float2 g, float keep, float2& p, float2& m, float2& v) {
+    m = add2(k.one, mul2(m, k.b1), mul2(g, k.c1));
+    v = add2(k.one, mul2(v, k.b2), mul2(__fmul2_rn(g, g), k.c2));
+    const float2 num = mul2(m, k.size);
+    const float2 den = add2(k.one, mul2(make_float2(__fsqrt_rn(v.x), __fsqrt_rn(v.y)), k.unbias), make_float2(k.eps, k.eps));
+    const float2 q = make_float2(-__fdiv_rn(num.x, den.x), -__fdiv_rn(num.y, den.y));
+    p = add2(k.one, mul2(p, keep), q);
 }
 
 __device__ __forceinline__ float inverse_of(float top) {
     return top > 0.0f ? fminf(__fdiv_rn(448.0f, top), FLT_MAX) : 0.0f;
 }
-// max of non-negative values by their bits (NaN above all others) over the 16 threads of a block
-__device__ __forceinline__ uint32_t max16(uint32_t v) {
+// the largest over the 16 threads of a block; NaN wins
+__device__ __forceinline__ float max16(float v) {
 #pragma unroll
-    for (int d = 8; d; d >>= 1) v = max(v, __shfl_xor_sync(~0u, v, d));
+    for (int d = 8; d; d >>= 1) v = max_abs(v, __shfl_xor_sync(~0u, v, d));
     return v;
 }
 
@@ -181,18 +206,18 @@ __global__ void __launch_bounds__(kThreads, BITS == 32 ? 4 : 3) adamw_kernel(con
             rm[q].load(mc + i * (SB / 8));
             rv[q].load(vc + i * (SB / 8));
         }
-        if (BITS == 8 && i < n) {
-            sm[q] = t.m_scale[i / kBlock];
-            sv[q] = t.v_scale[i / kBlock];
+        if (BITS == 8) {
+            sm[q] = i < n ? t.m_scale[i / kBlock] : 0.0f;
+            sv[q] = i < n ? t.v_scale[i / kBlock] : 0.0f;
         }
     }
-    uint32_t worst = 0;                                    // the largest gradient, for the finite check
+    float2 finite = make_float2(0.0f, 0.0f);               // sums 0 * g: NaN once a gradient is not finite
 #pragma unroll
     for (int q = 0; q < kRounds; ++q) {
         const int64_t i = base + q * (kThreads * kPer);
         const bool full = t.vec && i + kPer <= n;
         float p[8] = {}, g[8] = {}, m[8] = {}, v[8] = {};
-        uint32_t cm[2], cv[2];
+        uint32_t cm[2] = {}, cv[2] = {};
         if (full) {
             get8(rp[q], p);
             get8(rg[q], g);
@@ -204,7 +229,6 @@ __global__ void __launch_bounds__(kThreads, BITS == 32 ? 4 : 3) adamw_kernel(con
                 cv[0] = rv[q].a.x; cv[1] = rv[q].a.y;
             }
         } else {
-            cm[0] = cm[1] = cv[0] = cv[1] = 0u;
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 if (i + e < n) {
@@ -219,19 +243,19 @@ __global__ void __launch_bounds__(kThreads, BITS == 32 ? 4 : 3) adamw_kernel(con
                     }
                 }
         }
-        if constexpr (BITS == 8) {
-            const float a = i < n ? sm[q] : 0.0f, b = i < n ? sv[q] : 0.0f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                m[e] = __fmul_rn(from_e4m3(cm[e >> 2] >> (8 * (e & 3))), a);
-                v[e] = __fmul_rn(from_e4m3(cv[e >> 2] >> (8 * (e & 3))), b);
+        for (int e = 0; e < 8; e += 2) {
+            float2 p2 = make_float2(p[e], p[e + 1]), m2 = make_float2(m[e], m[e + 1]), v2 = make_float2(v[e], v[e + 1]);
+            if constexpr (BITS == 8) {
+                m2 = mul2(from_e4m3x2(cm[e >> 2] >> (8 * (e & 2))), sm[q]);
+                v2 = mul2(from_e4m3x2(cv[e >> 2] >> (8 * (e & 2))), sv[q]);
             }
-        }
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            g[e] = __fmul_rn(g[e], gs);
-            worst = max(worst, __float_as_uint(g[e]) & 0x7FFFFFFFu);
-            update(k, g[e], keep, p[e], m[e], v[e]);
+            const float2 g2 = mul2(make_float2(g[e], g[e + 1]), gs);
+            finite = __ffma2_rn(g2, make_float2(0.0f, 0.0f), finite);
+            update2(k, g2, keep, p2, m2, v2);
+            p[e] = p2.x; p[e + 1] = p2.y;
+            m[e] = m2.x; m[e + 1] = m2.y;
+            v[e] = v2.x; v[e + 1] = v2.y;
         }
         // a bf16 parameter's random words, stream 1; words of elements 4 j .. 4 j + 3 from one call
         if constexpr (sizeof(P) == 2) {
@@ -244,33 +268,39 @@ __global__ void __launch_bounds__(kThreads, BITS == 32 ? 4 : 3) adamw_kernel(con
             for (int e = 0; e < 8; ++e) p[e] = to_bf16<SR>(p[e], w[e >> 2].w[e & 3] & 0xFFFFu);
         }
         if constexpr (BITS == 8) {
-            uint32_t tm = 0, tv = 0;
+            // past the tensor's end everything is zero: it takes no part in the largest values
+            float topm = 0.0f, topv = 0.0f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
-                // past the tensor's end everything is zero: it takes no part in the largest value
-                tm = max(tm, __float_as_uint(m[e]) & 0x7FFFFFFFu);
-                tv = max(tv, __float_as_uint(v[e]) & 0x7FFFFFFFu);
+                topm = max_abs(topm, m[e]);
+                topv = max_abs(topv, v[e]);
             }
-            const float topm = __uint_as_float(max16(tm)), topv = __uint_as_float(max16(tv));
+            topm = max16(topm);
+            topv = max16(topv);
             if ((threadIdx.x & 15) == 0 && i < n) {
                 t.m_scale[i / kBlock] = __fmul_rn(topm, 1.0f / 448.0f);
                 t.v_scale[i / kBlock] = __fmul_rn(topv, 1.0f / 448.0f);
             }
             const float im = inverse_of(topm), iv = inverse_of(topv);
-            Philox4 w[2] = {};
-            if constexpr (SR) {
-                w[0] = words_of(k, i, 2 * t.id);
-                w[1] = words_of(k, i + 4, 2 * t.id);
-            }
-            cm[0] = cm[1] = cv[0] = cv[1] = 0u;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t r = w[e >> 2].w[e & 3], sign = __float_as_uint(m[e]) >> 31;
-                const uint32_t a = to_e4m3<SR>(__fmul_rn(m[e], im), r & 0xFFFFu) | sign << 7;
-                uint32_t b = to_e4m3<SR>(__fmul_rn(v[e], iv), r >> 16);
-                if (v[e] > 0.0f) b = max(b, 1u);
-                cm[e >> 2] |= a << (8 * (e & 3));
-                cv[e >> 2] |= b << (8 * (e & 3));
+            for (int h = 0; h < 2; ++h) {
+                Philox4 w = {};
+                if constexpr (SR) w = words_of(k, i + 4 * h, 2 * t.id);
+                uint32_t a[4], b[4];
+#pragma unroll
+                for (int e = 0; e < 4; e += 2) {
+                    const int f = 4 * h + e;
+                    const float2 x = mul2(mul2(make_float2(m[f], m[f + 1]), im), 0x1p-120f);
+                    const float2 y = mul2(mul2(make_float2(v[f], v[f + 1]), iv), 0x1p-120f);
+                    a[e] = to_e4m3_top<SR>(x.x, (w.w[e] << 4) & 0xFFFF0u, 0u);
+                    a[e + 1] = to_e4m3_top<SR>(x.y, (w.w[e + 1] << 4) & 0xFFFF0u, 0u);
+                    b[e] = to_e4m3_top<SR>(y.x, (w.w[e] >> 12) & 0xFFFF0u, v[f] > 0.0f ? 1u << 20 : 0u);
+                    b[e + 1] = to_e4m3_top<SR>(y.y, (w.w[e + 1] >> 12) & 0xFFFF0u, v[f + 1] > 0.0f ? 1u << 20 : 0u);
+                }
+                const uint32_t sign = top_bytes(__float_as_uint(m[4 * h]), __float_as_uint(m[4 * h + 1]),
+                                                __float_as_uint(m[4 * h + 2]), __float_as_uint(m[4 * h + 3]));
+                cm[h] = top_bytes(a[0], a[1], a[2], a[3]) | (sign & 0x80808080u);
+                cv[h] = top_bytes(b[0], b[1], b[2], b[3]);
             }
         }
         if (full) {
@@ -298,7 +328,7 @@ __global__ void __launch_bounds__(kThreads, BITS == 32 ? 4 : 3) adamw_kernel(con
                 }
         }
     }
-    if (worst >= 0x7F800000u) set_status(k.dev_status, NVFP4_ERR_NONFINITE);
+    if (!(finite.x + finite.y == 0.0f)) set_status(k.dev_status, NVFP4_ERR_NONFINITE);
 }
 
 bool known(int32_t t) { return t == NVFP4_F32 || t == NVFP4_BF16; }
@@ -405,6 +435,7 @@ extern "C" nvfp4_status nvfp4_adamw_step(const nvfp4_adamw_tensor* tensors, int3
     k.unbias = (float)(1.0 / std::sqrt(1.0 - std::pow(hp->beta2, (double)hp->step)));
     k.eps = (float)hp->eps;
     k.step = (uint32_t)hp->step;
+    k.one = 1.0f;
     k.grad_scale = grad_scale;
     k.dev_status = dev_status;
     k.key = philox_key(hp->sr_seed);
