@@ -10,7 +10,7 @@
 // zero: a denominator rounded to zero would blow the next step up.
 //
 // One launch for many tensors: their descriptors are the kernel's parameter (no table to copy to the
-// device), a block takes 4096 neighbouring elements of one tensor and finds it by bisection.  Bound by
+// device), a block takes 2048 or 4096 neighbouring elements of one tensor and finds it by bisection.  Bound by
 // memory: 26 bytes an element with fp32 parameters and states and bf16 gradients, 14.1 with 8-bit
 // states.  A thread takes 8 neighbouring elements with 16-byte accesses, 16 threads an 8-bit state's
 // block; tensors that do not lie on 16 bytes, and a tensor's last elements, go one by one.
@@ -29,9 +29,14 @@ using bf16 = __nv_bfloat16;
 
 constexpr int kBlock = 128;                    // elements with one scale
 constexpr int kThreads = 256, kPer = 8;        // a thread's elements at a time
-constexpr int kRounds = 2;
-constexpr int kSlice = kThreads * kPer * kRounds;      // elements of a CUDA block
-static_assert(kSlice % kBlock == 0 && kBlock == 16 * kPer, "an 8-bit block is 16 threads' elements");
+// Rounds of a CUDA block, their loads all issued first: 32-bit states bring enough bytes with one (272 M parameters: 998
+// us, 1085 with two), 8-bit ones want two (751 us; 768 .. 825 with one).  Four blocks an SM for both (8-bit with
+// three: 800 us).
+template <int BITS> struct Slice {
+    static constexpr int kRounds = BITS == 32 ? 1 : 2;
+    static constexpr int kElements = kThreads * kPer * kRounds;
+};
+static_assert(Slice<8>::kElements % kBlock == 0 && kBlock == 16 * kPer, "an 8-bit block is 16 threads' elements");
 
 struct AdamwConsts {
     float b1, c1, b2, c2;                      // beta, 1 - beta
@@ -170,7 +175,7 @@ __device__ __forceinline__ float max16(float v) {
 }
 
 template <typename P, typename G, int BITS, bool SR, int MAX>
-__global__ void __launch_bounds__(kThreads, BITS == 32 ? 4 : 3) adamw_kernel(const __grid_constant__ Batch<MAX> batch) {
+__global__ void __launch_bounds__(kThreads, 4) adamw_kernel(const __grid_constant__ Batch<MAX> batch) {
     pdl_launch_dependents();
     pdl_wait();
     // the tensor of this slice: the last that begins at or before it
@@ -185,11 +190,12 @@ __global__ void __launch_bounds__(kThreads, BITS == 32 ? 4 : 3) adamw_kernel(con
     const float gs = k.grad_scale ? *k.grad_scale : 1.0f;
     P* param = static_cast<P*>(t.param);
     const G* grad = static_cast<const G*>(t.grad);
+    constexpr int kRounds = Slice<BITS>::kRounds;
     constexpr int SB = BITS == 32 ? 32 : 8;                // bytes of eight elements of a state
     constexpr int PB = 8 * sizeof(P), GB = 8 * sizeof(G);
     const int64_t n = t.n;
     const float keep = t.keep;
-    const int64_t base = (int64_t)(blockIdx.x - t.first_slice) * kSlice + threadIdx.x * kPer;
+    const int64_t base = (int64_t)(blockIdx.x - t.first_slice) * Slice<BITS>::kElements + threadIdx.x * kPer;
     uint8_t *mc = static_cast<uint8_t*>(t.m), *vc = static_cast<uint8_t*>(t.v);
 
     // all rounds' loads first
@@ -362,6 +368,7 @@ cudaError_t step_types(const nvfp4_adamw_tensor* ts, int count, const nvfp4_adam
     b.k = k;
     b.count = 0;
     int64_t slices = 0;
+    const int64_t slice = hp.bits == 32 ? Slice<32>::kElements : Slice<8>::kElements;
     cudaError_t e = cudaSuccess;
     auto flush = [&] {
         if (b.count && e == cudaSuccess) e = launch<P, G, MAX>(b, hp.bits, hp.round == NVFP4_ROUND_SR, (unsigned)slices, s);
@@ -371,7 +378,7 @@ cudaError_t step_types(const nvfp4_adamw_tensor* ts, int count, const nvfp4_adam
     for (int i = 0; i < count; ++i) {
         const nvfp4_adamw_tensor& a = ts[i];
         if (a.n == 0 || !a.grad || a.param_dtype != pt || a.grad_dtype != gt) continue;
-        const int64_t mine = (a.n + kSlice - 1) / kSlice;  // at most 2^28
+        const int64_t mine = (a.n + slice - 1) / slice;    // at most 2^29
         if (b.count == MAX || slices + mine > (1ll << 30)) flush();
         const size_t state = hp.bits == 32 ? 16 : 8;
         const bool vec = aligned16(a.param) && aligned16(a.grad) && aligned_to(a.m, state) && aligned_to(a.v, state);
