@@ -72,45 +72,41 @@ struct Item {
     int rows, other_len, diag;
 };
 
-__device__ __forceinline__ void seq_bounds(const int32_t* cu, int s, int64_t total, int64_t& a, int64_t& b) {
-    if (!cu) {
-        a = 0;
-        b = total;
-        return;
-    }
-    a = min(max((int64_t)cu[s], (int64_t)0), total);       // in range whatever the offsets hold
-    b = min(max((int64_t)cu[s + 1], a), total);
-}
-
 // Whole warp: the tile and head of this CTA.  Tiles are numbered through the sequences; CTAs take
 // the last first (with a causal mask the longest of a sequence, of queries; of keys the other way
 // round), heads fastest, so that CTAs that run together read the same K and V.
 __device__ __forceinline__ void find_item(const Params& p, bool rows_are_q, int tile, int heads, Item* out) {
     const int lane = threadIdx.x & 31;
-    const int32_t* cu = rows_are_q ? p.cu_q : p.cu_k;
-    const int64_t total = rows_are_q ? p.tq : p.tk;
-    const int head = blockIdx.x % heads;
-    int64_t n = 0;                                         // tiles in all
+    const int32_t *cu = rows_are_q ? p.cu_q : p.cu_k, *cu_other = rows_are_q ? p.cu_k : p.cu_q;
+    const int64_t total = rows_are_q ? p.tq : p.tk, total_other = rows_are_q ? p.tk : p.tq;
+    // The lane's sequence of the present 32: its rows, the other side's, its tiles.  Offsets that break the rules are
+    // forced into range and reported.
+    int64_t a = 0, b = 0, oa = 0, ob = 0, tiles = 0;
     bool bad = false;
-    for (int s0 = 0; s0 < p.nseq; s0 += 32) {
+    auto bounds = [&](const int32_t* o, int s, int64_t all, int64_t& lo, int64_t& hi) {
+        const int64_t x = o ? o[s] : 0, y = o ? o[s + 1] : all;
+        bad |= x > y || (s == 0 && x != 0) || (s == p.nseq - 1 && y != all);
+        lo = min(max(x, (int64_t)0), all);
+        hi = min(max(y, lo), all);
+    };
+    auto load = [&](int s0) {
         const int s = s0 + lane;
-        int64_t tiles = 0;
+        a = b = oa = ob = tiles = 0;
         if (s < p.nseq) {
-            int64_t a, b;
-            seq_bounds(cu, s, total, a, b);
+            bounds(cu, s, total, a, b);
+            bounds(cu_other, s, total_other, oa, ob);
             tiles = (b - a + tile - 1) / tile;
-            if (p.cu_q && blockIdx.x == 0)
-                for (int w = 0; w < 2; ++w) {
-                    const int32_t* o = w ? p.cu_k : p.cu_q;
-                    bad |= o[s] > o[s + 1] || (s == 0 && o[0] != 0) ||
-                           (s == p.nseq - 1 && o[p.nseq] != (w ? p.tk : p.tq));
-                }
         }
+    };
+    int64_t n = 0;                                         // tiles in all
+    for (int s0 = 0; s0 < p.nseq; s0 += 32) {
+        load(s0);
+        int64_t sum = tiles;
 #pragma unroll
-        for (int d = 16; d; d >>= 1) tiles += __shfl_xor_sync(~0u, tiles, d);
-        n += tiles;
+        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+        n += sum;
     }
-    if (bad) set_status(p.dev_status, NVFP4_ERR_INVALID_ARG);
+    if (bad && blockIdx.x == 0) set_status(p.dev_status, NVFP4_ERR_INVALID_ARG);
     int64_t want = blockIdx.x / heads;
     if (rows_are_q) want = n - 1 - want;
     if (want < 0 || want >= n) {
@@ -118,10 +114,7 @@ __device__ __forceinline__ void find_item(const Params& p, bool rows_are_q, int 
         return;
     }
     for (int s0 = 0; s0 < p.nseq; s0 += 32) {
-        const int s = s0 + lane;
-        int64_t a = 0, b = 0;
-        if (s < p.nseq) seq_bounds(cu, s, total, a, b);
-        const int64_t tiles = (b - a + tile - 1) / tile;
+        if (p.nseq > 32) load(s0);                         // up to 32 sequences are still at hand
         int64_t upto = tiles;                              // inclusive prefix
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
@@ -130,10 +123,8 @@ __device__ __forceinline__ void find_item(const Params& p, bool rows_are_q, int 
         }
         if (want >= upto - tiles && want < upto) {
             const int64_t t0 = (want - (upto - tiles)) * tile;
-            int64_t oa, ob;
-            seq_bounds(rows_are_q ? p.cu_k : p.cu_q, s, rows_are_q ? p.tk : p.tq, oa, ob);
             out->valid = 1;
-            out->head = head;
+            out->head = blockIdx.x % heads;
             out->first = a + t0;
             out->rows = (int)min((int64_t)tile, b - a - t0);
             out->other = oa;

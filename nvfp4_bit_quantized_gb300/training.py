@@ -102,9 +102,10 @@ def layer_norm_forward(x: torch.Tensor, weight: torch.Tensor, bias: Optional[tor
     h, ldr = None, 0
     if residual is not None:
         ldr = _matrix(residual, "residual", shape, dtype, dev)
-        h = x.new_empty(shape)
-    y = x.new_empty(shape, dtype=out_dtype)
-    mean, rstd = x.new_empty(R, dtype=torch.float32), x.new_empty(R, dtype=torch.float32)
+        h = torch.empty(shape, dtype=dtype, device=x.device)
+    y = torch.empty(shape, dtype=out_dtype, device=x.device)
+    mean = torch.empty(R, dtype=torch.float32, device=x.device)
+    rstd = torch.empty(R, dtype=torch.float32, device=x.device)
     st = L.lib().nvfp4_layer_norm_forward(x.data_ptr(), _DT[dtype], R, C, ldx, _ptr(residual), ldr, w, b, _DT[weight.dtype],
                                           eps, y.data_ptr(), _DT[out_dtype], C, _ptr(h), C, mean.data_ptr(),
                                           rstd.data_ptr(), stream)
@@ -132,9 +133,9 @@ def layer_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
     w = _vector(weight, "weight", C, _DT, dev)
     m, s = _vector(mean, "mean", R, _F32_ONLY, dev), _vector(rstd, "rstd", R, _F32_ONLY, dev)
     stream = _here(dev)
-    dx = h.new_empty(shape)
-    dw = h.new_empty(C, dtype=torch.float32)
-    db = h.new_empty(C, dtype=torch.float32) if bias else None
+    dx = torch.empty(shape, dtype=dtype, device=h.device)
+    dw = torch.empty(C, dtype=torch.float32, device=h.device)
+    db = torch.empty(C, dtype=torch.float32, device=h.device) if bias else None
     lib = L.lib()
     ws = _workspace(lib.nvfp4_layer_norm_backward_workspace_bytes(R, C), dev, stream)
     st = lib.nvfp4_layer_norm_backward(dy.data_ptr(), _DT[dy.dtype], lddy, h.data_ptr(), _DT[dtype], R, C, ldx, w,
@@ -199,9 +200,9 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal:
     a, b, c = _heads(q, "q", qs, dev), _heads(k, "k", ks, dev), _heads(v, "v", ks, dev)
     stream = _here(dev)
     if out is None:
-        out = q.new_empty(qs)
+        out = torch.empty(qs, dtype=torch.bfloat16, device=q.device)
     d = _heads(out, "out", qs, dev)
-    lse = q.new_empty((H, T), dtype=torch.float32)
+    lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
     st = L.lib().nvfp4_attention_forward(shape, a, b, c, d, lse.data_ptr(), _status_ptr(dev), stream)
     if st:
         L.check(st, "nvfp4_attention_forward")
@@ -226,9 +227,9 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
         raise _invalid(f"lse must be contiguous float32 [{H}, {T}]")
     _on(lse, "lse", dev)
     stream = _here(dev)
-    dq = q.new_empty(qs) if dq is None else dq
-    dk = q.new_empty(ks) if dk is None else dk
-    dv = q.new_empty(ks) if dv is None else dv
+    dq = torch.empty(qs, dtype=torch.bfloat16, device=q.device) if dq is None else dq
+    dk = torch.empty(ks, dtype=torch.bfloat16, device=q.device) if dk is None else dk
+    dv = torch.empty(ks, dtype=torch.bfloat16, device=q.device) if dv is None else dv
     lib = L.lib()
     ws = _workspace(lib.nvfp4_attention_backward_workspace_bytes(shape), dev, stream)
     st = lib.nvfp4_attention_backward(shape, *ins, lse.data_ptr(), _heads(dq, "dq", qs, dev), _heads(dk, "dk", ks, dev),
