@@ -527,7 +527,20 @@ NVFP4_API nvfp4_status nvfp4_attention_forward(const nvfp4_attention_shape* shap
                                                const nvfp4_heads* k, const nvfp4_heads* v, const nvfp4_heads* out,
                                                float* lse, uint32_t* dev_status, void* stream);
 
-/* Workspace bytes nvfp4_attention_backward needs. */
+/*
+ * nvfp4_attention_forward_ws -- nvfp4_attention_forward that may share a tile of queries' keys among
+ * several multiprocessors when there are few tiles (few queries over many keys): each leaves the output
+ * and lse of its keys in `workspace` (device memory, 16-byte aligned, any contents, at least
+ * nvfp4_attention_forward_workspace_bytes bytes on the current device), and a second kernel joins them
+ * in a fixed order, in fp32.  workspace NULL: exactly nvfp4_attention_forward.
+ */
+NVFP4_API size_t nvfp4_attention_forward_workspace_bytes(const nvfp4_attention_shape* shape);
+NVFP4_API nvfp4_status nvfp4_attention_forward_ws(const nvfp4_attention_shape* shape, const nvfp4_heads* q,
+                                                  const nvfp4_heads* k, const nvfp4_heads* v, const nvfp4_heads* out,
+                                                  float* lse, void* workspace, size_t workspace_bytes,
+                                                  uint32_t* dev_status, void* stream);
+
+/* Workspace bytes nvfp4_attention_backward needs on the current device. */
 NVFP4_API size_t nvfp4_attention_backward_workspace_bytes(const nvfp4_attention_shape* shape);
 
 /*
@@ -536,8 +549,9 @@ NVFP4_API size_t nvfp4_attention_backward_workspace_bytes(const nvfp4_attention_
  *   dv = P^T dout;  dS = P (dP - delta) scale;  dq = dS k;  dk = dS^T q
  * (dk and dv summed over the query heads of a key head; P and dS rounded to BF16 for the products,
  * sums in fp32).  out and lse are the forward call's.  dq, dk, dv are laid out like q, k, v, with
- * strides of their own, and must not overlap one another or the inputs.  No atomics: results are
- * deterministic.  workspace: device memory, 16-byte aligned, any contents.
+ * strides of their own, and must not overlap one another or the inputs.  Where there are few tiles
+ * of queries or of keys, several multiprocessors share one and their fp32 sums are joined in a fixed
+ * order.  No atomics: results are deterministic.  workspace: device memory, 16-byte aligned, any contents.
  */
 NVFP4_API nvfp4_status nvfp4_attention_backward(const nvfp4_attention_shape* shape, const nvfp4_heads* dout,
                                                 const nvfp4_heads* q, const nvfp4_heads* k, const nvfp4_heads* v,

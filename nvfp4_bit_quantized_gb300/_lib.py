@@ -26,7 +26,8 @@ EXPORTS = [
     "nvfp4_sqrelu_maxima_bytes", "nvfp4_gemm_sqrelu_maxima", "nvfp4_quantize_dual_sqrelu_premax",
     "nvfp4_gemm_sqrelu_bwd_maxima", "nvfp4_quantize_dual_premax",
     "nvfp4_layer_norm_forward", "nvfp4_layer_norm_backward_workspace_bytes", "nvfp4_layer_norm_backward",
-    "nvfp4_attention_forward", "nvfp4_attention_backward_workspace_bytes", "nvfp4_attention_backward",
+    "nvfp4_attention_forward", "nvfp4_attention_forward_workspace_bytes", "nvfp4_attention_forward_ws",
+    "nvfp4_attention_backward_workspace_bytes", "nvfp4_attention_backward",
     "nvfp4_adamw_step",
 ]
 
@@ -133,6 +134,8 @@ def lib():
             "nvfp4_layer_norm_backward": (I32, [P, I32, I64, P, I32, I64, I64, I64, P, I32, P, P, P, I64, P, I64,
                                                 P, P, P, SZ, P]),
             "nvfp4_attention_forward": (I32, [AS, HD, HD, HD, HD, P, P, P]),
+            "nvfp4_attention_forward_workspace_bytes": (SZ, [AS]),
+            "nvfp4_attention_forward_ws": (I32, [AS, HD, HD, HD, HD, P, P, SZ, P, P]),
             "nvfp4_attention_backward_workspace_bytes": (SZ, [AS]),
             "nvfp4_attention_backward": (I32, [AS, HD, HD, HD, HD, HD, P, HD, HD, HD, P, SZ, P, P]),
             "nvfp4_adamw_step": (I32, [P, I32, c.POINTER(AdamWParams), P, P, P]),

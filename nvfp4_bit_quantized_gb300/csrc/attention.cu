@@ -60,6 +60,8 @@ struct Params {
     const int32_t *cu_q, *cu_k;
     uint32_t* dev_status;
     uint64_t timeout_ns;
+    int parts;                                 // CTAs that share a tile's steps
+    float *part_sums, *part_lse;               // what they leave, parts > 1: [parts][..., tokens, heads, dim], [parts][heads, tq]
 };
 
 // One CTA's rows.  `first` .. first + rows - 1 are its tile's tokens of one sequence; the other
@@ -76,7 +78,7 @@ struct Item {
 // the last first (with a causal mask the longest of a sequence, of queries; of keys the other way
 // round), heads fastest, so that CTAs that run together read the same K and V.
 __device__ __forceinline__ void find_item(const Params& p, bool rows_are_q, int tile, int heads, Item* out) {
-    const int lane = threadIdx.x & 31;
+    const int lane = threadIdx.x & 31, block = p.parts > 1 ? blockIdx.x / p.parts : blockIdx.x;
     const int32_t *cu = rows_are_q ? p.cu_q : p.cu_k, *cu_other = rows_are_q ? p.cu_k : p.cu_q;
     const int64_t total = rows_are_q ? p.tq : p.tk, total_other = rows_are_q ? p.tk : p.tq;
     // The lane's sequence of the present 32: its rows, the other side's, its tiles.  Offsets that break the rules are
@@ -107,7 +109,7 @@ __device__ __forceinline__ void find_item(const Params& p, bool rows_are_q, int 
         n += sum;
     }
     if (bad && blockIdx.x == 0) set_status(p.dev_status, NVFP4_ERR_INVALID_ARG);
-    int64_t want = blockIdx.x / heads;
+    int64_t want = block / heads;
     if (rows_are_q) want = n - 1 - want;
     if (want < 0 || want >= n) {
         if (lane == 0) out->valid = 0;
@@ -124,7 +126,7 @@ __device__ __forceinline__ void find_item(const Params& p, bool rows_are_q, int 
         if (want >= upto - tiles && want < upto) {
             const int64_t t0 = (want - (upto - tiles)) * tile;
             out->valid = 1;
-            out->head = blockIdx.x % heads;
+            out->head = block % heads;
             out->first = a + t0;
             out->rows = (int)min((int64_t)tile, b - a - t0);
             out->other = oa;
@@ -250,6 +252,31 @@ __device__ __forceinline__ void store32(bf16* row, int col, int dim, const uint3
             *reinterpret_cast<uint4*>(row + col + i) = make_uint4(w[0], w[1], w[2], w[3]);
         }
 }
+// The same in fp32: a part's row.
+__device__ __forceinline__ void store32(float* row, int col, int dim, const uint32_t (&v)[32], float f) {
+#pragma unroll
+    for (int i = 0; i < 32; i += 4)
+        if (col + i < dim)
+            *reinterpret_cast<float4*>(row + col + i) =
+                make_float4(__uint_as_float(v[i]) * f, __uint_as_float(v[i + 1]) * f, __uint_as_float(v[i + 2]) * f,
+                            __uint_as_float(v[i + 3]) * f);
+}
+__device__ __forceinline__ void store_zeros(float* row, int dim) {
+    for (int i = 0; i < dim; i += 4) *reinterpret_cast<float4*>(row + i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+}
+// This part's steps of `steps`.
+struct Share {
+    int first, count;
+    __device__ __forceinline__ Share(const Params& p, int steps) {
+        first = 0;
+        count = steps;
+        if (p.parts > 1) {                                 // the divisions take longer than some tiles' steps
+            const int part = blockIdx.x % p.parts;
+            first = (int)((int64_t)steps * part / p.parts);
+            count = (int)((int64_t)steps * (part + 1) / p.parts) - first;
+        }
+    }
+};
 __device__ __forceinline__ void store_zeros(bf16* row, int dim) {
     for (int i = 0; i < dim; i += 8) *reinterpret_cast<uint4*>(row + i) = make_uint4(0, 0, 0, 0);
 }
@@ -325,8 +352,10 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
             n[t] = rows[t] ? (keys + kRows - 1) / kRows : 0;
         }
     }
-    n[0] = uniform(n[0]);
-    n[1] = uniform(n[1]);
+    const Share mine(p, max(n[0], n[1]));
+    const int j0 = uniform(mine.first);                    // the key tiles j0 .. j0 + steps - 1 are this CTA's
+    n[0] = uniform(max(0, min(n[0] - j0, mine.count)));
+    n[1] = uniform(max(0, min(n[1] - j0, mine.count)));
     steps = max(n[0], n[1]);
 
     // inside the roles' own branches: code after a join is compiled for the smaller share
@@ -342,7 +371,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
                 const int slot = i % ST;
                 if (i >= ST && !wait(&empty[slot], i / ST - 1)) break;
                 mbar_arrive_expect_tx(&full[slot], TILE);
-                load_tile<HD>(ring + slot * TILE, (i & 1) ? &tmv : &tmk, item.other + (int64_t)(i >> 1) * kRows, hk, &full[slot]);
+                load_tile<HD>(ring + slot * TILE, (i & 1) ? &tmv : &tmk, item.other + (int64_t)(j0 + (i >> 1)) * kRows, hk, &full[slot]);
             }
             if (i < 2 * steps) {                           // aborted: the copies in flight land first
                 wait.drain(&q_full, 0);
@@ -360,7 +389,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
         const uint32_t ts = uniform(tmem + 128 * t), to = ts + 256;
         // waits for tile i (K of step 0, V of step 0, K of step 1, ...); both warps zero its foreign rows
         auto tile = [&](int i) {
-            const int valid = len - (i >> 1) * kRows;
+            const int valid = len - (j0 + (i >> 1)) * kRows;
             if (!wait.all(&full[i % ST], i / ST)) return false;
             if (valid < kRows && neighbours) zero_tail<HD>(ring + (i % ST) * TILE, valid);
             return true;
@@ -418,8 +447,8 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
             ld_wait();
 #pragma unroll
             for (int i = 0; i < 4; ++i) fence32(s[i]);
-            if ((j + 1) * kRows > common) {
-                const int lim = limit - j * kRows;
+            if ((j0 + j + 1) * kRows > common) {
+                const int lim = limit - (j0 + j) * kRows;
 #pragma unroll
                 for (int i = 0; i < 128; ++i)
                     if (i >= lim) s[i >> 5][i & 31] = 0xFF800000u;
@@ -477,21 +506,27 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
         }
         if (ok && rows[t] > 0) {                           // whole warps: the TMEM loads are collective
             const bool store = r < rows[t];
-            bf16* dst = p.out.at(item.first + (store ? row : 0), item.head);
+            const int64_t tok = item.first + (store ? row : 0), at = (int64_t)item.head * p.tq + tok;
+            const int part = blockIdx.x % p.parts;
+            bf16* dst = p.out.at(tok, item.head);
+            float* sum = p.part_sums + (((int64_t)part * p.tq + tok) * p.heads + item.head) * p.dim;
             const float inv = l == 0.0f ? 0.0f : 1.0f / l;
             if (n[t] == 0) {
-                if (store) store_zeros(dst, p.dim);
+                if (store && p.parts == 1) store_zeros(dst, p.dim);
+                if (store && p.parts > 1) store_zeros(sum, p.dim);
             } else {
                 for (int i = 0; i < p.dim; i += 32) {
                     uint32_t o[32];
                     ld32(to + i, o);
                     ld_wait();
                     fence32(o);
-                    if (store) store32(dst, i, p.dim, o, inv);
+                    if (store && p.parts == 1) store32(dst, i, p.dim, o, inv);
+                    if (store && p.parts > 1) store32(sum, i, p.dim, o, inv);
                 }
             }
             if (store)
-                p.lse[(int64_t)item.head * p.tq + item.first + row] = l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
+                (p.parts == 1 ? p.lse : p.part_lse + (int64_t)part * p.heads * p.tq)[at] =
+                    l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
     }
     fence_before();
@@ -566,7 +601,9 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         const int keys = p.causal ? min(item.other_len, max(0, item.rows + item.diag)) : item.other_len;
         steps = (keys + kRows - 1) / kRows;
     }
-    steps = uniform(steps);
+    const Share mine(p, steps);
+    const int j0 = uniform(mine.first);                    // the key tiles j0 .. j0 + steps - 1 are this CTA's
+    steps = uniform(mine.count);
 
     if (warp == 8 && steps > 0) {
         if (lane == 0) {
@@ -577,11 +614,11 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             for (int j = 0; j < steps; ++j) {
                 if (j >= 3 && !wait(&k_empty[j % 3], j / 3 - 1)) break;
                 mbar_arrive_expect_tx(&k_full[j % 3], TILE);
-                load_tile<HD>(ring_k + (j % 3) * TILE, &tmk, item.other + (int64_t)j * kRows, hk, &k_full[j % 3]);
+                load_tile<HD>(ring_k + (j % 3) * TILE, &tmk, item.other + (int64_t)(j0 + j) * kRows, hk, &k_full[j % 3]);
                 got_k = j + 1;
                 if (j >= 2 && !wait(&v_empty[j & 1], j / 2 - 1)) break;
                 mbar_arrive_expect_tx(&v_full[j & 1], TILE);
-                load_tile<HD>(ring_v + (j & 1) * TILE, &tmv, item.other + (int64_t)j * kRows, hk, &v_full[j & 1]);
+                load_tile<HD>(ring_v + (j & 1) * TILE, &tmv, item.other + (int64_t)(j0 + j) * kRows, hk, &v_full[j & 1]);
                 got_v = j + 1;
             }
             if (got_v < steps) {                           // aborted: the copies in flight land first
@@ -598,7 +635,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         const uint32_t desc_q = uniform(desc_k_major(smem_addr(smem_q)));
         const uint32_t desc_k = uniform(desc_k_major(smem_addr(ring_k))), desc_kt = uniform(desc_mn_major(smem_addr(ring_k)));
         auto issue_s = [&](int j) {
-            const int slot = j % 3, valid = len - j * kRows;
+            const int slot = j % 3, valid = len - (j0 + j) * kRows;
             if (!wait.all(&k_full[slot], j / 3)) return false;
             if (valid < kRows && neighbours) zero_tail<HD>(ring_k + slot * TILE, valid);
             mma_heads<HD>(tmem + 128 * (j & 1), desc_q, desc_k + slot * (TILE >> 4), ksteps, idesc_s);
@@ -704,8 +741,8 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                 x = __fmul2_rn(pr, __fadd2_rn(x, delta2));
                 w[i >> 1] = pack_bf16(x.x, x.y);
             }
-            if ((j + 1) * kRows > common) {                // masked pairs count for nothing, whatever they hold
-                const int lim = limit - j * kRows - 64 * half;
+            if ((j0 + j + 1) * kRows > common) {                // masked pairs count for nothing, whatever they hold
+                const int lim = limit - (j0 + j) * kRows - 64 * half;
 #pragma unroll
                 for (int i = 0; i < 32; ++i) {
                     if (2 * i >= lim) w[i] = 0u;
@@ -719,8 +756,10 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             if (lane == 0) mbar_arrive(&ds_ready[j & 1]);
         }
         bf16* dst = p.dq.at(tok, item.head);
+        float* sum = p.part_sums + (((int64_t)(blockIdx.x % p.parts) * p.tq + tok) * p.heads + item.head) * p.dim;
         if (steps == 0) {
-            if (in && half == 0) store_zeros(dst, p.dim);
+            if (in && half == 0 && p.parts == 1) store_zeros(dst, p.dim);
+            if (in && half == 0 && p.parts > 1) store_zeros(sum, p.dim);
         } else if (ok) {
             ok = wait(&mma_done[0], 0);
             fence_after();
@@ -730,7 +769,8 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                     ld32(tmem + 384 + i + lanes, v);
                     ld_wait();
                     fence32(v);
-                    if (in) store32(dst, i, p.dim, v, p.scale);
+                    if (in && p.parts == 1) store32(dst, i, p.dim, v, p.scale);
+                    if (in && p.parts > 1) store32(sum, i, p.dim, v, p.scale);
                 }
         }
     }
@@ -821,7 +861,8 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
         tiles = max(0, (item.other_len + kRows - 1) / kRows - first_tile);
         steps = tiles * share;
     }
-    steps = uniform(steps);
+    const Share mine(p, steps);
+    steps = uniform(mine.count);
     first_tile = uniform(first_tile);
     // the steps in order: the query tiles of the first head, of the second, ...
     struct Step {
@@ -833,7 +874,8 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
             }
         }
     };
-    const Step begin{uniform(item.head) * share, 0, uniform(tiles)};
+    const int ahead = mine.first > 0 ? mine.first / tiles : 0;
+    const Step begin{uniform(item.head * share + ahead), uniform(mine.first - ahead * tiles), uniform(tiles)};
     auto row_of = [&](const Step& s) { return (first_tile + s.tile) * kRows; };
 
     if (warp == 8 && steps > 0) {
@@ -1039,8 +1081,11 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
         const bool in = r < item.rows;
         const int64_t tok = item.first + (in ? r : 0);
         bf16* dst = half ? p.dk.at(tok, item.head) : p.dv.at(tok, item.head);
+        // parts: [part][dV, dK][tk, kv_heads, dim]
+        float* sum = p.part_sums + (((int64_t)(2 * (blockIdx.x % p.parts) + half) * p.tk + tok) * p.kv_heads + item.head) * p.dim;
         if (steps == 0) {
-            if (in) store_zeros(dst, p.dim);
+            if (in && p.parts == 1) store_zeros(dst, p.dim);
+            if (in && p.parts > 1) store_zeros(sum, p.dim);
         } else if (ok) {
             ok = wait(&ctl.mma_done[half], 0);
             fence_after();
@@ -1050,7 +1095,8 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
                     ld32(tmem + 256 + 128 * half + i + lanes, v);
                     ld_wait();
                     fence32(v);
-                    if (in) store32(dst, i, p.dim, v, half ? p.scale : 1.0f);
+                    if (in && p.parts == 1) store32(dst, i, p.dim, v, half ? p.scale : 1.0f);
+                    if (in && p.parts > 1) store32(sum, i, p.dim, v, half ? p.scale : 1.0f);
                 }
         }
     }
@@ -1060,6 +1106,56 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
         fence_after();
         tmem_free_all(tmem);
     }
+}
+
+// ---------------------------------------------------------------------------- joins
+// What the parts of a tile left, added in their order; a thread takes 8 elements of a token and head.  dK and dV: blockIdx.y
+// says which.
+constexpr int kJoinThreads = 256;
+
+__device__ __forceinline__ void add8(float (&s)[8], const float* p, float f) {
+    const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+    s[0] += f * a.x; s[1] += f * a.y; s[2] += f * a.z; s[3] += f * a.w;
+    s[4] += f * b.x; s[5] += f * b.y; s[6] += f * b.z; s[7] += f * b.w;
+}
+__device__ __forceinline__ void store8(bf16* dst, const float (&s)[8]) {
+    *reinterpret_cast<uint4*>(dst) = make_uint4(pack_bf16(s[0], s[1]), pack_bf16(s[2], s[3]), pack_bf16(s[4], s[5]), pack_bf16(s[6], s[7]));
+}
+
+__global__ void __launch_bounds__(kJoinThreads) join_sums_kernel(const float* sums, int parts, int64_t part_stride, int64_t which_stride,
+                                                                 int64_t tokens, int heads, int dim, Heads first, Heads second) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int groups = dim / 8;
+    const int64_t i = blockIdx.x * (int64_t)kJoinThreads + threadIdx.x;
+    if (i >= tokens * heads * groups) return;
+    const float* p = sums + blockIdx.y * which_stride + i * 8;
+    float s[8] = {};
+    for (int k = 0; k < parts; ++k) add8(s, p + k * part_stride, 1.0f);
+    const int64_t th = i / groups;
+    store8((blockIdx.y ? second : first).at(th / heads, (int)(th % heads)) + (i % groups) * 8, s);
+}
+
+// Forward: each part's output is that of its keys alone; their weights are exp(lse of the part - lse of all).
+__global__ void __launch_bounds__(kJoinThreads) join_out_kernel(const Params p) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int groups = p.dim / 8;
+    const int64_t i = blockIdx.x * (int64_t)kJoinThreads + threadIdx.x, part_stride = p.tq * p.heads * p.dim;
+    if (i >= p.tq * p.heads * groups) return;
+    const int64_t th = i / groups, tok = th / p.heads;
+    const int h = (int)(th % p.heads);
+    const float* lse = p.part_lse + h * p.tq + tok;
+    const int64_t lse_stride = p.heads * p.tq;
+    float top = -INFINITY, total = 0.0f;
+    for (int k = 0; k < p.parts; ++k) top = fmaxf(top, lse[k * lse_stride]);
+    const float ref = top == -INFINITY ? 0.0f : top;
+    for (int k = 0; k < p.parts; ++k) total += expf(lse[k * lse_stride] - ref);
+    float s[8] = {};
+    const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+    for (int k = 0; k < p.parts; ++k) add8(s, p.part_sums + k * part_stride + i * 8, expf(lse[k * lse_stride] - ref) * inv);
+    store8(p.out.at(tok, h) + (i % groups) * 8, s);
+    if (i % groups == 0) p.lse[h * p.tq + tok] = total == 0.0f ? -INFINITY : ref + logf(total);
 }
 
 // ---------------------------------------------------------------------------- host
@@ -1120,7 +1216,8 @@ nvfp4_status check_shape(const nvfp4_attention_shape* s) {
         return NVFP4_ERR_SHAPE;
     if (s->nseq < 1 || (!s->cu_q) != (!s->cu_k) || (!s->cu_q && s->nseq != 1) || !std::isfinite(s->scale))
         return NVFP4_ERR_INVALID_ARG;
-    if ((std::max(s->tq, s->tk) / kRows + s->nseq) * s->heads > INT_MAX) return NVFP4_ERR_SHAPE;   // the largest grid
+    if ((std::max(s->tq, s->tk) / kRows + s->nseq) * s->heads > INT_MAX) return NVFP4_ERR_SHAPE;   // the largest grid (parts only
+                                                                                                 // where it is small)
     if ((reinterpret_cast<uintptr_t>(s->cu_q) | reinterpret_cast<uintptr_t>(s->cu_k)) % 4) return NVFP4_ERR_ALIGNMENT;
     return NVFP4_OK;
 }
@@ -1154,6 +1251,7 @@ Params params_of(const nvfp4_attention_shape* s, uint32_t* dev_status) {
     p.cu_k = s->cu_k;
     p.dev_status = dev_status;
     p.timeout_ns = wait_timeout_ns();
+    p.parts = 1;
     return p;
 }
 
@@ -1161,15 +1259,50 @@ Params params_of(const nvfp4_attention_shape* s, uint32_t* dev_status) {
 int64_t tiles_of(int64_t tokens, int nseq, int tile) {
     return nseq == 1 ? (tokens + tile - 1) / tile : tokens / tile + nseq;
 }
+int sms() {
+    int dev = 0;
+    return cudaGetDevice(&dev) == cudaSuccess ? std::max(1, sm_count(dev)) : 1;
+}
+
+// How many CTAs share a tile's steps.  Tiles of queries, forward and dQ: where fewer than half the SMs have one, as many
+// as fill them.  Tiles of keys: each is a whole head group's work, so that few of them balance badly too; there the
+// aim is three a SM.  A part costs a tile of fp32 sums written and read: a CTA keeps at least 4 steps, of keys' tiles with
+// their two sums 8 (4096 tokens in 20 documents, 20 / 4 heads of 128, 10 steps a tile: backward 93 us, 111 in parts of 5).
+// 64 queries over 7000 keys, 8 / 2 heads of 128: forward 70 -> 19 us; 8192 tokens, 8 / 1 heads: backward 715 -> 325 us.
+int parts_for(int64_t ctas, int64_t steps, int64_t wanted, int least) {
+    if (ctas < 1 || 2 * ctas > wanted) return 1;
+    return (int)std::max<int64_t>(1, std::min<int64_t>({wanted / ctas, steps / least, 64}));
+}
+int64_t tile_steps(int64_t tokens, int nseq) { return (tokens / nseq + kRows - 1) / kRows; }
+int parts_of_fwd(const nvfp4_attention_shape* s) {
+    return parts_for(tiles_of(s->tq, s->nseq, 2 * kRows) * s->heads, tile_steps(s->tk, s->nseq), sms(), 4);
+}
+int parts_of_dq(const nvfp4_attention_shape* s) {
+    return parts_for(tiles_of(s->tq, s->nseq, kRows) * s->heads, tile_steps(s->tk, s->nseq), sms(), 4);
+}
+int parts_of_dkv(const nvfp4_attention_shape* s) {
+    return parts_for(tiles_of(s->tk, s->nseq, kRows) * s->kv_heads,
+                     tile_steps(s->tq, s->nseq) * (s->heads / s->kv_heads), 3 * sms(), 8);
+}
+size_t sums_bytes(int parts, int64_t tokens, int heads, int dim) {
+    return parts > 1 ? (size_t)parts * tokens * heads * dim * sizeof(float) : 0;
+}
+size_t delta_bytes(const nvfp4_attention_shape* s) {       // a multiple of 16
+    return ((size_t)s->heads * (size_t)s->tq * sizeof(float) + 15) / 16 * 16 + 16;
+}
+unsigned join_blocks(int64_t tokens, int heads, int dim) {
+    return (unsigned)((tokens * heads * (dim / 8) + kJoinThreads - 1) / kJoinThreads);
+}
 
 }  // namespace attn
 }  // namespace nvfp4
 
 using namespace nvfp4;
 
-extern "C" nvfp4_status nvfp4_attention_forward(const nvfp4_attention_shape* shape, const nvfp4_heads* q,
-                                                const nvfp4_heads* k, const nvfp4_heads* v, const nvfp4_heads* out,
-                                                float* lse, uint32_t* dev_status, void* stream) {
+namespace {
+nvfp4_status forward_impl(const nvfp4_attention_shape* shape, const nvfp4_heads* q, const nvfp4_heads* k,
+                          const nvfp4_heads* v, const nvfp4_heads* out, float* lse, void* workspace,
+                          size_t workspace_bytes, uint32_t* dev_status, void* stream) {
     using namespace attn;
     nvfp4_status st = check_shape(shape);
     if (st == NVFP4_OK) st = check_heads(q, shape->tq, shape->heads, shape->dim);
@@ -1183,21 +1316,54 @@ extern "C" nvfp4_status nvfp4_attention_forward(const nvfp4_attention_shape* sha
     Params p = params_of(shape, dev_status);
     p.out = heads_of(out);
     p.lse = lse;
+    if (workspace) {
+        if (!aligned16(workspace) || workspace_bytes < nvfp4_attention_forward_workspace_bytes(shape)) return NVFP4_ERR_WORKSPACE;
+        p.parts = parts_of_fwd(shape);
+        p.part_sums = static_cast<float*>(workspace);
+        p.part_lse = p.part_sums + sums_bytes(p.parts, p.tq, p.heads, p.dim) / sizeof(float);
+    }
     CUtensorMap mq, mk, mv;
     if (!make_map(&mq, q, p.tq, p.heads, p.dim) || !make_map(&mk, k, p.tk, p.kv_heads, p.dim) ||
         !make_map(&mv, v, p.tk, p.kv_heads, p.dim))
         return NVFP4_ERR_CUDA;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int64_t grid = tiles_of(p.tq, p.nseq, 2 * kRows) * p.heads;
+    const int64_t grid = tiles_of(p.tq, p.nseq, 2 * kRows) * p.heads * p.parts;
     if (!(p.dim <= 64 ? fwd_registers_fit<64>() : fwd_registers_fit<128>())) return NVFP4_ERR_CUDA;
-    const cudaError_t e = p.dim <= 64 ? launch(fwd_kernel<64>, Fwd<64>::SMEM, kFwdThreads, grid, s, mq, mk, mv, p)
-                                      : launch(fwd_kernel<128>, Fwd<128>::SMEM, kFwdThreads, grid, s, mq, mk, mv, p);
+    cudaError_t e = p.dim <= 64 ? launch(fwd_kernel<64>, Fwd<64>::SMEM, kFwdThreads, grid, s, mq, mk, mv, p)
+                                : launch(fwd_kernel<128>, Fwd<128>::SMEM, kFwdThreads, grid, s, mq, mk, mv, p);
+    if (e == cudaSuccess && p.parts > 1)
+        e = launch_pdl(join_out_kernel, dim3(join_blocks(p.tq, p.heads, p.dim)), dim3(kJoinThreads), 0, s, p);
     return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
+}
+}  // namespace
+
+extern "C" nvfp4_status nvfp4_attention_forward(const nvfp4_attention_shape* shape, const nvfp4_heads* q,
+                                                const nvfp4_heads* k, const nvfp4_heads* v, const nvfp4_heads* out,
+                                                float* lse, uint32_t* dev_status, void* stream) {
+    return forward_impl(shape, q, k, v, out, lse, nullptr, 0, dev_status, stream);
+}
+
+extern "C" size_t nvfp4_attention_forward_workspace_bytes(const nvfp4_attention_shape* shape) {
+    using namespace attn;
+    if (check_shape(shape) != NVFP4_OK) return 0;
+    const int parts = parts_of_fwd(shape);
+    return parts == 1 ? 16 : sums_bytes(parts, shape->tq, shape->heads, shape->dim) +
+                                 (size_t)parts * shape->heads * shape->tq * sizeof(float);
+}
+
+extern "C" nvfp4_status nvfp4_attention_forward_ws(const nvfp4_attention_shape* shape, const nvfp4_heads* q,
+                                                   const nvfp4_heads* k, const nvfp4_heads* v, const nvfp4_heads* out,
+                                                   float* lse, void* workspace, size_t workspace_bytes,
+                                                   uint32_t* dev_status, void* stream) {
+    return forward_impl(shape, q, k, v, out, lse, workspace, workspace_bytes, dev_status, stream);
 }
 
 extern "C" size_t nvfp4_attention_backward_workspace_bytes(const nvfp4_attention_shape* shape) {
-    if (attn::check_shape(shape) != NVFP4_OK) return 0;
-    return (size_t)shape->heads * (size_t)std::max<int64_t>(shape->tq, 4) * sizeof(float);
+    using namespace attn;
+    if (check_shape(shape) != NVFP4_OK) return 0;
+    // delta, then the parts' sums of one kernel at a time
+    return delta_bytes(shape) + std::max(sums_bytes(parts_of_dq(shape), shape->tq, shape->heads, shape->dim),
+                                         2 * sums_bytes(parts_of_dkv(shape), shape->tk, shape->kv_heads, shape->dim));
 }
 
 extern "C" nvfp4_status nvfp4_attention_backward(const nvfp4_attention_shape* shape, const nvfp4_heads* dout,
@@ -1230,14 +1396,25 @@ extern "C" nvfp4_status nvfp4_attention_backward(const nvfp4_attention_shape* sh
         !make_map(&mv, v, p.tk, p.kv_heads, p.dim) || !make_map(&mdo, dout, p.tq, p.heads, p.dim))
         return NVFP4_ERR_CUDA;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int64_t grid_q = tiles_of(p.tq, p.nseq, kRows) * p.heads, grid_k = tiles_of(p.tk, p.nseq, kRows) * p.kv_heads;
+    p.part_sums = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + delta_bytes(shape));
     cudaError_t e = cudaSuccess;
-    if (p.dim <= 64) {
-        if (p.tq > 0) e = launch(dq_kernel<64>, Dq<64>::PAD, kDqThreads, grid_q, s, mq, mk, mv, mdo, p);
-        if (e == cudaSuccess && p.tk > 0) e = launch(dkv_kernel<64>, Dkv<64>::SMEM, kDkvThreads, grid_k, s, mq, mk, mv, mdo, p);
-    } else {
-        if (p.tq > 0) e = launch(dq_kernel<128>, Dq<128>::PAD, kDqThreads, grid_q, s, mq, mk, mv, mdo, p);
-        if (e == cudaSuccess && p.tk > 0) e = launch(dkv_kernel<128>, Dkv<128>::SMEM, kDkvThreads, grid_k, s, mq, mk, mv, mdo, p);
+    if (p.tq > 0) {
+        p.parts = parts_of_dq(shape);
+        const int64_t grid = tiles_of(p.tq, p.nseq, kRows) * p.heads * p.parts;
+        e = p.dim <= 64 ? launch(dq_kernel<64>, Dq<64>::PAD, kDqThreads, grid, s, mq, mk, mv, mdo, p)
+                        : launch(dq_kernel<128>, Dq<128>::PAD, kDqThreads, grid, s, mq, mk, mv, mdo, p);
+        if (e == cudaSuccess && p.parts > 1)
+            e = launch_pdl(join_sums_kernel, dim3(join_blocks(p.tq, p.heads, p.dim)), dim3(kJoinThreads), 0, s, p.part_sums,
+                           p.parts, p.tq * p.heads * p.dim, 0, p.tq, p.heads, p.dim, p.dq, p.dq);
+    }
+    if (e == cudaSuccess && p.tk > 0) {
+        p.parts = parts_of_dkv(shape);
+        const int64_t grid = tiles_of(p.tk, p.nseq, kRows) * p.kv_heads * p.parts, sums = p.tk * p.kv_heads * p.dim;
+        e = p.dim <= 64 ? launch(dkv_kernel<64>, Dkv<64>::SMEM, kDkvThreads, grid, s, mq, mk, mv, mdo, p)
+                        : launch(dkv_kernel<128>, Dkv<128>::SMEM, kDkvThreads, grid, s, mq, mk, mv, mdo, p);
+        if (e == cudaSuccess && p.parts > 1)
+            e = launch_pdl(join_sums_kernel, dim3(join_blocks(p.tk, p.kv_heads, p.dim), 2), dim3(kJoinThreads), 0, s,
+                           p.part_sums, p.parts, 2 * sums, sums, p.tk, p.kv_heads, p.dim, p.dv, p.dk);
     }
     return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
 }

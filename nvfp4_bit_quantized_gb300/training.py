@@ -203,9 +203,12 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal:
         out = torch.empty(qs, dtype=torch.bfloat16, device=q.device)
     d = _heads(out, "out", qs, dev)
     lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
-    st = L.lib().nvfp4_attention_forward(shape, a, b, c, d, lse.data_ptr(), _status_ptr(dev), stream)
+    lib = L.lib()
+    ws = _workspace(lib.nvfp4_attention_forward_workspace_bytes(shape), dev, stream)
+    st = lib.nvfp4_attention_forward_ws(shape, a, b, c, d, lse.data_ptr(), ws.data_ptr(), ws.numel(), _status_ptr(dev),
+                                        stream)
     if st:
-        L.check(st, "nvfp4_attention_forward")
+        L.check(st, "nvfp4_attention_forward_ws")
     return out, lse
 
 

@@ -122,6 +122,35 @@ def test_every_head_size(nv, D):
     run_and_check(nv, q, k, v, dout, True, None, [0, 190], [0, 190], False)
 
 
+@pytest.mark.parametrize("T,S,H,G,D", [(1, 5000, 2, 1, 128), (130, 4100, 4, 2, 64), (4100, 130, 4, 1, 128), (2500, 2500, 8, 1, 64),
+                                       (300, 2049, 1, 1, 40), (2049, 1, 3, 1, 72)])
+@pytest.mark.parametrize("causal", [False, True])
+def test_few_tiles_with_many_steps(nv, T, S, H, G, D, causal):
+    """Several multiprocessors share a tile's steps: parts of every length, some of them masked away whole."""
+    q, k, v, dout = make(T, S, H, G, D, T + S)
+    run_and_check(nv, q, k, v, dout, causal, None, [0, T], [0, S], False)
+    o = [0, T // 3, T // 3, T]
+    oks = [0, S // 7, S // 2, S]
+    run_and_check(nv, q, k, v, dout, causal, None, o, oks, True)
+
+
+def test_forward_without_a_workspace_is_the_same_attention(nv):
+    import ctypes
+    from nvfp4_bit_quantized_gb300 import _lib as L
+    q, k, v, dout = make(70, 3000, 2, 2, 64, 3)
+    out, lse = nv.attention_forward(q, k, v)
+    o2, l2 = torch.empty_like(out), torch.empty_like(lse)
+    h = [L.HeadsC(x.data_ptr(), x.stride(0), x.stride(1)) for x in (q, k, v, o2)]
+    s = L.AttentionShapeC(70, 3000, 2, 2, 64, 0, 0.125, 1, None, None)
+    assert L.lib().nvfp4_attention_forward_workspace_bytes(ctypes.byref(s)) > 16      # the call above shared its tiles
+    st = L.lib().nvfp4_attention_forward(ctypes.byref(s), *(ctypes.byref(x) for x in h), l2.data_ptr(),
+                                         nv.dev_status().data_ptr(), torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    r = definition(q, k, v, dout, False, 0.125, [0, 70], [0, 3000])
+    check("out", o2, r)
+    assert torch.allclose(l2, lse, rtol=1e-5, atol=1e-5)
+
+
 PACKED = [([0, 1, 1, 130, 259, 300, 300], [0, 1, 1, 130, 259, 300, 300]),
           ([0, 0, 128, 256, 257, 700], [0, 64, 64, 320, 330, 500]),
           ([0, 5, 10, 15, 20, 25, 30, 35, 40], [0, 7, 14, 21, 28, 35, 42, 49, 56]),
