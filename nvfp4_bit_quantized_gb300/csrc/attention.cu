@@ -60,6 +60,7 @@ struct Params {
     const int32_t *cu_q, *cu_k;
     uint32_t* dev_status;
     uint64_t timeout_ns;
+    int work;                                  // tiles x heads x parts: what the CTAs go through
     int parts;                                 // CTAs that share a tile's steps
     float *part_sums, *part_lse;               // what they leave, parts > 1: [parts][..., tokens, heads, dim], [parts][heads, tq]
 };
@@ -68,7 +69,8 @@ struct Params {
 // side's sequence is `other` .. other + other_len - 1.  diag: row r of the tile faces other row
 // r + diag on the causal diagonal.
 struct Item {
-    int valid;
+    int valid;                                             // 0: nothing here; -1: no more work
+    int part;                                              // of the tile's steps, where CTAs share them
     int head;
     int64_t first, other;
     int rows, other_len, diag;
@@ -77,8 +79,8 @@ struct Item {
 // Whole warp: the tile and head of this CTA.  Tiles are numbered through the sequences; CTAs take
 // the last first (with a causal mask the longest of a sequence, of queries; of keys the other way
 // round), heads fastest, so that CTAs that run together read the same K and V.
-__device__ __forceinline__ void find_item(const Params& p, bool rows_are_q, int tile, int heads, Item* out) {
-    const int lane = threadIdx.x & 31, block = p.parts > 1 ? blockIdx.x / p.parts : blockIdx.x;
+__device__ __forceinline__ void find_item(const Params& p, bool rows_are_q, int tile, int heads, int work, Item* out) {
+    const int lane = threadIdx.x & 31, block = p.parts > 1 ? work / p.parts : work;
     const int32_t *cu = rows_are_q ? p.cu_q : p.cu_k, *cu_other = rows_are_q ? p.cu_k : p.cu_q;
     const int64_t total = rows_are_q ? p.tq : p.tk, total_other = rows_are_q ? p.tk : p.tq;
     // The lane's sequence of the present 32: its rows, the other side's, its tiles.  Offsets that break the rules are
@@ -108,7 +110,7 @@ __device__ __forceinline__ void find_item(const Params& p, bool rows_are_q, int 
         for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
         n += sum;
     }
-    if (bad && blockIdx.x == 0) set_status(p.dev_status, NVFP4_ERR_INVALID_ARG);
+    if (bad && work == 0) set_status(p.dev_status, NVFP4_ERR_INVALID_ARG);
     int64_t want = block / heads;
     if (rows_are_q) want = n - 1 - want;
     if (want < 0 || want >= n) {
@@ -126,6 +128,7 @@ __device__ __forceinline__ void find_item(const Params& p, bool rows_are_q, int 
         if (want >= upto - tiles && want < upto) {
             const int64_t t0 = (want - (upto - tiles)) * tile;
             out->valid = 1;
+            out->part = p.parts > 1 ? work - block * p.parts : 0;
             out->head = block % heads;
             out->first = a + t0;
             out->rows = (int)min((int64_t)tile, b - a - t0);
@@ -172,6 +175,59 @@ struct Wait {
     }
 };
 
+// A slot of a ring of N and the parity of its barriers' present phase.
+template <int N> struct Ring {
+    int slot = 0;
+    uint32_t phase = 0;
+    __device__ __forceinline__ void next() {
+        if (++slot == N) {
+            slot = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
+// The tiles that a CTA goes through, found one ahead by a warp of their own and read by `readers` others, which copy them.
+struct Queue {
+    Item item[2];
+    uint64_t full[2], empty[2];
+    __device__ __forceinline__ void init(int readers) {
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], readers);
+        }
+    }
+    // whole warp
+    __device__ __forceinline__ void feed(const Params& p, bool rows_are_q, int tile, int heads, const Wait& wait) {
+        Ring<2> r;
+        const int grid = gridDim.x;
+        for (int k = 0;; ++k) {
+            // to and fro: the CTA with the longest tile of one round has the shortest of the next
+            const int at = (k & 1) ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x, work = k * grid + at;
+            const bool more = work < p.work, last = (k + 1) * grid >= p.work;
+            if (!wait.all(&empty[r.slot], r.phase ^ 1u)) break;
+            if (more) find_item(p, rows_are_q, tile, heads, work, &item[r.slot]);
+            else if ((threadIdx.x & 31) == 0) item[r.slot].valid = -1;
+            __syncwarp();
+            if (!more && !last) continue;
+            if (more && item[r.slot].valid == 0) continue;         // the host counts sequences' last tiles generously
+            __syncwarp();
+            if ((threadIdx.x & 31) == 0) mbar_arrive(&full[r.slot]);
+            if (!more) break;
+            r.next();
+        }
+    }
+    // whole warp; false: no more, or aborted
+    __device__ __forceinline__ bool next(Ring<2>& r, const Wait& wait, Item& out) {
+        if (!wait.all(&full[r.slot], r.phase)) return false;
+        out = item[r.slot];
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) mbar_arrive(&empty[r.slot]);
+        r.next();
+        return out.valid > 0;
+    }
+};
+
 // The two MMA warps issue their groups of MMAs in turns, first (w = 0) and second (w = 1) of each round: the tensor
 // cores then work off one group after the other.  Groups issued at will run interleaved and end
 // together, and nothing is left to run while the softmax warps work on what both produced.
@@ -185,18 +241,6 @@ struct Turns {
     __device__ __forceinline__ void pass() const {
         if (elect_one()) mbar_arrive(&bar[w ^ 1]);
         __syncwarp();
-    }
-};
-
-// A slot of a ring of N and the parity of its barriers' present phase.
-template <int N> struct Ring {
-    int slot = 0;
-    uint32_t phase = 0;
-    __device__ __forceinline__ void next() {
-        if (++slot == N) {
-            slot = 0;
-            phase ^= 1u;
-        }
     }
 };
 
@@ -267,11 +311,10 @@ __device__ __forceinline__ void store_zeros(float* row, int dim) {
 // This part's steps of `steps`.
 struct Share {
     int first, count;
-    __device__ __forceinline__ Share(const Params& p, int steps) {
+    __device__ __forceinline__ Share(const Params& p, int part, int steps) {
         first = 0;
         count = steps;
         if (p.parts > 1) {                                 // the divisions take longer than some tiles' steps
-            const int part = blockIdx.x % p.parts;
             first = (int)((int64_t)steps * part / p.parts);
             count = (int)((int64_t)steps * (part + 1) / p.parts) - first;
         }
@@ -288,8 +331,12 @@ __device__ __forceinline__ uint8_t* align1024(uint8_t* p) {
 // ---------------------------------------------------------------------------- forward
 // Warps 0-3 and 4-7: the softmax of tile 0 and tile 1, a row per thread; warp 8: TMA; warps 9 and 10: the MMAs
 // of tile 0 and of tile 1 (one warp cannot issue MMAs of 64 cycles fast enough beside the softmax
-// warps).  While one tile's softmax runs, the tensor cores work on the other tile.  TMEM: S (then P, bf16, in its first 64
-// columns) of tile t at 128 t, O of tile t at 256 + 128 t.  O is rescaled only when a row's maximum has
+// warps); warp 11: the next tiles to work on.  While one tile's softmax runs, the tensor cores work on the
+// other tile.  A CTA stays for all its tiles: the next ones' queries and keys are loaded, and their first
+// scores computed, while the last ones' outputs are stored.  TMEM: S of tile t at 128 t.  HD = 128: P (bf16) in the
+// first 64 columns of S, O of tile t at 256 + 128 t.  HD = 64, where the softmax takes longer than the MMAs:
+// O at 256 + 64 t and P in columns of its own at 384 + 64 t, so that the next scores are computed as soon as
+// the present ones have been read, and a softmax follows the other without a pause.  O is rescaled only when a row's maximum has
 // grown by more than 2^8 since it was last taken: P stays below 2^8 and the final division by the
 // sum cancels the choice.
 // A softmax thread holds a row's 128 scores at once: registers move from the third warpgroup to its two.
@@ -300,6 +347,25 @@ template <int HD> struct Fwd {
     static constexpr int TILE = kRows * HD * 2;
     static constexpr int STAGES = HD == 128 ? 4 : 8;
     static constexpr int SMEM = (2 + STAGES) * TILE + 1024;
+    static constexpr bool OWN_P = HD == 64;                // P has columns of its own
+};
+
+// Rows and key tiles of an item's two query tiles: tile t takes the key tiles j0 .. j0 + n[t] - 1.
+struct FwdPlan {
+    int rows[2], n[2], j0, steps;
+    __device__ __forceinline__ FwdPlan(const Params& p, const Item& item) {
+        for (int t = 0; t < 2; ++t) {
+            rows[t] = min(max(item.rows - kRows * t, 0), kRows);
+            int keys = item.other_len;
+            if (p.causal) keys = min(keys, max(0, kRows * t + rows[t] + item.diag));
+            n[t] = rows[t] ? (keys + kRows - 1) / kRows : 0;
+        }
+        const Share mine(p, item.part, max(n[0], n[1]));
+        j0 = uniform(mine.first);
+        n[0] = uniform(max(0, min(n[0] - j0, mine.count)));
+        n[1] = uniform(max(0, min(n[1] - j0, mine.count)));
+        steps = max(n[0], n[1]);
+    }
 };
 
 template <int HD>
@@ -307,10 +373,13 @@ __global__ void __launch_bounds__(kFwdThreads, 1)
 fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
            const __grid_constant__ CUtensorMap tmv, const Params p) {
     constexpr int TILE = Fwd<HD>::TILE, ST = Fwd<HD>::STAGES;
+    constexpr bool OWN_P = Fwd<HD>::OWN_P;
+    constexpr int O_COLS = OWN_P ? 64 : 128;
     extern __shared__ uint8_t raw[];
-    __shared__ uint64_t q_full, full[ST], empty[ST], s_full[2], p_ready[2], o_full[2], turn[2], mma_done[2];
+    __shared__ uint64_t q_full, q_empty, full[ST], empty[ST], s_full[2], s_read[2], p_ready[2], pv_done[2], o_empty[2],
+        turn[2], mma_done[2];
     __shared__ uint32_t tmem_slot, abort_flag;
-    __shared__ Item item;
+    __shared__ Queue queue;
     uint8_t* smem_q = align1024(raw);
     uint8_t* ring = smem_q + 2 * TILE;
     const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
@@ -318,6 +387,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
         mbar_init(&q_full, 1);
+        mbar_init(&q_empty, 2);
         for (int i = 0; i < ST; ++i) {
             mbar_init(&full[i], 1);
             mbar_init(&empty[i], 2);
@@ -325,103 +395,172 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
         for (int t = 0; t < 2; ++t) {
             mbar_init(&s_full[t], 1);
             mbar_init(&p_ready[t], 4);
-            mbar_init(&o_full[t], 1);
+            mbar_init(&s_read[t], 4);
+            mbar_init(&pv_done[t], 1);
+            mbar_init(&o_empty[t], 4);
             mbar_init(&turn[t], 1);
             mbar_init(&mma_done[t], 1);
         }
+        queue.init(11);
         abort_flag = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
     if (warp == 9) tmem_alloc_all(&tmem_slot);
     pdl_wait();
-    if (warp == 8) find_item(p, true, 2 * kRows, p.heads, &item);
     fence_before();
     __syncthreads();
     fence_after();
     const uint32_t tmem = uniform(tmem_slot);
     const Wait wait{p.timeout_ns, &abort_flag, p.dev_status};
-    const int hk = item.head / (p.heads / p.kv_heads);
-
-    // rows and key tiles of each of the two query tiles
-    int rows[2] = {0, 0}, n[2] = {0, 0}, steps = 0;
-    if (item.valid) {
-        for (int t = 0; t < 2; ++t) {
-            rows[t] = min(max(item.rows - kRows * t, 0), kRows);
-            int keys = item.other_len;
-            if (p.causal) keys = min(keys, max(0, kRows * t + rows[t] + item.diag));
-            n[t] = rows[t] ? (keys + kRows - 1) / kRows : 0;
-        }
-    }
-    const Share mine(p, max(n[0], n[1]));
-    const int j0 = uniform(mine.first);                    // the key tiles j0 .. j0 + steps - 1 are this CTA's
-    n[0] = uniform(max(0, min(n[0] - j0, mine.count)));
-    n[1] = uniform(max(0, min(n[1] - j0, mine.count)));
-    steps = max(n[0], n[1]);
+    Ring<2> items;
+    Item item;
 
     // inside the roles' own branches: code after a join is compiled for the smaller share
     if (warp >= 8) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kFwdRegsOther));
-      if (warp == 8 && steps > 0) {
-        if (lane == 0) {
-            mbar_arrive_expect_tx(&q_full, TILE * (rows[1] ? 2 : 1));
-            load_tile<HD>(smem_q, &tmq, item.first, item.head, &q_full);
-            if (rows[1]) load_tile<HD>(smem_q + TILE, &tmq, item.first + kRows, item.head, &q_full);
-            int i = 0;                                     // K of step 0, V of step 0, K of step 1, ...
-            for (; i < 2 * steps; ++i) {
-                const int slot = i % ST;
-                if (i >= ST && !wait(&empty[slot], i / ST - 1)) break;
-                mbar_arrive_expect_tx(&full[slot], TILE);
-                load_tile<HD>(ring + slot * TILE, (i & 1) ? &tmv : &tmk, item.other + (int64_t)(j0 + (i >> 1)) * kRows, hk, &full[slot]);
+      if (warp == 11) {
+        queue.feed(p, true, 2 * kRows, p.heads, wait);
+      } else if (warp == 8) {
+        Ring<ST> r;
+        uint32_t loads = 0, queries = 0;                   // tiles and query pairs loaded
+        bool ok = true;
+        while (ok && queue.next(items, wait, item)) {
+            const FwdPlan plan(p, item);
+            if (plan.steps == 0) continue;
+            const int hk = item.head / (p.heads / p.kv_heads);
+            if (lane == 0) {
+                ok = wait(&q_empty, queries ^ 1u);
+                if (ok) {
+                    mbar_arrive_expect_tx(&q_full, TILE * (plan.rows[1] ? 2 : 1));
+                    load_tile<HD>(smem_q, &tmq, item.first, item.head, &q_full);
+                    if (plan.rows[1]) load_tile<HD>(smem_q + TILE, &tmq, item.first + kRows, item.head, &q_full);
+                    ++queries;
+                }
+                for (int i = 0; ok && i < 2 * plan.steps; ++i) {       // K of step 0, V of step 0, K of step 1, ...
+                    ok = wait(&empty[r.slot], r.phase ^ 1u);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&full[r.slot], TILE);
+                    load_tile<HD>(ring + r.slot * TILE, (i & 1) ? &tmv : &tmk,
+                                  item.other + (int64_t)(plan.j0 + (i >> 1)) * kRows, hk, &full[r.slot]);
+                    ++loads;
+                    r.next();
+                }
             }
-            if (i < 2 * steps) {                           // aborted: the copies in flight land first
-                wait.drain(&q_full, 0);
-                for (int j = max(0, i - ST); j < i; ++j) wait.drain(&full[j % ST], j / ST);
-            }
+            ok = __all_sync(~0u, ok);
         }
-    } else if ((warp == 9 || warp == 10) && steps > 0) {
-        const int t = warp - 9, nt = t ? n[1] : n[0];
+        if (lane == 0 && abort_flag) {                     // the copies in flight land first
+            if (queries) wait.drain(&q_full, (queries - 1) & 1u);
+            for (uint32_t j = loads > ST ? loads - ST : 0; j < loads; ++j) wait.drain(&full[j % ST], (j / ST) & 1u);
+        }
+      } else if (warp == 9 || warp == 10) {
+        const int t = warp - 9;
         const uint32_t idesc_s = idesc_bf16(kRows, false, p.scale < 0.0f);
         const uint32_t idesc_o = idesc_bf16((p.dim + 15) & ~15, true, false);
-        const bool neighbours = item.other + item.other_len < p.tk;
-        const int ksteps = (p.dim + 15) / 16, len = uniform(item.other_len);
+        const int ksteps = (p.dim + 15) / 16;
         const uint32_t desc_q = uniform(desc_k_major(smem_addr(smem_q + t * TILE)));
         const uint32_t desc_k = uniform(desc_k_major(smem_addr(ring))), desc_v = uniform(desc_mn_major(smem_addr(ring)));
-        const uint32_t ts = uniform(tmem + 128 * t), to = ts + 256;
-        // waits for tile i (K of step 0, V of step 0, K of step 1, ...); both warps zero its foreign rows
-        auto tile = [&](int i) {
-            const int valid = len - (j0 + (i >> 1)) * kRows;
-            if (!wait.all(&full[i % ST], i / ST)) return false;
-            if (valid < kRows && neighbours) zero_tail<HD>(ring + (i % ST) * TILE, valid);
-            return true;
-        };
+        const uint32_t ts = uniform(tmem + 128 * t), to = uniform(tmem + 256 + O_COLS * t);
+        const uint32_t tp = OWN_P ? uniform(tmem + 384 + 64 * t) : ts;
         const Turns turns{turn, wait, t};
-        bool ok = wait.all(&q_full, 0) && tile(0) && turns.take(0);
-        if (ok) {
-            if (nt > 0) {
-                mma_heads<HD>(ts, desc_q, desc_k, ksteps, idesc_s);
-                commit(&s_full[t], elect_one());
+        Ring<ST> rk, rv;                                   // the next K and the next V to arrive
+        rv.next();
+        uint32_t queries = 0, outputs = 0, step = 0;       // done so far: query pairs, outputs, steps of this tile
+        int round = 0;
+        bool ok = true;
+        while (ok && queue.next(items, wait, item)) {
+            const FwdPlan plan(p, item);
+            if (plan.steps == 0) continue;
+            const int len = uniform(item.other_len) - plan.j0 * kRows, nt = t ? plan.n[1] : plan.n[0];
+            const bool neighbours = uniform((int)(item.other + item.other_len < p.tk)) != 0;
+            // waits for a tile of step j; both warps zero its foreign rows
+            auto tile = [&](const Ring<ST>& r, int j) {
+                const int valid = len - j * kRows;
+                if (!wait.all(&full[r.slot], r.phase)) return false;
+                if (valid < kRows && neighbours) zero_tail<HD>(ring + r.slot * TILE, valid);
+                return true;
+            };
+            auto two = [](Ring<ST>& r) {
+                r.next();
+                r.next();
+            };
+            if constexpr (OWN_P) {
+                ok = wait.all(&q_full, queries) && tile(rk, 0) && (step == 0 || nt == 0 || wait.all(&s_read[t], step - 1));
+                if (!ok) break;
+                if (nt > 0) {
+                    fence_after();
+                    mma_heads<HD>(ts, desc_q, desc_k + rk.slot * (TILE >> 4), ksteps, idesc_s);
+                    commit(&s_full[t], elect_one());
+                }
+                commit(&empty[rk.slot], elect_one());
+                if (nt <= 1) commit(&q_empty, elect_one());
+                two(rk);
+                for (int j = 0; j < plan.steps; ++j) {
+                    if (j + 1 < plan.steps) {
+                        ok = tile(rk, j + 1) && (j + 1 >= nt || wait.all(&s_read[t], step));
+                        if (!ok) break;
+                        if (j + 1 < nt) {
+                            fence_after();
+                            mma_heads<HD>(ts, desc_q, desc_k + rk.slot * (TILE >> 4), ksteps, idesc_s);
+                            commit(&s_full[t], elect_one());
+                        }
+                        commit(&empty[rk.slot], elect_one());
+                        if (j + 2 == nt) commit(&q_empty, elect_one());
+                        two(rk);
+                    }
+                    ok = tile(rv, j) && (j > 0 || nt == 0 || wait.all(&o_empty[t], outputs ^ 1u)) &&
+                         (j >= nt || wait.all(&p_ready[t], step));
+                    if (!ok) break;
+                    if (j < nt) {
+                        fence_after();
+                        mma_rows(to, tp, tp + 32, desc_v + rv.slot * (TILE >> 4), idesc_o, j > 0);
+                        commit(&pv_done[t], elect_one());
+                        ++step;
+                    }
+                    commit(&empty[rv.slot], elect_one());
+                    two(rv);
+                }
+            } else {
+                ok = wait.all(&q_full, queries) && tile(rk, 0) && turns.take(round);
+                if (!ok) break;
+                if (nt > 0) {
+                    mma_heads<HD>(ts, desc_q, desc_k + rk.slot * (TILE >> 4), ksteps, idesc_s);
+                    commit(&s_full[t], elect_one());
+                }
+                turns.pass();
+                ++round;
+                commit(&empty[rk.slot], elect_one());
+                if (nt <= 1) commit(&q_empty, elect_one());
+                two(rk);
+                for (int j = 0; j < plan.steps; ++j) {
+                    // what comes last is waited for last: a wait costs time even where it is over
+                    ok = tile(rv, j) && (j + 1 >= plan.steps || tile(rk, j + 1)) &&
+                         (j > 0 || nt == 0 || wait.all(&o_empty[t], outputs ^ 1u)) && turns.take(round) &&
+                         (j >= nt || wait.all(&p_ready[t], step));
+                    if (!ok) break;
+                    if (j < nt) {
+                        fence_after();
+                        mma_rows(to, tp, tp + 32, desc_v + rv.slot * (TILE >> 4), idesc_o, j > 0);
+                        if (j + 1 == nt) commit(&pv_done[t], elect_one());
+                        ++step;
+                    }
+                    if (j + 1 < nt) {
+                        mma_heads<HD>(ts, desc_q, desc_k + rk.slot * (TILE >> 4), ksteps, idesc_s);
+                        commit(&s_full[t], elect_one());
+                    }
+                    turns.pass();
+                    ++round;
+                    commit(&empty[rv.slot], elect_one());
+                    two(rv);
+                    if (j + 1 < plan.steps) {
+                        commit(&empty[rk.slot], elect_one());
+                        if (j + 2 == nt) commit(&q_empty, elect_one());    // the last scores that read the queries
+                        two(rk);
+                    }
+                }
             }
-            turns.pass();
-            commit(&empty[0], elect_one());
-        }
-        for (int j = 0; ok && j < steps; ++j) {
-            const int slot_v = (2 * j + 1) % ST, slot_k = (2 * j + 2) % ST;
-            // what comes last is waited for last: a wait costs time even where it is over
-            ok = tile(2 * j + 1) && (j + 1 >= steps || tile(2 * j + 2)) && turns.take(j + 1) &&
-                 (j >= nt || wait.all(&p_ready[t], j));
             if (!ok) break;
-            if (j < nt) {
-                fence_after();
-                mma_rows(to, ts, ts + 32, desc_v + slot_v * (TILE >> 4), idesc_o, j > 0);
-                if (j + 1 == nt) commit(&o_full[t], elect_one());
-            }
-            if (j + 1 < nt) {
-                mma_heads<HD>(ts, desc_q, desc_k + slot_k * (TILE >> 4), ksteps, idesc_s);
-                commit(&s_full[t], elect_one());
-            }
-            turns.pass();
-            commit(&empty[slot_v], elect_one());
-            if (j + 1 < steps) commit(&empty[slot_k], elect_one());
+            ++queries;
+            outputs += nt > 0;
         }
         commit(&mma_done[t], elect_one());
         wait.drain(&mma_done[t], 0);
@@ -430,103 +569,133 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kFwdRegsSoftmax));
         const int t = warp >> 2, r = (warp & 3) * 32 + lane, row = kRows * t + r;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + 128 * t + lanes, to = tmem + 256 + 128 * t + lanes;
-        // keys this row sees, and those that every row of the tile sees
-        const int limit = p.causal ? min(item.other_len, max(0, row + item.diag + 1)) : item.other_len;
-        const int common = p.causal ? min(item.other_len, kRows * t + item.diag + 1) : item.other_len;
+        const uint32_t ts = tmem + 128 * t + lanes, to = tmem + 256 + O_COLS * t + lanes;
+        const uint32_t tp = OWN_P ? tmem + 384 + 64 * t + lanes : ts;
         const float2 c2 = make_float2(p.c, p.c);
-        float m = -INFINITY, l = 0.0f;
+        uint32_t step = 0, outputs = 0;
         bool ok = true;
-        for (int j = 0; j < n[t]; ++j) {
-            ok = wait(&s_full[t], j);
+        while (ok && queue.next(items, wait, item)) {
+            const FwdPlan plan(p, item);
+            const int nt = t ? plan.n[1] : plan.n[0], rows = t ? plan.rows[1] : plan.rows[0];
+            // keys this row sees, and those that every row of the tile sees, from the first of this CTA's on
+            const int len = item.other_len, first = plan.j0 * kRows;
+            const int limit = (p.causal ? min(len, max(0, row + item.diag + 1)) : len) - first;
+            const int common = (p.causal ? min(len, kRows * t + item.diag + 1) : len) - first;
+            float m = -INFINITY, l = 0.0f;
+            for (int j = 0; j < nt; ++j, ++step) {
+                ok = wait(&s_full[t], step);
+                if (!ok) break;
+                fence_after();
+                uint32_t s[4][32];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) ld32(ts + 32 * i, s[i]);
+                ld_wait();
+#pragma unroll
+                for (int i = 0; i < 4; ++i) fence32(s[i]);
+                if constexpr (OWN_P) {                     // the next scores may come
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&s_read[t]);
+                }
+                if ((j + 1) * kRows > common) {
+                    const int lim = limit - j * kRows;
+#pragma unroll
+                    for (int i = 0; i < 128; ++i)
+                        if (i >= lim) s[i >> 5][i & 31] = 0xFF800000u;
+                }
+                float mx[4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    mx[i] = __uint_as_float(s[i][0]);
+#pragma unroll
+                    for (int e = 1; e < 32; ++e) mx[i] = fmaxf(mx[i], __uint_as_float(s[i][e]));
+                }
+                const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
+                const bool grow = top > m + 8.0f;
+                if (__any_sync(~0u, grow)) {
+                    const float mn = grow ? top : m, f = grow ? ex2(m - mn) : 1.0f;
+                    m = mn;
+                    l *= f;
+                    if (j > 0) {
+                        if constexpr (OWN_P) {
+                            ok = wait(&pv_done[t], step - 1);
+                            if (!ok) break;
+                            fence_after();
+                        }
+                        for (int i = 0; i < p.dim; i += 32) {
+                            uint32_t o[32];
+                            ld32(to + i, o);
+                            ld_wait();
+                            fence32(o);
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            st32(to + i, o);
+                        }
+                    }
+                }
+                const float neg = m == -INFINITY ? 0.0f : -m;
+                const float2 neg2 = make_float2(neg, neg);
+                float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
+                uint32_t w[4][16];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+#pragma unroll
+                    for (int e = 0; e < 16; ++e) {
+                        float2 x = make_float2(__uint_as_float(s[i][2 * e]), __uint_as_float(s[i][2 * e + 1]));
+                        x = __ffma2_rn(x, c2, neg2);
+                        x = make_float2(ex2(x.x), ex2(x.y));
+                        sum[e & 1] = __fadd2_rn(sum[e & 1], x);
+                        w[i][e] = pack_bf16(x.x, x.y);
+                    }
+                    if constexpr (!OWN_P) st16(tp + 16 * i, w[i]);
+                }
+                if constexpr (OWN_P) {                     // the last P has to have been read
+                    if (j > 0) {
+                        ok = wait(&pv_done[t], step - 1);
+                        if (!ok) break;
+                        fence_after();
+                    }
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) st16(tp + 16 * i, w[i]);
+                }
+                l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+                st_wait();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&p_ready[t]);
+            }
+            if (ok && nt > 0) {
+                ok = wait(&pv_done[t], OWN_P ? step - 1 : outputs);
+                fence_after();
+            }
             if (!ok) break;
-            fence_after();
-            uint32_t s[4][32];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) ld32(ts + 32 * i, s[i]);
-            ld_wait();
-#pragma unroll
-            for (int i = 0; i < 4; ++i) fence32(s[i]);
-            if ((j0 + j + 1) * kRows > common) {
-                const int lim = limit - (j0 + j) * kRows;
-#pragma unroll
-                for (int i = 0; i < 128; ++i)
-                    if (i >= lim) s[i >> 5][i & 31] = 0xFF800000u;
-            }
-            float mx[4];
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                mx[i] = __uint_as_float(s[i][0]);
-#pragma unroll
-                for (int e = 1; e < 32; ++e) mx[i] = fmaxf(mx[i], __uint_as_float(s[i][e]));
-            }
-            const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
-            const bool grow = top > m + 8.0f;
-            if (__any_sync(~0u, grow)) {
-                const float mn = grow ? top : m, f = grow ? ex2(m - mn) : 1.0f;
-                m = mn;
-                l *= f;
-                if (j > 0) {
+            if (rows > 0) {                                // whole warps: the TMEM loads are collective
+                const bool store = r < rows;
+                const int64_t tok = item.first + (store ? row : 0), at = (int64_t)item.head * p.tq + tok;
+                bf16* dst = p.out.at(tok, item.head);
+                float* sum = p.part_sums + (((int64_t)item.part * p.tq + tok) * p.heads + item.head) * p.dim;
+                const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+                if (nt == 0) {
+                    if (store && p.parts == 1) store_zeros(dst, p.dim);
+                    if (store && p.parts > 1) store_zeros(sum, p.dim);
+                } else {
                     for (int i = 0; i < p.dim; i += 32) {
                         uint32_t o[32];
                         ld32(to + i, o);
                         ld_wait();
                         fence32(o);
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                        st32(to + i, o);
+                        if (store && p.parts == 1) store32(dst, i, p.dim, o, inv);
+                        if (store && p.parts > 1) store32(sum, i, p.dim, o, inv);
                     }
+                    fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&o_empty[t]);
+                    ++outputs;
                 }
+                if (store)
+                    (p.parts == 1 ? p.lse : p.part_lse + (int64_t)item.part * p.heads * p.tq)[at] =
+                        l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
             }
-            const float neg = m == -INFINITY ? 0.0f : -m;
-            const float2 neg2 = make_float2(neg, neg);
-            float2 sum[2] = {make_float2(0.0f, 0.0f), make_float2(0.0f, 0.0f)};
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t w[16];
-#pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    float2 x = make_float2(__uint_as_float(s[i][2 * e]), __uint_as_float(s[i][2 * e + 1]));
-                    x = __ffma2_rn(x, c2, neg2);
-                    x = make_float2(ex2(x.x), ex2(x.y));
-                    sum[e & 1] = __fadd2_rn(sum[e & 1], x);
-                    w[e] = pack_bf16(x.x, x.y);
-                }
-                st16(ts + 16 * i, w);
-            }
-            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
-            st_wait();
-            fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&p_ready[t]);
-        }
-        if (ok && n[t] > 0) {
-            ok = wait(&o_full[t], 0);
-            fence_after();
-        }
-        if (ok && rows[t] > 0) {                           // whole warps: the TMEM loads are collective
-            const bool store = r < rows[t];
-            const int64_t tok = item.first + (store ? row : 0), at = (int64_t)item.head * p.tq + tok;
-            const int part = blockIdx.x % p.parts;
-            bf16* dst = p.out.at(tok, item.head);
-            float* sum = p.part_sums + (((int64_t)part * p.tq + tok) * p.heads + item.head) * p.dim;
-            const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-            if (n[t] == 0) {
-                if (store && p.parts == 1) store_zeros(dst, p.dim);
-                if (store && p.parts > 1) store_zeros(sum, p.dim);
-            } else {
-                for (int i = 0; i < p.dim; i += 32) {
-                    uint32_t o[32];
-                    ld32(to + i, o);
-                    ld_wait();
-                    fence32(o);
-                    if (store && p.parts == 1) store32(dst, i, p.dim, o, inv);
-                    if (store && p.parts > 1) store32(sum, i, p.dim, o, inv);
-                }
-            }
-            if (store)
-                (p.parts == 1 ? p.lse : p.part_lse + (int64_t)part * p.heads * p.tq)[at] =
-                    l == 0.0f ? -INFINITY : (m + log2f(l)) * kLn2;
         }
     }
     fence_before();
@@ -589,7 +758,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
     }
     if (warp == 9) tmem_alloc_all(&tmem_slot);
     pdl_wait();
-    if (warp == 8) find_item(p, true, kRows, p.heads, &item);
+    if (warp == 8) find_item(p, true, kRows, p.heads, blockIdx.x, &item);
     fence_before();
     __syncthreads();
     fence_after();
@@ -601,7 +770,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         const int keys = p.causal ? min(item.other_len, max(0, item.rows + item.diag)) : item.other_len;
         steps = (keys + kRows - 1) / kRows;
     }
-    const Share mine(p, steps);
+    const Share mine(p, item.part, steps);
     const int j0 = uniform(mine.first);                    // the key tiles j0 .. j0 + steps - 1 are this CTA's
     steps = uniform(mine.count);
 
@@ -756,7 +925,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
             if (lane == 0) mbar_arrive(&ds_ready[j & 1]);
         }
         bf16* dst = p.dq.at(tok, item.head);
-        float* sum = p.part_sums + (((int64_t)(blockIdx.x % p.parts) * p.tq + tok) * p.heads + item.head) * p.dim;
+        float* sum = p.part_sums + (((int64_t)item.part * p.tq + tok) * p.heads + item.head) * p.dim;
         if (steps == 0) {
             if (in && half == 0 && p.parts == 1) store_zeros(dst, p.dim);
             if (in && half == 0 && p.parts > 1) store_zeros(sum, p.dim);
@@ -846,7 +1015,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
     }
     if (warp == 9) tmem_alloc_all(&ctl.tmem_slot);
     pdl_wait();
-    if (warp == 8) find_item(p, false, kRows, p.kv_heads, &ctl.item);
+    if (warp == 8) find_item(p, false, kRows, p.kv_heads, blockIdx.x, &ctl.item);
     fence_before();
     __syncthreads();
     fence_after();
@@ -861,7 +1030,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
         tiles = max(0, (item.other_len + kRows - 1) / kRows - first_tile);
         steps = tiles * share;
     }
-    const Share mine(p, steps);
+    const Share mine(p, item.part, steps);
     steps = uniform(mine.count);
     first_tile = uniform(first_tile);
     // the steps in order: the query tiles of the first head, of the second, ...
@@ -1082,7 +1251,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
         const int64_t tok = item.first + (in ? r : 0);
         bf16* dst = half ? p.dk.at(tok, item.head) : p.dv.at(tok, item.head);
         // parts: [part][dV, dK][tk, kv_heads, dim]
-        float* sum = p.part_sums + (((int64_t)(2 * (blockIdx.x % p.parts) + half) * p.tk + tok) * p.kv_heads + item.head) * p.dim;
+        float* sum = p.part_sums + (((int64_t)(2 * item.part + half) * p.tk + tok) * p.kv_heads + item.head) * p.dim;
         if (steps == 0) {
             if (in && p.parts == 1) store_zeros(dst, p.dim);
             if (in && p.parts > 1) store_zeros(sum, p.dim);
@@ -1327,7 +1496,8 @@ nvfp4_status forward_impl(const nvfp4_attention_shape* shape, const nvfp4_heads*
         !make_map(&mv, v, p.tk, p.kv_heads, p.dim))
         return NVFP4_ERR_CUDA;
     const cudaStream_t s = static_cast<cudaStream_t>(stream);
-    const int64_t grid = tiles_of(p.tq, p.nseq, 2 * kRows) * p.heads * p.parts;
+    p.work = (int)(tiles_of(p.tq, p.nseq, 2 * kRows) * p.heads * p.parts);
+    const int64_t grid = std::min(p.work, sms());
     if (!(p.dim <= 64 ? fwd_registers_fit<64>() : fwd_registers_fit<128>())) return NVFP4_ERR_CUDA;
     cudaError_t e = p.dim <= 64 ? launch(fwd_kernel<64>, Fwd<64>::SMEM, kFwdThreads, grid, s, mq, mk, mv, p)
                                 : launch(fwd_kernel<128>, Fwd<128>::SMEM, kFwdThreads, grid, s, mq, mk, mv, p);
