@@ -606,9 +606,9 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
                 float mx[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    mx[i] = __uint_as_float(s[i][0]);
+                    mx[i] = fmaxf(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]));
 #pragma unroll
-                    for (int e = 1; e < 32; ++e) mx[i] = fmaxf(mx[i], __uint_as_float(s[i][e]));
+                    for (int e = 2; e < 32; e += 2) mx[i] = max3(mx[i], __uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1]));
                 }
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
                 const bool grow = top > m + 8.0f;
@@ -708,231 +708,311 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
 
 // ---------------------------------------------------------------------------- backward, dQ
 // Warps 0-7: a row per thread, warps 0-3 the first 64 keys of a tile, warps 4-7 the last 64; warp 8: TMA; warp 9:
-// the MMAs of S and dQ; warp 10: those of dP.  TMEM: S of even and odd steps at 0 and 128 (dS takes S's place, in the columns its own warps
-// have read), dP at 256, dQ at 384.  The tensor cores do dQ of a step and S of the one after next while
-// the warps work on the step between.  The first kernel of the backward pass: it also leaves delta.
-constexpr int kDqThreads = 352;
+// the MMAs of S and dQ; warp 10: those of dP; warp 11: the next tiles to work on.  TMEM: S of even and odd steps at 0
+// and 128 (dS takes S's place, in the columns its own warps have read), dP at 256, dQ at 384.  The tensor
+// cores do dQ of a step and S of the one after next while the warps work on the step between.  The first
+// kernel of the backward pass: it also leaves delta, computed while the last tile's dQ is still under way.
+constexpr int kDqThreads = 384;
 template <int HD> struct Dq {
     static constexpr int TILE = kRows * HD * 2;
-    static constexpr int SMEM = 7 * TILE + 1024;           // Q, dO, three K, two V
-    static constexpr int PAD = HD == 128 ? SMEM : 120 * 1024;   // one CTA per SM: TMEM is taken whole
+    static constexpr int KS = HD == 128 ? 3 : 5, VS = HD == 128 ? 2 : 3;
+    struct Ctl {
+        uint64_t q_full, q_empty, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], s_full[2], dp_full, ds_ready[2], dq_full,
+            dq_empty, part_ready, turn[2], mma_done[2];
+        Queue queue;
+        uint32_t tmem_slot, abort_flag;
+        float part[2][2][kRows];                           // delta's two halves, of two items in turn
+    };
+    static constexpr int TILES = (2 + KS + VS) * TILE;     // Q, dO, the K's, the V's
+    static constexpr int SMEM = TILES + (int)sizeof(Ctl);
+    static_assert(SMEM <= 232448 && SMEM > 116 * 1024, "one CTA fits an SM (TMEM is taken whole)");
 };
 
 template <int HD>
 __global__ void __launch_bounds__(kDqThreads, 1)
 dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
           const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmdo, const Params p) {
-    constexpr int TILE = Dq<HD>::TILE;
-    extern __shared__ uint8_t raw[];
-    __shared__ uint64_t q_full, k_full[3], k_empty[3], v_full[2], v_empty[2], s_full[2], dp_full, ds_ready[2], turn[2], mma_done[2];
-    __shared__ uint32_t tmem_slot, abort_flag;
-    __shared__ Item item;
-    __shared__ float part[2][kRows];
-    uint8_t* smem_q = align1024(raw);
+    using Cfg = Dq<HD>;
+    constexpr int TILE = Cfg::TILE, KS = Cfg::KS, VS = Cfg::VS;
+    extern __shared__ __align__(1024) uint8_t tiles_smem[];
+    uint8_t* smem_q = tiles_smem;
     uint8_t* smem_do = smem_q + TILE;
     uint8_t* ring_k = smem_do + TILE;
-    uint8_t* ring_v = ring_k + 3 * TILE;
+    uint8_t* ring_v = ring_k + KS * TILE;
+    typename Cfg::Ctl& ctl = *reinterpret_cast<typename Cfg::Ctl*>(tiles_smem + Cfg::TILES);
     const int warp = uniform((int)(threadIdx.x >> 5)), lane = threadIdx.x & 31;
 
     pdl_launch_dependents();
     if (threadIdx.x == 0) {
-        mbar_init(&q_full, 1);
-        for (int i = 0; i < 3; ++i) {
-            mbar_init(&k_full[i], 1);
-            mbar_init(&k_empty[i], 1);
+        mbar_init(&ctl.q_full, 1);
+        mbar_init(&ctl.q_empty, 2);
+        for (int i = 0; i < KS; ++i) {
+            mbar_init(&ctl.k_full[i], 1);
+            mbar_init(&ctl.k_empty[i], 1);
+        }
+        for (int i = 0; i < VS; ++i) {
+            mbar_init(&ctl.v_full[i], 1);
+            mbar_init(&ctl.v_empty[i], 1);
         }
         for (int i = 0; i < 2; ++i) {
-            mbar_init(&v_full[i], 1);
-            mbar_init(&v_empty[i], 1);
-            mbar_init(&s_full[i], 1);
+            mbar_init(&ctl.s_full[i], 1);
+            mbar_init(&ctl.ds_ready[i], 8);
+            mbar_init(&ctl.turn[i], 1);
+            mbar_init(&ctl.mma_done[i], 1);
         }
-        mbar_init(&dp_full, 1);
-        mbar_init(&ds_ready[0], 8);
-        mbar_init(&ds_ready[1], 8);
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&turn[i], 1);
-            mbar_init(&mma_done[i], 1);
-        }
-        abort_flag = 0u;
+        mbar_init(&ctl.dp_full, 1);
+        mbar_init(&ctl.dq_full, 1);
+        mbar_init(&ctl.dq_empty, 8);
+        mbar_init(&ctl.part_ready, 8);
+        ctl.queue.init(11);
+        ctl.abort_flag = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     }
-    if (warp == 9) tmem_alloc_all(&tmem_slot);
+    if (warp == 9) tmem_alloc_all(&ctl.tmem_slot);
     pdl_wait();
-    if (warp == 8) find_item(p, true, kRows, p.heads, blockIdx.x, &item);
     fence_before();
     __syncthreads();
     fence_after();
-    const uint32_t tmem = uniform(tmem_slot);
-    const Wait wait{p.timeout_ns, &abort_flag, p.dev_status};
-    const int hk = item.head / (p.heads / p.kv_heads);
-    int steps = 0;
-    if (item.valid) {
-        const int keys = p.causal ? min(item.other_len, max(0, item.rows + item.diag)) : item.other_len;
-        steps = (keys + kRows - 1) / kRows;
-    }
-    const Share mine(p, item.part, steps);
-    const int j0 = uniform(mine.first);                    // the key tiles j0 .. j0 + steps - 1 are this CTA's
-    steps = uniform(mine.count);
+    const uint32_t tmem = uniform(ctl.tmem_slot);
+    const Wait wait{p.timeout_ns, &ctl.abort_flag, p.dev_status};
+    Ring<2> items;
+    Item item;
+    // an item's key tiles: j0 .. j0 + steps - 1
+    auto share_of = [&](const Item& it) {
+        const int keys = p.causal ? min(it.other_len, max(0, it.rows + it.diag)) : it.other_len;
+        return Share(p, it.part, (keys + kRows - 1) / kRows);
+    };
 
-    if (warp == 8 && steps > 0) {
-        if (lane == 0) {
-            mbar_arrive_expect_tx(&q_full, 2 * TILE);
-            load_tile<HD>(smem_q, &tmq, item.first, item.head, &q_full);
-            load_tile<HD>(smem_do, &tmdo, item.first, item.head, &q_full);
-            int got_k = 0, got_v = 0;
-            for (int j = 0; j < steps; ++j) {
-                if (j >= 3 && !wait(&k_empty[j % 3], j / 3 - 1)) break;
-                mbar_arrive_expect_tx(&k_full[j % 3], TILE);
-                load_tile<HD>(ring_k + (j % 3) * TILE, &tmk, item.other + (int64_t)(j0 + j) * kRows, hk, &k_full[j % 3]);
-                got_k = j + 1;
-                if (j >= 2 && !wait(&v_empty[j & 1], j / 2 - 1)) break;
-                mbar_arrive_expect_tx(&v_full[j & 1], TILE);
-                load_tile<HD>(ring_v + (j & 1) * TILE, &tmv, item.other + (int64_t)(j0 + j) * kRows, hk, &v_full[j & 1]);
-                got_v = j + 1;
+    if (warp == 11) {
+        ctl.queue.feed(p, true, kRows, p.heads, wait);
+    } else if (warp == 8) {
+        Ring<KS> rk;
+        Ring<VS> rv;
+        uint32_t got_k = 0, got_v = 0, queries = 0;
+        bool ok = true;
+        while (ok && ctl.queue.next(items, wait, item)) {
+            const Share mine = share_of(item);
+            if (mine.count == 0) continue;
+            const int hk = item.head / (p.heads / p.kv_heads);
+            if (lane == 0) {
+                ok = wait(&ctl.q_empty, queries ^ 1u);
+                if (ok) {
+                    mbar_arrive_expect_tx(&ctl.q_full, 2 * TILE);
+                    load_tile<HD>(smem_q, &tmq, item.first, item.head, &ctl.q_full);
+                    load_tile<HD>(smem_do, &tmdo, item.first, item.head, &ctl.q_full);
+                    ++queries;
+                }
+                for (int j = 0; ok && j < mine.count; ++j) {
+                    const int64_t tok = item.other + (int64_t)(mine.first + j) * kRows;
+                    ok = wait(&ctl.k_empty[rk.slot], rk.phase ^ 1u);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&ctl.k_full[rk.slot], TILE);
+                    load_tile<HD>(ring_k + rk.slot * TILE, &tmk, tok, hk, &ctl.k_full[rk.slot]);
+                    ++got_k;
+                    rk.next();
+                    ok = wait(&ctl.v_empty[rv.slot], rv.phase ^ 1u);
+                    if (!ok) break;
+                    mbar_arrive_expect_tx(&ctl.v_full[rv.slot], TILE);
+                    load_tile<HD>(ring_v + rv.slot * TILE, &tmv, tok, hk, &ctl.v_full[rv.slot]);
+                    ++got_v;
+                    rv.next();
+                }
             }
-            if (got_v < steps) {                           // aborted: the copies in flight land first
-                wait.drain(&q_full, 0);
-                for (int i = max(0, got_k - 3); i < got_k; ++i) wait.drain(&k_full[i % 3], i / 3);
-                for (int i = max(0, got_v - 2); i < got_v; ++i) wait.drain(&v_full[i & 1], i / 2);
-            }
+            ok = __all_sync(~0u, ok);
         }
-    } else if (warp == 9 && steps > 0) {
+        if (lane == 0 && ctl.abort_flag) {                 // the copies in flight land first
+            if (queries) wait.drain(&ctl.q_full, (queries - 1) & 1u);
+            for (uint32_t i = got_k > KS ? got_k - KS : 0; i < got_k; ++i) wait.drain(&ctl.k_full[i % KS], (i / KS) & 1u);
+            for (uint32_t i = got_v > VS ? got_v - VS : 0; i < got_v; ++i) wait.drain(&ctl.v_full[i % VS], (i / VS) & 1u);
+        }
+    } else if (warp == 9) {
         const uint32_t idesc_s = idesc_bf16(kRows, false, p.scale < 0.0f);
         const uint32_t idesc_dq = idesc_bf16((p.dim + 15) & ~15, true, false);
-        const bool neighbours = item.other + item.other_len < p.tk;
-        const int ksteps = (p.dim + 15) / 16, len = uniform(item.other_len);
+        const int ksteps = (p.dim + 15) / 16;
         const uint32_t desc_q = uniform(desc_k_major(smem_addr(smem_q)));
         const uint32_t desc_k = uniform(desc_k_major(smem_addr(ring_k))), desc_kt = uniform(desc_mn_major(smem_addr(ring_k)));
-        auto issue_s = [&](int j) {
-            const int slot = j % 3, valid = len - (j0 + j) * kRows;
-            if (!wait.all(&k_full[slot], j / 3)) return false;
-            if (valid < kRows && neighbours) zero_tail<HD>(ring_k + slot * TILE, valid);
-            mma_heads<HD>(tmem + 128 * (j & 1), desc_q, desc_k + slot * (TILE >> 4), ksteps, idesc_s);
-            commit(&s_full[j & 1], elect_one());
-            return true;
-        };
-        // rounds: S 0, dP 0; S 1, dP 1; dQ 0 and S 2, dP 2; ...: the warps wait for dP first
-        const Turns turns{turn, wait, 0};
-        bool ok = wait.all(&q_full, 0) && issue_s(0);
-        turns.pass();
-        if (steps > 1) {
-            ok = ok && turns.take(1) && issue_s(1);
+        const Turns turns{ctl.turn, wait, 0};
+        Ring<KS> rs, rq;                                   // the next K for S, and for dQ
+        uint32_t queries = 0, gs = 0, gq = 0;              // items, and steps whose S and dQ have been issued
+        int round = 0;
+        bool ok = true;
+        while (ok && ctl.queue.next(items, wait, item)) {
+            const Share mine = share_of(item);
+            const int steps = uniform(mine.count), len = uniform(item.other_len - mine.first * kRows);
+            if (steps == 0) continue;
+            const bool neighbours = uniform((int)(item.other + item.other_len < p.tk)) != 0;
+            auto issue_s = [&](int j) {
+                const int valid = len - j * kRows;
+                if (!wait.all(&ctl.k_full[rs.slot], rs.phase)) return false;
+                if (valid < kRows && neighbours) zero_tail<HD>(ring_k + rs.slot * TILE, valid);
+                mma_heads<HD>(tmem + 128 * (gs & 1), desc_q, desc_k + rs.slot * (TILE >> 4), ksteps, idesc_s);
+                commit(&ctl.s_full[gs & 1], elect_one());
+                if (j + 1 == steps) commit(&ctl.q_empty, elect_one());
+                rs.next();
+                ++gs;
+                return true;
+            };
+            // rounds: S 0, dP 0; S 1, dP 1; dQ 0 and S 2, dP 2; ...: the warps wait for dP first
+            ok = wait.all(&ctl.q_full, queries) && turns.take(round++) && issue_s(0);
             turns.pass();
-        }
-        for (int j = 0; ok && j < steps; ++j) {
-            ok = (j + 2 > steps || turns.take(j + 2)) && wait.all(&ds_ready[j & 1], j >> 1);
-            if (!ok) break;
-            fence_after();
-            const uint32_t ds = tmem + 128 * (j & 1);
-            mma_rows(tmem + 384, ds, ds + 64, desc_kt + (j % 3) * (TILE >> 4), idesc_dq, j > 0);
-            commit(&k_empty[j % 3], elect_one());
-            if (j + 2 < steps) ok = issue_s(j + 2);
+            ok = ok && turns.take(round++) && (steps < 2 || issue_s(1));
             turns.pass();
+            for (int j = 0; ok && j < steps; ++j) {
+                ok = (j > 0 || wait.all(&ctl.dq_empty, queries ^ 1u)) && turns.take(round++) &&
+                     wait.all(&ctl.ds_ready[gq & 1], gq >> 1);
+                if (!ok) break;
+                fence_after();
+                const uint32_t ds = tmem + 128 * (gq & 1);
+                mma_rows(tmem + 384, ds, ds + 64, desc_kt + rq.slot * (TILE >> 4), idesc_dq, j > 0);
+                commit(&ctl.k_empty[rq.slot], elect_one());
+                if (j + 1 == steps) commit(&ctl.dq_full, elect_one());
+                rq.next();
+                ++gq;
+                if (j + 2 < steps) ok = issue_s(j + 2);
+                turns.pass();
+            }
+            ++queries;
         }
-        commit(&mma_done[0], elect_one());
-        wait.drain(&mma_done[0], 0);
-    } else if (warp == 10 && steps > 0) {
+        commit(&ctl.mma_done[0], elect_one());
+        wait.drain(&ctl.mma_done[0], 0);
+    } else if (warp == 10) {
         // V's rows past the sequence reach only columns of dP that are masked: no need to zero them
         const uint32_t idesc_dp = idesc_bf16(kRows, false, false);
         const int ksteps = (p.dim + 15) / 16;
         const uint32_t desc_do = uniform(desc_k_major(smem_addr(smem_do))), desc_v = uniform(desc_k_major(smem_addr(ring_v)));
-        const Turns turns{turn, wait, 1};
-        bool ok = wait.all(&q_full, 0);
-        for (int j = 0; ok && j < steps; ++j) {
-            ok = wait.all(&v_full[j & 1], j / 2) && turns.take(j) &&
-                 (j == 0 || wait.all(&ds_ready[(j - 1) & 1], (j - 1) >> 1));    // dP of j - 1 has been read
-            if (!ok) break;
-            fence_after();
-            mma_heads<HD>(tmem + 256, desc_do, desc_v + (j & 1) * (TILE >> 4), ksteps, idesc_dp);
-            commit(&dp_full, elect_one());
-            turns.pass();
-            commit(&v_empty[j & 1], elect_one());
+        const Turns turns{ctl.turn, wait, 1};
+        Ring<VS> rv;
+        uint32_t queries = 0, g = 0;
+        int round = 0;
+        bool ok = true;
+        while (ok && ctl.queue.next(items, wait, item)) {
+            const int steps = uniform(share_of(item).count);
+            if (steps == 0) continue;
+            ok = wait.all(&ctl.q_full, queries);
+            for (int j = 0; ok && j < steps + 2; ++j) {
+                if (j >= steps) {                          // the first warp's last two rounds
+                    ok = turns.take(round++);
+                    turns.pass();
+                    continue;
+                }
+                ok = wait.all(&ctl.v_full[rv.slot], rv.phase) && turns.take(round++) &&
+                     (g == 0 || wait.all(&ctl.ds_ready[(g - 1) & 1], (g - 1) >> 1));    // the last dP has been read
+                if (!ok) break;
+                fence_after();
+                mma_heads<HD>(tmem + 256, desc_do, desc_v + rv.slot * (TILE >> 4), ksteps, idesc_dp);
+                commit(&ctl.dp_full, elect_one());
+                turns.pass();
+                commit(&ctl.v_empty[rv.slot], elect_one());
+                if (j + 1 == steps) commit(&ctl.q_empty, elect_one());
+                rv.next();
+                ++g;
+            }
+            ++queries;
         }
-        commit(&mma_done[1], elect_one());
-        wait.drain(&mma_done[1], 0);
-    } else if (warp < 8 && item.valid) {
+        commit(&ctl.mma_done[1], elect_one());
+        wait.drain(&ctl.mma_done[1], 0);
+    } else {
         const int half = warp >> 2, r = (warp & 3) * 32 + lane;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const bool in = r < item.rows;
-        const int64_t tok = item.first + (in ? r : 0), at = (int64_t)item.head * p.tq + tok;
-        // delta = dout . out, half a row each
-        float d = 0.0f;
-        {
-            const bf16 *o = p.out.at(tok, item.head), *g = p.dout.at(tok, item.head);
+        const uint32_t tdp = tmem + 256 + 64 * half + lanes;
+        const float2 c2 = make_float2(p.c, p.c);
+        // delta = dout . out of row r, half a row each; -lse log2(e)
+        float d = 0.0f, neg = 0.0f;
+        uint32_t buf = 0;
+        auto row_stats = [&](const Item& it) {
+            const bool in = r < it.rows;
+            const int64_t tok = it.first + (in ? r : 0), at = (int64_t)it.head * p.tq + tok;
+            const bf16 *o = p.out.at(tok, it.head), *g = p.dout.at(tok, it.head);
             const int mid = min(p.dim, 64);
+            const float lse = in ? p.lse[at] : 0.0f;
+            float sum = 0.0f;
             for (int i = half ? mid : 0; i < (half ? p.dim : mid); i += 8) {
                 const uint4 a = *reinterpret_cast<const uint4*>(o + i), b = *reinterpret_cast<const uint4*>(g + i);
                 const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
 #pragma unroll
-                for (int e = 0; e < 4; ++e) d += bf16_lo(x[e]) * bf16_lo(y[e]) + bf16_hi(x[e]) * bf16_hi(y[e]);
+                for (int e = 0; e < 4; ++e) sum += bf16_lo(x[e]) * bf16_lo(y[e]) + bf16_hi(x[e]) * bf16_hi(y[e]);
             }
-            part[half][r] = d;
-            asm volatile("bar.sync 1, 256;" ::: "memory");
-            d = part[0][r] + part[1][r];
-            if (in && half == 0) p.delta[at] = d;
-        }
-        const float lse = in ? p.lse[at] : 0.0f;
-        const float neg = lse == -INFINITY ? -INFINITY : -lse * kLog2e;      // a row that sees no key: P = 0
-        const int limit = p.causal ? min(item.other_len, max(0, r + item.diag + 1)) : item.other_len;
-        const int common = p.causal ? min(item.other_len, item.diag + 1) : item.other_len;
-        const float2 c2 = make_float2(p.c, p.c), neg2 = make_float2(neg, neg), delta2 = make_float2(-d, -d);
-        bool ok = true;
-        for (int j = 0; j < steps; ++j) {
-            const uint32_t ts = tmem + 128 * (j & 1) + 64 * half + lanes, tdp = tmem + 256 + 64 * half + lanes;
-            ok = wait(&s_full[j & 1], j >> 1);
-            if (!ok) break;
-            fence_after();
-            uint32_t s[2][32], g[2][32], w[32];
-            ld32(ts, s[0]);
-            ld32(ts + 32, s[1]);
-            ld_wait();
-            fence32(s[0]);
-            fence32(s[1]);
-#pragma unroll
-            for (int i = 0; i < 64; i += 2) {
-                float2 x = make_float2(__uint_as_float(s[i >> 5][i & 31]), __uint_as_float(s[i >> 5][(i & 31) + 1]));
-                x = __ffma2_rn(x, c2, neg2);
-                s[i >> 5][i & 31] = __float_as_uint(ex2(x.x));
-                s[i >> 5][(i & 31) + 1] = __float_as_uint(ex2(x.y));
-            }
-            ok = wait(&dp_full, j);
-            if (!ok) break;
-            fence_after();
-            ld32(tdp, g[0]);
-            ld32(tdp + 32, g[1]);
-            ld_wait();
-            fence32(g[0]);
-            fence32(g[1]);
-#pragma unroll
-            for (int i = 0; i < 64; i += 2) {
-                const float2 pr = make_float2(__uint_as_float(s[i >> 5][i & 31]), __uint_as_float(s[i >> 5][(i & 31) + 1]));
-                float2 x = make_float2(__uint_as_float(g[i >> 5][i & 31]), __uint_as_float(g[i >> 5][(i & 31) + 1]));
-                x = __fmul2_rn(pr, __fadd2_rn(x, delta2));
-                w[i >> 1] = pack_bf16(x.x, x.y);
-            }
-            if ((j0 + j + 1) * kRows > common) {                // masked pairs count for nothing, whatever they hold
-                const int lim = limit - (j0 + j) * kRows - 64 * half;
-#pragma unroll
-                for (int i = 0; i < 32; ++i) {
-                    if (2 * i >= lim) w[i] = 0u;
-                    else if (2 * i + 1 >= lim) w[i] &= 0xFFFFu;
-                }
-            }
-            st32(ts, w);
-            st_wait();
-            fence_before();
+            // the other half's warps meet at a barrier with a bounded wait; two buffers take turns
+            ctl.part[buf & 1][half][r] = sum;
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ds_ready[j & 1]);
-        }
-        bf16* dst = p.dq.at(tok, item.head);
-        float* sum = p.part_sums + (((int64_t)item.part * p.tq + tok) * p.heads + item.head) * p.dim;
-        if (steps == 0) {
-            if (in && half == 0 && p.parts == 1) store_zeros(dst, p.dim);
-            if (in && half == 0 && p.parts > 1) store_zeros(sum, p.dim);
-        } else if (ok) {
-            ok = wait(&mma_done[0], 0);
-            fence_after();
-            if (ok)
+            if (lane == 0) mbar_arrive(&ctl.part_ready);
+            if (!wait(&ctl.part_ready, buf)) return false;
+            d = ctl.part[buf & 1][0][r] + ctl.part[buf & 1][1][r];
+            ++buf;
+            if (in && half == 0 && it.part == 0) p.delta[at] = d;
+            neg = lse == -INFINITY ? -INFINITY : -lse * kLog2e;            // a row that sees no key: P = 0
+            return true;
+        };
+        uint32_t queries = 0, g = 0;
+        bool ok = ctl.queue.next(items, wait, item) && row_stats(item);
+        while (ok) {
+            const Share mine = share_of(item);
+            const int steps = mine.count, first = mine.first * kRows;
+            const bool in = r < item.rows;
+            const int64_t tok = item.first + (in ? r : 0);
+            const int limit = (p.causal ? min(item.other_len, max(0, r + item.diag + 1)) : item.other_len) - first;
+            const int common = (p.causal ? min(item.other_len, item.diag + 1) : item.other_len) - first;
+            const float2 neg2 = make_float2(neg, neg), delta2 = make_float2(-d, -d);
+            for (int j = 0; j < steps; ++j, ++g) {
+                const uint32_t ts = tmem + 128 * (g & 1) + 64 * half + lanes;
+                ok = wait(&ctl.s_full[g & 1], g >> 1);
+                if (!ok) break;
+                fence_after();
+                uint32_t s[2][32], u[2][32], w[32];
+                ld32(ts, s[0]);
+                ld32(ts + 32, s[1]);
+                ld_wait();
+                fence32(s[0]);
+                fence32(s[1]);
+#pragma unroll
+                for (int i = 0; i < 64; i += 2) {
+                    float2 x = make_float2(__uint_as_float(s[i >> 5][i & 31]), __uint_as_float(s[i >> 5][(i & 31) + 1]));
+                    x = __ffma2_rn(x, c2, neg2);
+                    s[i >> 5][i & 31] = __float_as_uint(ex2(x.x));
+                    s[i >> 5][(i & 31) + 1] = __float_as_uint(ex2(x.y));
+                }
+                ok = wait(&ctl.dp_full, g);
+                if (!ok) break;
+                fence_after();
+                ld32(tdp, u[0]);
+                ld32(tdp + 32, u[1]);
+                ld_wait();
+                fence32(u[0]);
+                fence32(u[1]);
+#pragma unroll
+                for (int i = 0; i < 64; i += 2) {
+                    const float2 pr = make_float2(__uint_as_float(s[i >> 5][i & 31]), __uint_as_float(s[i >> 5][(i & 31) + 1]));
+                    float2 x = make_float2(__uint_as_float(u[i >> 5][i & 31]), __uint_as_float(u[i >> 5][(i & 31) + 1]));
+                    x = __fmul2_rn(pr, __fadd2_rn(x, delta2));
+                    w[i >> 1] = pack_bf16(x.x, x.y);
+                }
+                if ((j + 1) * kRows > common) {            // masked pairs count for nothing, whatever they hold
+                    const int lim = limit - j * kRows - 64 * half;
+#pragma unroll
+                    for (int i = 0; i < 32; ++i) {
+                        if (2 * i >= lim) w[i] = 0u;
+                        else if (2 * i + 1 >= lim) w[i] &= 0xFFFFu;
+                    }
+                }
+                st32(ts, w);
+                st_wait();
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.ds_ready[g & 1]);
+            }
+            if (!ok) break;
+            // the next item's delta while this one's dQ is finished
+            Item next;
+            const bool more = ctl.queue.next(items, wait, next) && row_stats(next);
+            bf16* dst = p.dq.at(tok, item.head);
+            float* sum = p.part_sums + (((int64_t)item.part * p.tq + tok) * p.heads + item.head) * p.dim;
+            if (steps == 0) {
+                if (in && half == 0 && p.parts == 1) store_zeros(dst, p.dim);
+                if (in && half == 0 && p.parts > 1) store_zeros(sum, p.dim);
+            } else {
+                ok = wait(&ctl.dq_full, queries);
+                if (!ok) break;
+                fence_after();
                 for (int i = 64 * half; i < min(p.dim, 64 * half + 64); i += 32) {
                     uint32_t v[32];
                     ld32(tmem + 384 + i + lanes, v);
@@ -941,6 +1021,13 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                     if (in && p.parts == 1) store32(dst, i, p.dim, v, p.scale);
                     if (in && p.parts > 1) store32(sum, i, p.dim, v, p.scale);
                 }
+                fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&ctl.dq_empty);
+                ++queries;
+            }
+            item = next;
+            ok = more;
         }
     }
     fence_before();
@@ -1570,9 +1657,10 @@ extern "C" nvfp4_status nvfp4_attention_backward(const nvfp4_attention_shape* sh
     cudaError_t e = cudaSuccess;
     if (p.tq > 0) {
         p.parts = parts_of_dq(shape);
-        const int64_t grid = tiles_of(p.tq, p.nseq, kRows) * p.heads * p.parts;
-        e = p.dim <= 64 ? launch(dq_kernel<64>, Dq<64>::PAD, kDqThreads, grid, s, mq, mk, mv, mdo, p)
-                        : launch(dq_kernel<128>, Dq<128>::PAD, kDqThreads, grid, s, mq, mk, mv, mdo, p);
+        p.work = (int)(tiles_of(p.tq, p.nseq, kRows) * p.heads * p.parts);
+        const int64_t grid = std::min(p.work, sms());
+        e = p.dim <= 64 ? launch(dq_kernel<64>, Dq<64>::SMEM, kDqThreads, grid, s, mq, mk, mv, mdo, p)
+                        : launch(dq_kernel<128>, Dq<128>::SMEM, kDqThreads, grid, s, mq, mk, mv, mdo, p);
         if (e == cudaSuccess && p.parts > 1)
             e = launch_pdl(join_sums_kernel, dim3(join_blocks(p.tq, p.heads, p.dim)), dim3(kJoinThreads), 0, s, p.part_sums,
                            p.parts, p.tq * p.heads * p.dim, 0, p.tq, p.heads, p.dim, p.dq, p.dq);
