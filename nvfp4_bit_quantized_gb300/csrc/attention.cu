@@ -76,9 +76,10 @@ struct Item {
     int rows, other_len, diag;
 };
 
-// Whole warp: the tile and head of this CTA.  Tiles are numbered through the sequences; CTAs take
-// the last first (with a causal mask the longest of a sequence, of queries; of keys the other way
-// round), heads fastest, so that CTAs that run together read the same K and V.
+// Whole warp: the tile and head that `work` stands for.  The longest tiles come first, as they are under a causal mask:
+// a sequence's tiles are as long as the number of them up to them (of queries) or from them on (of keys).  That order runs
+// through all sequences where there are at most 32, whose offsets a warp holds at once; more are taken one after another.
+// Heads are fastest, so that CTAs that run together read the same K and V.
 __device__ __forceinline__ void find_item(const Params& p, bool rows_are_q, int tile, int heads, int work, Item* out) {
     const int lane = threadIdx.x & 31, block = p.parts > 1 ? work / p.parts : work;
     const int32_t *cu = rows_are_q ? p.cu_q : p.cu_k, *cu_other = rows_are_q ? p.cu_k : p.cu_q;
@@ -112,30 +113,48 @@ __device__ __forceinline__ void find_item(const Params& p, bool rows_are_q, int 
     }
     if (bad && work == 0) set_status(p.dev_status, NVFP4_ERR_INVALID_ARG);
     int64_t want = block / heads;
-    if (rows_are_q) want = n - 1 - want;
-    if (want < 0 || want >= n) {
+    if (want >= n) {
         if (lane == 0) out->valid = 0;
         return;
     }
+    auto found = [&](int64_t index) {                      // one lane: tile `index` of its sequence
+        const int64_t t0 = index * tile;
+        out->valid = 1;
+        out->part = p.parts > 1 ? work - block * p.parts : 0;
+        out->head = block % heads;
+        out->first = a + t0;
+        out->rows = (int)min((int64_t)tile, b - a - t0);
+        out->other = oa;
+        out->other_len = (int)(ob - oa);
+        out->diag = (int)(t0 + (ob - oa) - (b - a));
+    };
+    if (p.nseq <= 32) {
+        // each sequence of at least c tiles has one of length c: bands of c with the same sequences, from the longest on
+        const int mine = (int)tiles;
+        int cur = __reduce_max_sync(~0u, mine), left = (int)want;
+        while (cur > 0) {
+            const uint32_t mask = __ballot_sync(~0u, mine >= cur);
+            const int count = __popc(mask), next = __reduce_max_sync(~0u, mine < cur ? mine : 0);
+            if (left < (cur - next) * count) {
+                const int c = cur - left / count, rank = left % count;
+                if (mine >= cur && __popc(mask & ((1u << lane) - 1u)) == rank) found(rows_are_q ? c - 1 : mine - c);
+                break;
+            }
+            left -= (cur - next) * count;
+            cur = next;
+        }
+        return;
+    }
+    if (rows_are_q) want = n - 1 - want;
     for (int s0 = 0; s0 < p.nseq; s0 += 32) {
-        if (p.nseq > 32) load(s0);                         // up to 32 sequences are still at hand
+        load(s0);
         int64_t upto = tiles;                              // inclusive prefix
 #pragma unroll
         for (int d = 1; d < 32; d <<= 1) {
             const int64_t v = __shfl_up_sync(~0u, upto, d);
             if (lane >= d) upto += v;
         }
-        if (want >= upto - tiles && want < upto) {
-            const int64_t t0 = (want - (upto - tiles)) * tile;
-            out->valid = 1;
-            out->part = p.parts > 1 ? work - block * p.parts : 0;
-            out->head = block % heads;
-            out->first = a + t0;
-            out->rows = (int)min((int64_t)tile, b - a - t0);
-            out->other = oa;
-            out->other_len = (int)(ob - oa);
-            out->diag = (int)(t0 + (ob - oa) - (b - a));
-        }
+        if (want >= upto - tiles && want < upto) found(want - (upto - tiles));
         const int64_t all = __shfl_sync(~0u, upto, 31);
         if (want < all) break;
         want -= all;
@@ -606,9 +625,9 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
                 float mx[4];
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    mx[i] = fmaxf(__uint_as_float(s[i][0]), __uint_as_float(s[i][1]));
+                    mx[i] = __uint_as_float(s[i][0]);
 #pragma unroll
-                    for (int e = 2; e < 32; e += 2) mx[i] = max3(mx[i], __uint_as_float(s[i][e]), __uint_as_float(s[i][e + 1]));
+                    for (int e = 1; e < 32; ++e) mx[i] = fmaxf(mx[i], __uint_as_float(s[i][e]));
                 }
                 const float top = fmaxf(fmaxf(mx[0], mx[1]), fmaxf(mx[2], mx[3])) * p.c;
                 const bool grow = top > m + 8.0f;
