@@ -303,19 +303,34 @@ __device__ __forceinline__ void mma_rows(uint32_t d, uint32_t a0, uint32_t a1, u
         mma_ts(d, k < 4 ? a0 + k * 8 : a1 + (k - 4) * 8, b + k * (2048 >> 4), idesc, k ? 1u : accumulate, lead);
 }
 
-// A row of `dim` bf16 values (a multiple of 8), 32 columns at a time: v * f, or zeros.
-__device__ __forceinline__ void store32(bf16* row, int col, int dim, const uint32_t (&v)[32], float f) {
+// Whole warp: 32 columns from `col` of 32 rows of `dim` bf16 values (a multiple of 8), a lane's row v * f; the first row is
+// token t's, `rows` of them are stored.  Four lanes first exchange 16-byte pieces, so that they write 64 bytes of one
+// row after the other: a row per lane, a store touches 32 lines.
+__device__ __forceinline__ void store32(const Heads& to, int64_t t, int head, int rows, int col, int dim,
+                                        const uint32_t (&v)[32], float f) {
+    const int lane = threadIdx.x & 31, q = lane & 3;
+    uint32_t w[4][4];
 #pragma unroll
-    for (int i = 0; i < 32; i += 8)
-        if (col + i < dim) {
-            uint32_t w[4];
+    for (int i = 0; i < 16; ++i) w[i >> 2][i & 3] = pack_bf16(__uint_as_float(v[2 * i]) * f, __uint_as_float(v[2 * i + 1]) * f);
 #pragma unroll
-            for (int j = 0; j < 4; ++j)
-                w[j] = pack_bf16(__uint_as_float(v[i + 2 * j]) * f, __uint_as_float(v[i + 2 * j + 1]) * f);
-            *reinterpret_cast<uint4*>(row + col + i) = make_uint4(w[0], w[1], w[2], w[3]);
-        }
+    for (int n = 1; n <= 2; n *= 2)
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+            if (!(k & n))
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t got = __shfl_xor_sync(~0u, q & n ? w[k][e] : w[k | n][e], n);
+                    if (q & n) w[k][e] = got;
+                    else w[k | n][e] = got;
+                }
+    if (col + 8 * q < dim) {
+        bf16* at = to.at(t + (lane & ~3), head) + col + 8 * q;
+#pragma unroll
+        for (int k = 0; k < 4; ++k, at += to.ts)
+            if ((lane & ~3) + k < rows) *reinterpret_cast<uint4*>(at) = make_uint4(w[k][0], w[k][1], w[k][2], w[k][3]);
+    }
 }
-// The same in fp32: a part's row.
+// The same in fp32, a row per lane: a part's.
 __device__ __forceinline__ void store32(float* row, int col, int dim, const uint32_t (&v)[32], float f) {
 #pragma unroll
     for (int i = 0; i < 32; i += 4)
@@ -703,7 +718,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
                         ld32(to + i, o);
                         ld_wait();
                         fence32(o);
-                        if (store && p.parts == 1) store32(dst, i, p.dim, o, inv);
+                        if (p.parts == 1) store32(p.out, item.first + row - lane, item.head, rows - (r - lane), i, p.dim, o, inv);
                         if (store && p.parts > 1) store32(sum, i, p.dim, o, inv);
                     }
                     fence_before();
@@ -737,10 +752,10 @@ template <int HD> struct Dq {
     static constexpr int KS = HD == 128 ? 3 : 5, VS = HD == 128 ? 2 : 3;
     struct Ctl {
         uint64_t q_full, q_empty, k_full[KS], k_empty[KS], v_full[VS], v_empty[VS], s_full[2], dp_full, ds_ready[2], dq_full,
-            dq_empty, part_ready, turn[2], mma_done[2];
+            dq_empty, delta_ready, turn[2], mma_done[2];
         Queue queue;
         uint32_t tmem_slot, abort_flag;
-        float part[2][2][kRows];                           // delta's two halves, of two items in turn
+        float delta[2][kRows];                             // of two items in turn
     };
     static constexpr int TILES = (2 + KS + VS) * TILE;     // Q, dO, the K's, the V's
     static constexpr int SMEM = TILES + (int)sizeof(Ctl);
@@ -782,7 +797,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         mbar_init(&ctl.dp_full, 1);
         mbar_init(&ctl.dq_full, 1);
         mbar_init(&ctl.dq_empty, 8);
-        mbar_init(&ctl.part_ready, 8);
+        mbar_init(&ctl.delta_ready, 8);
         ctl.queue.init(11);
         ctl.abort_flag = 0u;
         asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
@@ -931,32 +946,55 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         commit(&ctl.mma_done[1], elect_one());
         wait.drain(&ctl.mma_done[1], 0);
     } else {
-        const int half = warp >> 2, r = (warp & 3) * 32 + lane;
-        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const int half = warp >> 2, row0 = (warp & 3) * 32, r = row0 + lane;
+        const uint32_t lanes = (uint32_t)row0 << 16;
         const uint32_t tdp = tmem + 256 + 64 * half + lanes;
         const float2 c2 = make_float2(p.c, p.c);
-        // delta = dout . out of row r, half a row each; -lse log2(e)
+        // delta = dout . out of row r; -lse log2(e).  A warp takes 16 rows, HD / 8 lanes each: read a row per lane, a load
+        // touches 32 lines.
         float d = 0.0f, neg = 0.0f;
         uint32_t buf = 0;
         auto row_stats = [&](const Item& it) {
-            const bool in = r < it.rows;
-            const int64_t tok = it.first + (in ? r : 0), at = (int64_t)it.head * p.tq + tok;
-            const bf16 *o = p.out.at(tok, it.head), *g = p.dout.at(tok, it.head);
-            const int mid = min(p.dim, 64);
-            const float lse = in ? p.lse[at] : 0.0f;
-            float sum = 0.0f;
-            for (int i = half ? mid : 0; i < (half ? p.dim : mid); i += 8) {
-                const uint4 a = *reinterpret_cast<const uint4*>(o + i), b = *reinterpret_cast<const uint4*>(g + i);
-                const uint32_t x[4] = {a.x, a.y, a.z, a.w}, y[4] = {b.x, b.y, b.z, b.w};
+            constexpr int LANES = HD / 8, N = HD / 16;     // of a row; rows of a lane
+            const int sub = lane / LANES, c = lane % LANES;
+            uint4 o[N], g[N];
 #pragma unroll
-                for (int e = 0; e < 4; ++e) sum += bf16_lo(x[e]) * bf16_lo(y[e]) + bf16_hi(x[e]) * bf16_hi(y[e]);
+            for (int i = 0; i < N; ++i) {
+                const int row = 16 * warp + 16 / N * i + sub;
+                o[i] = g[i] = make_uint4(0, 0, 0, 0);
+                if (row < it.rows && 8 * c < p.dim) {
+                    o[i] = *reinterpret_cast<const uint4*>(p.out.at(it.first + row, it.head) + 8 * c);
+                    g[i] = *reinterpret_cast<const uint4*>(p.dout.at(it.first + row, it.head) + 8 * c);
+                }
             }
-            // the other half's warps meet at a barrier with a bounded wait; two buffers take turns
-            ctl.part[buf & 1][half][r] = sum;
+            const bool in = r < it.rows;
+            const int64_t at = (int64_t)it.head * p.tq + it.first + (in ? r : 0);
+            const float lse = in ? p.lse[at] : 0.0f;
+            float sum[N];
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                const uint32_t x[4] = {o[i].x, o[i].y, o[i].z, o[i].w}, y[4] = {g[i].x, g[i].y, g[i].z, g[i].w};
+                sum[i] = 0.0f;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) sum[i] += bf16_lo(x[e]) * bf16_lo(y[e]) + bf16_hi(x[e]) * bf16_hi(y[e]);
+            }
+            // N rows' sums over 2 N lanes: a lane keeps half of its rows in each round, row c / 2 at last
+#pragma unroll
+            for (int n = N / 2; n; n >>= 1) {
+                const bool upper = c & (2 * n);
+#pragma unroll
+                for (int i = 0; i < n; ++i) {
+                    const float keep = upper ? sum[i + n] : sum[i], give = upper ? sum[i] : sum[i + n];
+                    sum[i] = keep + __shfl_xor_sync(~0u, give, 2 * n);
+                }
+            }
+            sum[0] += __shfl_xor_sync(~0u, sum[0], 1);
+            if (!(c & 1)) ctl.delta[buf & 1][16 * warp + 16 / N * (c / 2) + sub] = sum[0];
+            // all warps' rows: a barrier with a bounded wait; two buffers take turns
             __syncwarp();
-            if (lane == 0) mbar_arrive(&ctl.part_ready);
-            if (!wait(&ctl.part_ready, buf)) return false;
-            d = ctl.part[buf & 1][0][r] + ctl.part[buf & 1][1][r];
+            if (lane == 0) mbar_arrive(&ctl.delta_ready);
+            if (!wait.all(&ctl.delta_ready, buf)) return false;
+            d = ctl.delta[buf & 1][r];
             ++buf;
             if (in && half == 0 && it.part == 0) p.delta[at] = d;
             neg = lse == -INFINITY ? -INFINITY : -lse * kLog2e;            // a row that sees no key: P = 0
@@ -1037,7 +1075,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                     ld32(tmem + 384 + i + lanes, v);
                     ld_wait();
                     fence32(v);
-                    if (in && p.parts == 1) store32(dst, i, p.dim, v, p.scale);
+                    if (p.parts == 1) store32(p.dq, item.first + row0, item.head, item.rows - row0, i, p.dim, v, p.scale);
                     if (in && p.parts > 1) store32(sum, i, p.dim, v, p.scale);
                 }
                 fence_before();
@@ -1370,7 +1408,9 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
                     ld32(tmem + 256 + 128 * half + i + lanes, v);
                     ld_wait();
                     fence32(v);
-                    if (in && p.parts == 1) store32(dst, i, p.dim, v, half ? p.scale : 1.0f);
+                    if (p.parts == 1)
+                        store32(half ? p.dk : p.dv, item.first + r - lane, item.head, item.rows - (r - lane), i, p.dim, v,
+                                half ? p.scale : 1.0f);
                     if (in && p.parts > 1) store32(sum, i, p.dim, v, half ? p.scale : 1.0f);
                 }
         }
