@@ -80,7 +80,8 @@ struct Item {
 // a sequence's tiles are as long as the number of them up to them (of queries) or from them on (of keys).  That order runs
 // through all sequences where there are at most 32, whose offsets a warp holds at once; more are taken one after another.
 // Heads are fastest, so that CTAs that run together read the same K and V.
-__device__ __forceinline__ void find_item(const Params& p, bool rows_are_q, int tile, int heads, int work, Item* out) {
+template <int tile>
+__device__ __forceinline__ void find_item(const Params& p, bool rows_are_q, int heads, int work, Item* out) {
     const int lane = threadIdx.x & 31, block = p.parts > 1 ? work / p.parts : work;
     const int32_t *cu = rows_are_q ? p.cu_q : p.cu_k, *cu_other = rows_are_q ? p.cu_k : p.cu_q;
     const int64_t total = rows_are_q ? p.tq : p.tk, total_other = rows_are_q ? p.tk : p.tq;
@@ -100,7 +101,7 @@ __device__ __forceinline__ void find_item(const Params& p, bool rows_are_q, int 
         if (s < p.nseq) {
             bounds(cu, s, total, a, b);
             bounds(cu_other, s, total_other, oa, ob);
-            tiles = (b - a + tile - 1) / tile;
+            tiles = (int64_t)((uint64_t)(b - a + tile - 1) / tile);
         }
     };
     int64_t n = 0;                                         // tiles in all
@@ -217,7 +218,7 @@ struct Queue {
         }
     }
     // whole warp
-    __device__ __forceinline__ void feed(const Params& p, bool rows_are_q, int tile, int heads, const Wait& wait) {
+    template <int tile> __device__ __forceinline__ void feed(const Params& p, bool rows_are_q, int heads, const Wait& wait) {
         Ring<2> r;
         const int grid = gridDim.x;
         for (int k = 0;; ++k) {
@@ -225,7 +226,7 @@ struct Queue {
             const int at = (k & 1) ? grid - 1 - (int)blockIdx.x : (int)blockIdx.x, work = k * grid + at;
             const bool more = work < p.work, last = (k + 1) * grid >= p.work;
             if (!wait.all(&empty[r.slot], r.phase ^ 1u)) break;
-            if (more) find_item(p, rows_are_q, tile, heads, work, &item[r.slot]);
+            if (more) find_item<tile>(p, rows_are_q, heads, work, &item[r.slot]);
             else if ((threadIdx.x & 31) == 0) item[r.slot].valid = -1;
             __syncwarp();
             if (!more && !last) continue;
@@ -349,8 +350,8 @@ struct Share {
         first = 0;
         count = steps;
         if (p.parts > 1) {                                 // the divisions take longer than some tiles' steps
-            first = (int)((int64_t)steps * part / p.parts);
-            count = (int)((int64_t)steps * (part + 1) / p.parts) - first;
+            first = steps * part / p.parts;                // at most 2^23 steps and 64 parts
+            count = steps * (part + 1) / p.parts - first;
         }
     }
 };
@@ -453,7 +454,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
     if (warp >= 8) {
       asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kFwdRegsOther));
       if (warp == 11) {
-        queue.feed(p, true, 2 * kRows, p.heads, wait);
+        queue.feed<2 * kRows>(p, true, p.heads, wait);
       } else if (warp == 8) {
         Ring<ST> r;
         uint32_t loads = 0, queries = 0;                   // tiles and query pairs loaded
@@ -632,10 +633,14 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
                     if (lane == 0) mbar_arrive(&s_read[t]);
                 }
                 if ((j + 1) * kRows > common) {
-                    const int lim = limit - j * kRows;
+                    // most blocks of 32 columns are on one side of the mask for the whole warp
+                    const int lim = limit - j * kRows, least = __reduce_min_sync(~0u, lim);
 #pragma unroll
-                    for (int i = 0; i < 128; ++i)
-                        if (i >= lim) s[i >> 5][i & 31] = 0xFF800000u;
+                    for (int i = 0; i < 4; ++i)
+                        if (least < 32 * i + 32)
+#pragma unroll
+                            for (int e = 0; e < 32; ++e)
+                                if (32 * i + e >= lim) s[i][e] = 0xFF800000u;
                 }
                 float mx[4];
 #pragma unroll
@@ -820,7 +825,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
     };
 
     if (warp == 11) {
-        ctl.queue.feed(p, true, kRows, p.heads, wait);
+        ctl.queue.template feed<kRows>(p, true, p.heads, wait);
     } else if (warp == 8) {
         Ring<KS> rk;
         Ring<VS> rv;
@@ -1147,7 +1152,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
     }
     if (warp == 9) tmem_alloc_all(&ctl.tmem_slot);
     pdl_wait();
-    if (warp == 8) find_item(p, false, kRows, p.kv_heads, blockIdx.x, &ctl.item);
+    if (warp == 8) find_item<kRows>(p, false, p.kv_heads, blockIdx.x, &ctl.item);
     fence_before();
     __syncthreads();
     fence_after();
