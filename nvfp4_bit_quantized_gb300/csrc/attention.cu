@@ -2,18 +2,27 @@
 // formulas), on the tcgen05 tensor cores: bf16 heads of at most 128 elements, fp32 accumulators in
 // TMEM, fp32 softmax statistics and sums.
 //
-// Three kernels, each one CTA per SM on one tile of rows that stays in shared memory while tiles of
+// Three kernels, one CTA per SM, each on a tile of rows that stays in shared memory while tiles of
 // 128 rows of the other side stream past by TMA (HD = 64 or 128: the head size rounded up; the MMAs
 // themselves run over the head size rounded up to 16):
 //   fwd   256 queries of a head as two tiles; S = Q K^T, P = exp2(c S - m), O += P V;
 //   dq    128 queries of a head;   S = Q K^T, dP = dO V^T, dS = P (dP - delta), dQ += dS K;
 //   dkv   128 keys of a key head, over all query heads that read it;
 //         S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q.
+// fwd and dq stay on their SM for all their tiles and begin the next one while the last is stored.  Where there are too few
+// tiles for the SMs, CTAs share a tile's steps and leave fp32 parts that a last kernel joins in order.
 // P and dS go back to TMEM as bf16 and are the A operand of their product from there; the streamed
 // tile that was the K-major B operand of the first product is the MN-major B operand of the second, so
 // each tile is loaded once.  The backward pass computes S and dP in both of its kernels (7 products
 // instead of 5): in exchange dQ needs neither atomics (whose order would change the result from run
 // to run) nor a pass of partial sums through memory.
+//
+// 8192 tokens, 40 / 8 heads of 128, causal: forward 391 .. 403 us, 1.71 .. 1.76 PFLOP/s of bf16; backward 1.27 .. 1.30 ms, 1.32 ..
+// 1.35 PFLOP/s counting five products, 1.85 counting the seven.  What bounds them there is the rate of the tensor
+// cores under the power limit (cuBLAS sustains 1.71).  With short sequences (8192 tokens in 13 documents, 32 heads
+// of 64: forward 78 .. 86 us, backward with 8 key heads 202) it is what a tile costs beside its steps: its loads, masks and stores,
+// code that runs once a tile and is not in the instruction caches then.  So loops outside the steps are not unrolled (forward
+// 90 us with them unrolled; the long case gains 2 % from it).
 //
 // Tiles that reach past their sequence: rows past the tensor's end arrive as zeros (TMA); rows
 // of a neighbouring sequence are zeroed in shared memory before the MMAs read them where they are summed
@@ -105,6 +114,7 @@ __device__ __forceinline__ void find_item(const Params& p, bool rows_are_q, int 
         }
     };
     int64_t n = 0;                                         // tiles in all
+#pragma unroll 1
     for (int s0 = 0; s0 < p.nseq; s0 += 32) {
         load(s0);
         int64_t sum = tiles;
@@ -147,6 +157,7 @@ __device__ __forceinline__ void find_item(const Params& p, bool rows_are_q, int 
         return;
     }
     if (rows_are_q) want = n - 1 - want;
+#pragma unroll 1
     for (int s0 = 0; s0 < p.nseq; s0 += 32) {
         load(s0);
         int64_t upto = tiles;                              // inclusive prefix
@@ -276,6 +287,7 @@ __device__ __forceinline__ void load_tile(uint8_t* dst, const CUtensorMap* tm, i
 template <int HD>
 __device__ __forceinline__ void zero_tail(uint8_t* tile, int valid) {
     const int lane = threadIdx.x & 31;
+#pragma unroll 1
     for (int i = lane; i < (kRows - valid) * 8; i += 32)
 #pragma unroll
         for (int b = 0; b < HD / 64; ++b)
@@ -341,6 +353,7 @@ __device__ __forceinline__ void store32(float* row, int col, int dim, const uint
                             __uint_as_float(v[i + 3]) * f);
 }
 __device__ __forceinline__ void store_zeros(float* row, int dim) {
+#pragma unroll 1
     for (int i = 0; i < dim; i += 4) *reinterpret_cast<float4*>(row + i) = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 }
 // This part's steps of `steps`.
@@ -356,6 +369,7 @@ struct Share {
     }
 };
 __device__ __forceinline__ void store_zeros(bf16* row, int dim) {
+#pragma unroll 1
     for (int i = 0; i < dim; i += 8) *reinterpret_cast<uint4*>(row + i) = make_uint4(0, 0, 0, 0);
 }
 
@@ -661,6 +675,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
                             if (!ok) break;
                             fence_after();
                         }
+#pragma unroll 1
                         for (int i = 0; i < p.dim; i += 32) {
                             uint32_t o[32];
                             ld32(to + i, o);
@@ -718,6 +733,7 @@ fwd_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
                     if (store && p.parts == 1) store_zeros(dst, p.dim);
                     if (store && p.parts > 1) store_zeros(sum, p.dim);
                 } else {
+#pragma unroll 1
                     for (int i = 0; i < p.dim; i += 32) {
                         uint32_t o[32];
                         ld32(to + i, o);
@@ -863,7 +879,9 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
         }
         if (lane == 0 && ctl.abort_flag) {                 // the copies in flight land first
             if (queries) wait.drain(&ctl.q_full, (queries - 1) & 1u);
+#pragma unroll 1
             for (uint32_t i = got_k > KS ? got_k - KS : 0; i < got_k; ++i) wait.drain(&ctl.k_full[i % KS], (i / KS) & 1u);
+#pragma unroll 1
             for (uint32_t i = got_v > VS ? got_v - VS : 0; i < got_v; ++i) wait.drain(&ctl.v_full[i % VS], (i / VS) & 1u);
         }
     } else if (warp == 9) {
@@ -1063,6 +1081,7 @@ dq_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUten
                 ok = wait(&ctl.dq_full, queries);
                 if (!ok) break;
                 fence_after();
+#pragma unroll 1
                 for (int i = 64 * half; i < min(p.dim, 64 * half + 64); i += 32) {
                     uint32_t v[32];
                     ld32(tmem + 384 + i + lanes, v);
@@ -1207,7 +1226,9 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
             }
             if (got_do < steps) {                          // aborted: the copies in flight land first
                 wait.drain(&ctl.kv_full, 0);
+#pragma unroll 1
                 for (int i = max(0, got_q - QS); i < got_q; ++i) wait.drain(&ctl.q_full[i % QS], i / QS);
+#pragma unroll 1
                 for (int i = max(0, got_do - DS); i < got_do; ++i) wait.drain(&ctl.do_full[i % DS], i / DS);
             }
         }
@@ -1396,6 +1417,7 @@ dkv_kernel(const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUte
             ok = wait(&ctl.mma_done[half], 0);
             fence_after();
             if (ok)
+#pragma unroll 1
                 for (int i = 0; i < p.dim; i += 32) {
                     uint32_t v[32];
                     ld32(tmem + 256 + 128 * half + i + lanes, v);
@@ -1439,6 +1461,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_sums_kernel(const float* su
     if (i >= tokens * heads * groups) return;
     const float* p = sums + blockIdx.y * which_stride + i * 8;
     float s[8] = {};
+#pragma unroll 1
     for (int k = 0; k < parts; ++k) add8(s, p + k * part_stride, 1.0f);
     const int64_t th = i / groups;
     store8((blockIdx.y ? second : first).at(th / heads, (int)(th % heads)) + (i % groups) * 8, s);
@@ -1456,11 +1479,14 @@ __global__ void __launch_bounds__(kJoinThreads) join_out_kernel(const Params p) 
     const float* lse = p.part_lse + h * p.tq + tok;
     const int64_t lse_stride = p.heads * p.tq;
     float top = -INFINITY, total = 0.0f;
+#pragma unroll 1
     for (int k = 0; k < p.parts; ++k) top = fmaxf(top, lse[k * lse_stride]);
     const float ref = top == -INFINITY ? 0.0f : top;
+#pragma unroll 1
     for (int k = 0; k < p.parts; ++k) total += expf(lse[k * lse_stride] - ref);
     float s[8] = {};
     const float inv = total == 0.0f ? 0.0f : 1.0f / total;
+#pragma unroll 1
     for (int k = 0; k < p.parts; ++k) add8(s, p.part_sums + k * part_stride + i * 8, expf(lse[k * lse_stride] - ref) * inv);
     store8(p.out.at(tok, h) + (i % groups) * 8, s);
     if (i % groups == 0) p.lse[h * p.tq + tok] = total == 0.0f ? -INFINITY : ref + logf(total);
