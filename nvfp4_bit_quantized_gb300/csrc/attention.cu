@@ -17,8 +17,8 @@
 // instead of 5): in exchange dQ needs neither atomics (whose order would change the result from run
 // to run) nor a pass of partial sums through memory.
 //
-// 8192 tokens, 40 / 8 heads of 128, causal: forward 391 .. 403 us, 1.71 .. 1.76 PFLOP/s of bf16; backward 1.27 .. 1.30 ms, 1.32 ..
-// 1.35 PFLOP/s counting five products, 1.85 counting the seven.  What bounds them there is the rate of the tensor
+// 8192 tokens, 40 / 8 heads of 128, causal: forward 399 .. 404 us, 1.70 .. 1.72 PFLOP/s of bf16; backward 1.28 .. 1.33 ms, 1.29 ..
+// 1.34 PFLOP/s counting five products, 1.81 .. 1.88 counting the seven.  What bounds them there is the rate of the tensor
 // cores under the power limit (cuBLAS sustains 1.71).  With short sequences (8192 tokens in 13 documents, 32 heads
 // of 64: forward 78 .. 86 us, backward with 8 key heads 202) it is what a tile costs beside its steps: its loads, masks and stores,
 // code that runs once a tile and is not in the instruction caches then.  So loops outside the steps are not unrolled (forward
@@ -175,7 +175,9 @@ __device__ __forceinline__ void find_item(const Params& p, bool rows_are_q, int 
 
 // Bounded waits, as mbar_wait_bounded, but timed by the SM's own clock: reading the global timer, as that one
 // does after the first failed try, takes longer than most waits here last.  Two cycles a nanosecond:
-// at the highest clock, 2.07 GHz, the limit, at lower clocks a multiple of it.
+// at the highest clock, 2.07 GHz, the limit, at lower clocks a multiple of it.  The lanes of a converged warp try, read the
+// flag and the clock together and get one answer; `all` also tells the compiler so, and costs a vote (1 % of the backward
+// pass where the softmax warps use it).
 struct Wait {
     uint64_t timeout_ns;
     volatile uint32_t* abort;

@@ -108,3 +108,14 @@ def test_adamw_rejects_bad_arguments(lib):
         assert call(t, **kw) == want, (t, kw)
     assert call(count=0) == lib.OK and call(count=-1) == lib.ERR_INVALID_ARG
     assert L.nvfp4_adamw_step(None, 1, None, None, None, None) == lib.ERR_INVALID_ARG
+
+
+def test_attention_forward_rejects_a_bad_workspace(lib):
+    L, ref = lib.lib(), ctypes.byref
+    s = lib.AttentionShapeC(8, 8, 4, 2, 64, 1, 0.125, 1, None, None)
+    h = lib.HeadsC(FAR, 512, 64)
+    need = L.nvfp4_attention_forward_workspace_bytes(ref(s))
+    assert need > 0
+    assert L.nvfp4_attention_forward_workspace_bytes(ref(lib.AttentionShapeC(8, 8, 4, 3, 64, 1, 0.125, 1, None, None))) == 0
+    for ws, n in ((FAR + 4, need), (FAR, need - 1)):
+        assert L.nvfp4_attention_forward_ws(ref(s), ref(h), ref(h), ref(h), ref(h), FAR, ws, n, None, None) == lib.ERR_WORKSPACE
