@@ -92,7 +92,7 @@ def lib():
         P, I64, I32, U32, U64, SZ = c.c_void_p, c.c_int64, c.c_int32, c.c_uint32, c.c_uint64, c.c_size_t
         F32T = c.c_float
         QP, QT = c.POINTER(QParams), c.POINTER(QTensorC)
-        HD, AS = c.POINTER(HeadsC), c.POINTER(AttentionShapeC)
+        HD = AS = P                                    # addresses of HeadsC and AttentionShapeC
         sigs = {
             "nvfp4_scales_mma_bytes": (SZ, [I64, I64]),
             "nvfp4_quantize_workspace_bytes": (SZ, [I64, I64, QP]),

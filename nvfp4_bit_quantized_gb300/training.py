@@ -7,6 +7,9 @@ launched; device-side errors land in the status word read by ``status_query``.""
 from __future__ import annotations
 
 import ctypes
+import functools
+import struct
+import threading
 from typing import Dict, List, Optional, Sequence, Tuple, Union
 
 import torch
@@ -137,7 +140,7 @@ def layer_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
     dw = torch.empty(C, dtype=torch.float32, device=h.device)
     db = torch.empty(C, dtype=torch.float32, device=h.device) if bias else None
     lib = L.lib()
-    ws = _workspace(lib.nvfp4_layer_norm_backward_workspace_bytes(R, C), dev, stream)
+    ws = _workspace(_norm_workspace(dev, R, C), dev, stream)
     st = lib.nvfp4_layer_norm_backward(dy.data_ptr(), _DT[dy.dtype], lddy, h.data_ptr(), _DT[dtype], R, C, ldx, w,
                                        _DT[weight.dtype], m, s, _ptr(dh), lddh, dx.data_ptr(), C, dw.data_ptr(), _ptr(db),
                                        ws.data_ptr(), ws.numel(), stream)
@@ -148,7 +151,33 @@ def layer_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
 
 # ----------------------------------------------------------------------------- attention
 
-def _heads(t: torch.Tensor, name: str, shape, dev: int) -> L.HeadsC:
+# A call's descriptors (AttentionShapeC, then a HeadsC for each tensor) are packed in one go into memory of the calling
+# thread; the library has read them when it returns.
+_SHAPE, _SHAPE_BYTES, _HEADS_BYTES = "qqiiiifiPP", ctypes.sizeof(L.AttentionShapeC), ctypes.sizeof(L.HeadsC)
+_PACK = {n: struct.Struct(_SHAPE + "Pqq" * n) for n in (4, 8)}
+assert all(s.size == _SHAPE_BYTES + n * _HEADS_BYTES for n, s in _PACK.items())
+
+
+class _Descriptors(threading.local):
+    def __init__(self):
+        self.memory = ctypes.create_string_buffer(_PACK[8].size)
+        shape = ctypes.addressof(self.memory)
+        self.at = [shape] + [shape + _SHAPE_BYTES + i * _HEADS_BYTES for i in range(8)]
+
+    def pack(self, n: int, *fields) -> List[int]:
+        """Addresses of the shape and of n tensors' descriptors."""
+        try:
+            _PACK[n].pack_into(self.memory, 0, *fields)
+        except (struct.error, OverflowError) as e:
+            raise _invalid(f"attention: {e}")
+        return self.at
+
+
+_descriptors = _Descriptors()
+
+
+def _heads(t: torch.Tensor, name: str, shape, dev: int) -> Tuple[int, int, int]:
+    """The fields of a HeadsC."""
     if t.shape != shape or t.dtype is not torch.bfloat16 or t.get_device() != dev:
         if t.dim() != 3:
             raise NVFP4Error(L.ERR_SHAPE, f"{name} must be [tokens, heads, dim]")
@@ -159,10 +188,25 @@ def _heads(t: torch.Tensor, name: str, shape, dev: int) -> L.HeadsC:
     tokens, heads, unit = t.stride()
     if unit != 1 and shape[2] > 1:
         raise _invalid(f"{name} must be contiguous along dim")
-    return L.HeadsC(t.data_ptr() or None, tokens, heads)
+    return t.data_ptr(), tokens, heads
 
 
-def _attention_shape(q, k, causal, scale, cu_q, cu_k, dev) -> L.AttentionShapeC:
+# What the C entries return for a workspace depends on these alone.
+@functools.lru_cache(maxsize=256)
+def _attention_workspace(back: bool, dev: int, tq: int, tk: int, heads: int, kv_heads: int, dim: int, nseq: int) -> int:
+    lib = L.lib()
+    cu = None if nseq == 1 else 4                          # not read
+    shape = ctypes.byref(L.AttentionShapeC(tq, tk, heads, kv_heads, dim, False, 1.0, nseq, cu, cu))
+    return (lib.nvfp4_attention_backward_workspace_bytes if back else lib.nvfp4_attention_forward_workspace_bytes)(shape)
+
+
+@functools.lru_cache(maxsize=256)
+def _norm_workspace(dev: int, rows: int, cols: int) -> int:
+    return L.lib().nvfp4_layer_norm_backward_workspace_bytes(rows, cols)
+
+
+def _attention_shape(q, k, causal, scale, cu_q, cu_k, dev) -> Tuple:
+    """The fields of an AttentionShapeC."""
     if q.dim() != 3 or k.dim() != 3:
         raise NVFP4Error(L.ERR_SHAPE, "q and k must be [tokens, heads, dim]")
     nseq = 1
@@ -179,8 +223,8 @@ def _attention_shape(q, k, causal, scale, cu_q, cu_k, dev) -> L.AttentionShapeC:
             raise NVFP4Error(L.ERR_SHAPE, "cu_q and cu_k differ in length")
         nseq = cu_q.shape[0] - 1
     T, H, D = q.shape
-    return L.AttentionShapeC(T, k.shape[0], H, k.shape[1], D, bool(causal), D ** -0.5 if scale is None else scale, nseq,
-                             _ptr(cu_q), _ptr(cu_k))
+    return (T, k.shape[0], H, k.shape[1], D, bool(causal), D ** -0.5 if scale is None else scale, nseq,
+            0 if cu_q is None else cu_q.data_ptr(), 0 if cu_k is None else cu_k.data_ptr())
 
 
 def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal: bool = False,
@@ -203,10 +247,10 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal:
         out = torch.empty(qs, dtype=torch.bfloat16, device=q.device)
     d = _heads(out, "out", qs, dev)
     lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
-    lib = L.lib()
-    ws = _workspace(lib.nvfp4_attention_forward_workspace_bytes(shape), dev, stream)
-    st = lib.nvfp4_attention_forward_ws(shape, a, b, c, d, lse.data_ptr(), ws.data_ptr(), ws.numel(), _status_ptr(dev),
-                                        stream)
+    ws = _workspace(_attention_workspace(False, dev, T, ks[0], H, ks[1], D, shape[7]), dev, stream)
+    s, a, b, c, d, *_ = _descriptors.pack(4, *shape, *a, *b, *c, *d)
+    st = L.lib().nvfp4_attention_forward_ws(s, a, b, c, d, lse.data_ptr(), ws.data_ptr(), ws.numel(), _status_ptr(dev),
+                                            stream)
     if st:
         L.check(st, "nvfp4_attention_forward_ws")
     return out, lse
@@ -224,8 +268,8 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     shape = _attention_shape(q, k, causal, scale, cu_q, cu_k, dev)
     T, H, D = qs = q.shape
     ks = (k.shape[0], k.shape[1], D)
-    ins = [_heads(dout, "dout", qs, dev), _heads(q, "q", qs, dev), _heads(k, "k", ks, dev), _heads(v, "v", ks, dev),
-           _heads(out, "out", qs, dev)]
+    a, b, c = _heads(dout, "dout", qs, dev), _heads(q, "q", qs, dev), _heads(k, "k", ks, dev)
+    d, e = _heads(v, "v", ks, dev), _heads(out, "out", qs, dev)
     if lse.dtype != torch.float32 or lse.shape != (H, T) or not lse.is_contiguous():
         raise _invalid(f"lse must be contiguous float32 [{H}, {T}]")
     _on(lse, "lse", dev)
@@ -233,10 +277,11 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     dq = torch.empty(qs, dtype=torch.bfloat16, device=q.device) if dq is None else dq
     dk = torch.empty(ks, dtype=torch.bfloat16, device=q.device) if dk is None else dk
     dv = torch.empty(ks, dtype=torch.bfloat16, device=q.device) if dv is None else dv
-    lib = L.lib()
-    ws = _workspace(lib.nvfp4_attention_backward_workspace_bytes(shape), dev, stream)
-    st = lib.nvfp4_attention_backward(shape, *ins, lse.data_ptr(), _heads(dq, "dq", qs, dev), _heads(dk, "dk", ks, dev),
-                                      _heads(dv, "dv", ks, dev), ws.data_ptr(), ws.numel(), _status_ptr(dev), stream)
+    ws = _workspace(_attention_workspace(True, dev, T, ks[0], H, ks[1], D, shape[7]), dev, stream)
+    s, a, b, c, d, e, f, g, h = _descriptors.pack(8, *shape, *a, *b, *c, *d, *e, *_heads(dq, "dq", qs, dev),
+                                                  *_heads(dk, "dk", ks, dev), *_heads(dv, "dv", ks, dev))
+    st = L.lib().nvfp4_attention_backward(s, a, b, c, d, e, lse.data_ptr(), f, g, h, ws.data_ptr(), ws.numel(),
+                                          _status_ptr(dev), stream)
     if st:
         L.check(st, "nvfp4_attention_backward")
     return dq, dk, dv
