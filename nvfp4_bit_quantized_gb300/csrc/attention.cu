@@ -34,6 +34,7 @@
 #include <cudaTypedefs.h>
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
+#include <atomic>
 #include <climits>
 #include <cmath>
 #include <cstdint>
@@ -1526,10 +1527,17 @@ bool make_map(CUtensorMap* m, const nvfp4_heads* h, int64_t tokens, int heads, i
               CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename Kernel, typename... Args>
-cudaError_t launch(Kernel kern, int smem, int threads, int64_t grid, cudaStream_t s, const Args&... args) {
-    // set on every call: a kernel's attribute belongs to the current device
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+// A kernel's shared memory is an attribute of the kernel on a device: set once on each of the first 64.
+template <auto kern, typename... Args>
+cudaError_t launch(int smem, int threads, int64_t grid, cudaStream_t s, const Args&... args) {
+    static std::atomic<uint64_t> set{0};
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (e == cudaSuccess && !(set.load(std::memory_order_relaxed) & bit)) {
+        e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e == cudaSuccess) set.fetch_or(bit, std::memory_order_relaxed);
+    }
     return e == cudaSuccess ? launch_pdl(kern, dim3((unsigned)grid), dim3(threads), smem, s, args...) : e;
 }
 
@@ -1666,8 +1674,8 @@ nvfp4_status forward_impl(const nvfp4_attention_shape* shape, const nvfp4_heads*
     p.work = (int)(tiles_of(p.tq, p.nseq, 2 * kRows) * p.heads * p.parts);
     const int64_t grid = std::min(p.work, sms());
     if (!(p.dim <= 64 ? fwd_registers_fit<64>() : fwd_registers_fit<128>())) return NVFP4_ERR_CUDA;
-    cudaError_t e = p.dim <= 64 ? launch(fwd_kernel<64>, Fwd<64>::SMEM, kFwdThreads, grid, s, mq, mk, mv, p)
-                                : launch(fwd_kernel<128>, Fwd<128>::SMEM, kFwdThreads, grid, s, mq, mk, mv, p);
+    cudaError_t e = p.dim <= 64 ? launch<fwd_kernel<64>>(Fwd<64>::SMEM, kFwdThreads, grid, s, mq, mk, mv, p)
+                                : launch<fwd_kernel<128>>(Fwd<128>::SMEM, kFwdThreads, grid, s, mq, mk, mv, p);
     if (e == cudaSuccess && p.parts > 1)
         e = launch_pdl(join_out_kernel, dim3(join_blocks(p.tq, p.heads, p.dim)), dim3(kJoinThreads), 0, s, p);
     return e == cudaSuccess ? NVFP4_OK : NVFP4_ERR_CUDA;
@@ -1739,8 +1747,8 @@ extern "C" nvfp4_status nvfp4_attention_backward(const nvfp4_attention_shape* sh
         p.parts = parts_of_dq(shape);
         p.work = (int)(tiles_of(p.tq, p.nseq, kRows) * p.heads * p.parts);
         const int64_t grid = std::min(p.work, sms());
-        e = p.dim <= 64 ? launch(dq_kernel<64>, Dq<64>::SMEM, kDqThreads, grid, s, mq, mk, mv, mdo, p)
-                        : launch(dq_kernel<128>, Dq<128>::SMEM, kDqThreads, grid, s, mq, mk, mv, mdo, p);
+        e = p.dim <= 64 ? launch<dq_kernel<64>>(Dq<64>::SMEM, kDqThreads, grid, s, mq, mk, mv, mdo, p)
+                        : launch<dq_kernel<128>>(Dq<128>::SMEM, kDqThreads, grid, s, mq, mk, mv, mdo, p);
         if (e == cudaSuccess && p.parts > 1)
             e = launch_pdl(join_sums_kernel, dim3(join_blocks(p.tq, p.heads, p.dim)), dim3(kJoinThreads), 0, s, p.part_sums,
                            p.parts, p.tq * p.heads * p.dim, 0, p.tq, p.heads, p.dim, p.dq, p.dq);
@@ -1748,8 +1756,8 @@ extern "C" nvfp4_status nvfp4_attention_backward(const nvfp4_attention_shape* sh
     if (e == cudaSuccess && p.tk > 0) {
         p.parts = parts_of_dkv(shape);
         const int64_t grid = tiles_of(p.tk, p.nseq, kRows) * p.kv_heads * p.parts, sums = p.tk * p.kv_heads * p.dim;
-        e = p.dim <= 64 ? launch(dkv_kernel<64>, Dkv<64>::SMEM, kDkvThreads, grid, s, mq, mk, mv, mdo, p)
-                        : launch(dkv_kernel<128>, Dkv<128>::SMEM, kDkvThreads, grid, s, mq, mk, mv, mdo, p);
+        e = p.dim <= 64 ? launch<dkv_kernel<64>>(Dkv<64>::SMEM, kDkvThreads, grid, s, mq, mk, mv, mdo, p)
+                        : launch<dkv_kernel<128>>(Dkv<128>::SMEM, kDkvThreads, grid, s, mq, mk, mv, mdo, p);
         if (e == cudaSuccess && p.parts > 1)
             e = launch_pdl(join_sums_kernel, dim3(join_blocks(p.tk, p.kv_heads, p.dim), 2), dim3(kJoinThreads), 0, s,
                            p.part_sums, p.parts, 2 * sums, sums, p.tk, p.kv_heads, p.dim, p.dv, p.dk);

@@ -324,3 +324,37 @@ def test_refusals(nv):
             f()
             print("not refused:", n)
     assert nv.status_query() == 0
+
+
+def test_calls_from_several_threads(nv):
+    """Each thread's calls have their own descriptors: results are those of calls made one after another, bit for bit."""
+    import threading
+    cases = [make(70 + 61 * i, 130 + 40 * i, 4, 2, 64, 10 + i) for i in range(4)]
+
+    def call(q, k, v, dout):
+        out, lse = nv.attention_forward(q, k, v, causal=True)
+        return (out, lse) + nv.attention_backward(dout, q, k, v, out, lse, causal=True)
+    want = [call(*c) for c in cases]
+    torch.cuda.synchronize()
+    bad = []
+
+    def work(i):
+        stream = torch.cuda.Stream()
+        with torch.cuda.stream(stream):
+            for _ in range(20):
+                got = call(*cases[i])
+                stream.synchronize()
+                bad.extend((i, n) for n, (a, b) in enumerate(zip(got, want[i])) if not torch.equal(a, b))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad[:10]
+
+
+def test_a_scale_past_fp32_is_refused(nv):
+    q, k, v, _ = make(8, 8, 2, 2, 64, 3)
+    for scale in (1e300, float("inf"), float("nan")):
+        with pytest.raises(nv.NVFP4Error):
+            nv.attention_forward(q, k, v, scale=scale)
