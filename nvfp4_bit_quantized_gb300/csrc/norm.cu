@@ -804,7 +804,36 @@ __global__ void __launch_bounds__(kLoopThreads) norm_bwd_cols_loop_kernel(BwdPar
     if (c >= p.cols) return;
     const int64_t r0 = p.rows * blockIdx.y / p.nparts, r1 = p.rows * (blockIdx.y + 1) / p.nparts;
     float sw[E] = {}, sb[E] = {};
-    for (int64_t r = r0; r < r1; ++r) {
+    int64_t r = r0;
+    // Chunks of 16 bytes: four rows' loads before the first is used (whole backward pass, 300 x 12000 bf16: 27 -> 23 us, 2048 x
+    // 16384: 107 -> 102).  Single elements the compiler's own unrolling serves better (3000 x 10001: 120 us, 174 with both
+    // loops in batches of this kind).
+    if constexpr (E == 8)
+        for (; r < r1; r += 4) {
+            Chunk<Y, E> dy[4];
+            Chunk<X, E> x[4];
+            float mean[4], rstd[4], g[E], v[E];
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (r + u < r1) {
+                    dy[u].load(static_cast<const Y*>(p.dy) + (r + u) * p.lddy + c);
+                    x[u].load(static_cast<const X*>(p.x) + (r + u) * p.ldx + c);
+                    mean[u] = p.mean[r + u];
+                    rstd[u] = p.rstd[r + u];
+                }
+#pragma unroll
+            for (int u = 0; u < 4; ++u)
+                if (r + u < r1) {
+                    dy[u].get(g);
+                    x[u].get(v);
+#pragma unroll
+                    for (int e = 0; e < E; ++e) {
+                        sw[e] = fmaf(g[e], (v[e] - mean[u]) * rstd[u], sw[e]);
+                        sb[e] += g[e];
+                    }
+                }
+        }
+    for (; r < r1; ++r) {
         Chunk<Y, E> dy;
         Chunk<X, E> x;
         float g[E], v[E];
