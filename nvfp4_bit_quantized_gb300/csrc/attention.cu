@@ -18,7 +18,8 @@
 // to run) nor a pass of partial sums through memory.
 //
 // 8192 tokens, 40 / 8 heads of 128, causal: forward 399 .. 404 us, 1.70 .. 1.72 PFLOP/s of bf16; backward 1.28 .. 1.33 ms, 1.29 ..
-// 1.34 PFLOP/s counting five products, 1.81 .. 1.88 counting the seven.  What bounds them there is the rate of the tensor
+// 1.34 PFLOP/s counting five products, 1.81 .. 1.88 counting the seven (in a CUDA graph; in a long row of passes at the clocks
+// that the power limit leaves, 442 .. 452 us and 1.47 ms).  What bounds them there is the rate of the tensor
 // cores under the power limit (cuBLAS sustains 1.71).  With short sequences (8192 tokens in 13 documents, 32 heads
 // of 64: forward 78 .. 86 us, backward with 8 key heads 202) it is what a tile costs beside its steps: its loads, masks and stores,
 // code that runs once a tile and is not in the instruction caches then.  So loops outside the steps are not unrolled (forward
@@ -1612,7 +1613,8 @@ int sms() {
 // as fill them.  Tiles of keys: each is a whole head group's work, so that few of them balance badly too; there the
 // aim is three a SM.  A part costs a tile of fp32 sums written and read: a CTA keeps at least 4 steps, of keys' tiles with
 // their two sums 8 (4096 tokens in 20 documents, 20 / 4 heads of 128, 10 steps a tile: backward 93 us, 111 in parts of 5).
-// 64 queries over 7000 keys, 8 / 2 heads of 128: forward 70 -> 19 us; 8192 tokens, 8 / 1 heads: backward 715 -> 325 us.
+// 64 queries over 7000 keys, 8 / 2 heads of 128: forward 70 -> 19 us; 8192 tokens, 8 / 1 heads: backward 715 -> 325 us (303
+// with the later steps).
 int parts_for(int64_t ctas, int64_t steps, int64_t wanted, int least) {
     if (ctas < 1 || 2 * ctas > wanted) return 1;
     return (int)std::max<int64_t>(1, std::min<int64_t>({wanted / ctas, steps / least, 64}));
