@@ -433,7 +433,8 @@ NVFP4_API size_t nvfp4_layer_norm_backward_workspace_bytes(int64_t rows, int64_t
  * dy: [rows, cols] of y_dtype; dh (the gradient that reaches h by the residual path), dx: of
  * x_dtype; dweight, dbias: [cols] fp32, overwritten; dbias may be NULL.  dx may be dh or dy where
  * types and pitches are equal.  The column sums have a fixed order: results are deterministic.
- * rows = 0 leaves dweight = dbias = 0.  workspace: device memory, 16-byte aligned, any contents.
+ * rows = 0 leaves dweight = dbias = 0; the rows' operands and the weight may then be NULL.
+ * workspace: device memory, 16-byte aligned, any contents.
  */
 NVFP4_API nvfp4_status nvfp4_layer_norm_backward(const void* dy, int32_t y_dtype, int64_t lddy, const void* x,
                                                  int32_t x_dtype, int64_t rows, int64_t cols, int64_t ldx,

@@ -1077,13 +1077,18 @@ extern "C" nvfp4_status nvfp4_layer_norm_backward(const void* dy, int32_t y_dtyp
     if (!workspace || !aligned16(workspace) ||
         workspace_bytes < nvfp4_layer_norm_backward_workspace_bytes(rows, cols))
         return NVFP4_ERR_WORKSPACE;
+    const cudaStream_t s = static_cast<cudaStream_t>(stream);
+    if (rows == 0) {                                       // no kernel: they read the weight before they look for rows
+        cudaError_t e = cudaMemsetAsync(dweight, 0, cols * sizeof(float), s);
+        if (e == cudaSuccess && dbias) e = cudaMemsetAsync(dbias, 0, cols * sizeof(float), s);
+        return to_status(e);
+    }
     const bool vec = cols % 8 == 0 && rows16(x, ldx) && rows16(dy, lddy) && rows16(dh, lddh) && rows16(dx, lddx) &&
                      aligned16(weight);
     const size_t xb = x_dtype == NVFP4_F32 ? 4 : 2, yb = y_dtype == NVFP4_F32 ? 4 : 2;
     const BwdPlan plan = bwd_plan(rows, cols, vec, xb * (dh ? 2 : 1) + yb);
     const BwdParams p{dy,   x,    weight, dh,  mean, rstd, dx,   dweight, dbias, static_cast<float*>(workspace),
                       rows, cols, lddy,   ldx, lddh, lddx, w_dtype == NVFP4_F32, plan.parts};
-    const cudaStream_t s = static_cast<cudaStream_t>(stream);
     return with_types(x_dtype, y_dtype, [&](auto tx, auto ty) {
         using X = typename decltype(tx)::type;
         using Y = typename decltype(ty)::type;
@@ -1109,7 +1114,7 @@ extern "C" nvfp4_status nvfp4_layer_norm_backward(const void* dy, int32_t y_dtyp
             auto loops = [&](auto cols_kern, auto rows_kern, int per) {
                 const dim3 cut((unsigned)((cols / per + kLoopThreads - 1) / kLoopThreads), plan.parts);
                 e = launch_pdl(cols_kern, cut, block, 0, s, p);
-                if (e == cudaSuccess && rows > 0)
+                if (e == cudaSuccess)
                     e = launch_pdl(rows_kern, dim3((unsigned)std::min<int64_t>(rows, 1 << 30)), block, 0, s, p);
             };
             if (vec) loops(norm_bwd_cols_loop_kernel<X, Y, 8>, norm_bwd_rows_loop_kernel<X, Y, 8>, 8);

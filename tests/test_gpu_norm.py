@@ -198,3 +198,20 @@ def test_refusals(nv):
         with pytest.raises(nv.NVFP4Error):
             f()
     assert nv.status_query() == 0
+
+
+@pytest.mark.parametrize("C", [7, 64, 300, 5120, 9000, 70001])
+@pytest.mark.parametrize("bias", [False, True])
+def test_backward_of_no_rows_needs_only_its_outputs(nv, C, bias):
+    """The C entry with rows = 0 and every operand of the rows NULL, the weight among them: the sums are zeros and nothing else is
+    read, whichever kernels the width would take."""
+    from nvfp4_bit_quantized_gb300 import _lib as L
+    dw, db = (torch.full((C,), float("nan"), device="cuda") for _ in range(2))
+    need = L.lib().nvfp4_layer_norm_backward_workspace_bytes(0, C)
+    ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+    st = L.lib().nvfp4_layer_norm_backward(None, L.BF16, C, None, L.BF16, 0, C, C, None, L.F32, None, None, None, 0, None, C,
+                                           dw.data_ptr(), db.data_ptr() if bias else None, ws.data_ptr(), ws.numel(),
+                                           torch.cuda.current_stream().cuda_stream)
+    assert st == 0
+    torch.cuda.synchronize()
+    assert not dw.any() and (torch.isnan(db).all() if not bias else not db.any())
