@@ -66,8 +66,15 @@ def status_query(device=None) -> int:
 _ws: dict = {}
 
 
-def _workspace(nbytes: int) -> torch.Tensor:
-    key = (torch.cuda.current_device(), _stream())
+def _workspace(nbytes: int, key: Optional[tuple] = None) -> torch.Tensor:
+    """Scratch memory for one call on the current device and stream (``key``, where the caller has them): a buffer
+    that is kept for them and replaced by a larger one when a call needs more.  While the stream is
+    captured the memory is the call's own, from the graph's pool: the graph's launches keep its address, and a kept
+    buffer could be replaced, or at work for another call, when the graph is replayed."""
+    if torch.cuda.is_current_stream_capturing():
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device="cuda")
+    if key is None:
+        key = (torch.cuda.current_device(), _stream())
     t = _ws.get(key)
     if t is None or t.numel() < nbytes:
         t = torch.empty(max(nbytes, 1 << 16), dtype=torch.uint8, device="cuda")

@@ -17,7 +17,7 @@ import torch
 from . import _lib as L
 from ._lib import NVFP4Error
 from . import api
-from .api import _DT, _check_2d, _ptr, dev_status
+from .api import _DT, _check_2d, _ptr, _workspace, dev_status
 
 
 def _invalid(what: str) -> NVFP4Error:
@@ -64,12 +64,6 @@ def _vector(t: torch.Tensor, name: str, n: int, dtypes, dev: int) -> int:
     if t.get_device() != dev:
         _on(t, name, dev)
     return t.data_ptr()
-
-
-def _workspace(nbytes: int, dev: int, stream: int) -> torch.Tensor:
-    """The module's workspace of this device and stream (the one the quantizers use), grown to ``nbytes``."""
-    t = api._ws.get((dev, stream))
-    return t if t is not None and t.numel() >= nbytes else api._workspace(nbytes)
 
 
 def _status_ptr(dev: int) -> int:
@@ -140,7 +134,7 @@ def layer_norm_backward(dy: torch.Tensor, h: torch.Tensor, weight: torch.Tensor,
     dw = torch.empty(C, dtype=torch.float32, device=h.device)
     db = torch.empty(C, dtype=torch.float32, device=h.device) if bias else None
     lib = L.lib()
-    ws = _workspace(_norm_workspace(dev, R, C), dev, stream)
+    ws = _workspace(_norm_workspace(dev, R, C), (dev, stream))
     st = lib.nvfp4_layer_norm_backward(dy.data_ptr(), _DT[dy.dtype], lddy, h.data_ptr(), _DT[dtype], R, C, ldx, w,
                                        _DT[weight.dtype], m, s, _ptr(dh), lddh, dx.data_ptr(), C, dw.data_ptr(), _ptr(db),
                                        ws.data_ptr(), ws.numel(), stream)
@@ -247,7 +241,7 @@ def attention_forward(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, causal:
         out = torch.empty(qs, dtype=torch.bfloat16, device=q.device)
     d = _heads(out, "out", qs, dev)
     lse = torch.empty((H, T), dtype=torch.float32, device=q.device)
-    ws = _workspace(_attention_workspace(False, dev, T, ks[0], H, ks[1], D, shape[7]), dev, stream)
+    ws = _workspace(_attention_workspace(False, dev, T, ks[0], H, ks[1], D, shape[7]), (dev, stream))
     s, a, b, c, d, *_ = _descriptors.pack(4, *shape, *a, *b, *c, *d)
     st = L.lib().nvfp4_attention_forward_ws(s, a, b, c, d, lse.data_ptr(), ws.data_ptr(), ws.numel(), _status_ptr(dev),
                                             stream)
@@ -277,7 +271,7 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
     dq = torch.empty(qs, dtype=torch.bfloat16, device=q.device) if dq is None else dq
     dk = torch.empty(ks, dtype=torch.bfloat16, device=q.device) if dk is None else dk
     dv = torch.empty(ks, dtype=torch.bfloat16, device=q.device) if dv is None else dv
-    ws = _workspace(_attention_workspace(True, dev, T, ks[0], H, ks[1], D, shape[7]), dev, stream)
+    ws = _workspace(_attention_workspace(True, dev, T, ks[0], H, ks[1], D, shape[7]), (dev, stream))
     s, a, b, c, d, e, f, g, h = _descriptors.pack(8, *shape, *a, *b, *c, *d, *e, *_heads(dq, "dq", qs, dev),
                                                   *_heads(dk, "dk", ks, dev), *_heads(dv, "dv", ks, dev))
     st = L.lib().nvfp4_attention_backward(s, a, b, c, d, e, lse.data_ptr(), f, g, h, ws.data_ptr(), ws.numel(),

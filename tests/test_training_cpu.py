@@ -119,3 +119,42 @@ def test_attention_forward_rejects_a_bad_workspace(lib):
     assert L.nvfp4_attention_forward_workspace_bytes(ref(lib.AttentionShapeC(8, 8, 4, 3, 64, 1, 0.125, 1, None, None))) == 0
     for ws, n in ((FAR + 4, need), (FAR, need - 1)):
         assert L.nvfp4_attention_forward_ws(ref(s), ref(h), ref(h), ref(h), ref(h), FAR, ws, n, None, None) == lib.ERR_WORKSPACE
+
+
+class FakeBuffer:
+    def __init__(self, n, **kw):
+        self.n = n
+
+    def numel(self):
+        return self.n
+
+
+@pytest.fixture
+def workspaces(monkeypatch):
+    """api._workspace with the device's part replaced; returns what sets whether the stream is captured."""
+    import torch
+    from nvfp4_bit_quantized_gb300 import api
+    state = {"capturing": False, "stream": 5}
+    monkeypatch.setattr(torch, "empty", FakeBuffer)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "is_current_stream_capturing", lambda: state["capturing"])
+    monkeypatch.setattr(api, "_stream", lambda: state["stream"])
+    api._ws.clear()
+    yield api, state
+    api._ws.clear()
+
+
+def test_a_captured_call_has_scratch_memory_of_its_own(workspaces):
+    """A kept buffer is replaced when it grows; what a graph's launches point to must be neither kept nor replaced."""
+    api, state = workspaces
+    kept = api._workspace(1000)
+    assert api._workspace(1 << 16) is kept and api._workspace(1, (0, 5)) is kept
+    state["capturing"] = True
+    a, b = api._workspace(1000), api._workspace(1000, (0, 5))
+    assert kept is not a and kept is not b and a is not b and a.numel() >= 1000
+    state["capturing"] = False
+    assert api._workspace(1000) is kept
+    larger = api._workspace(1 << 20)
+    assert larger is not kept and larger is not a and api._workspace(1000) is larger
+    state["stream"] = 6
+    assert api._workspace(1000) is not larger
