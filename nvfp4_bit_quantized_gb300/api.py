@@ -9,6 +9,7 @@ word read by :func:`status_query`.
 from __future__ import annotations
 
 import ctypes
+import threading
 from dataclasses import dataclass
 from typing import Optional
 
@@ -63,22 +64,34 @@ def status_query(device=None) -> int:
 
 # ----------------------------------------------------------------------------- workspace
 
-_ws: dict = {}
+class _Workspaces(threading.local):
+    """Each thread has buffers of its own: a call is several launches, and ctypes lets another thread's call put its
+    launches between them, on the same stream too."""
+
+    def __init__(self):
+        self.buffers: dict = {}
+
+    def clear(self) -> None:
+        self.buffers.clear()
+
+
+_ws = _Workspaces()
 
 
 def _workspace(nbytes: int, key: Optional[tuple] = None) -> torch.Tensor:
     """Scratch memory for one call on the current device and stream (``key``, where the caller has them): a buffer
-    that is kept for them and replaced by a larger one when a call needs more.  While the stream is
+    that this thread keeps for them and replaces by a larger one when a call needs more.  While the stream is
     captured the memory is the call's own, from the graph's pool: the graph's launches keep its address, and a kept
     buffer could be replaced, or at work for another call, when the graph is replayed."""
     if torch.cuda.is_current_stream_capturing():
         return torch.empty(max(nbytes, 16), dtype=torch.uint8, device="cuda")
     if key is None:
         key = (torch.cuda.current_device(), _stream())
-    t = _ws.get(key)
+    buffers = _ws.buffers
+    t = buffers.get(key)
     if t is None or t.numel() < nbytes:
         t = torch.empty(max(nbytes, 1 << 16), dtype=torch.uint8, device="cuda")
-        _ws[key] = t
+        buffers[key] = t
     return t
 
 

@@ -88,3 +88,27 @@ def test_graphs_of_one_stream_are_replayed_on_two(nv):
         for _, want, got in graphs + [(None, eager, again)]:
             for a, b in zip(got, want):
                 assert torch.equal(a, b)
+
+
+def test_threads_on_one_stream(nv):
+    import threading
+    stream = torch.cuda.Stream()
+    calls = [Calls(nv, 256 + 128 * i, 2000 + 300 * i, 20 + i) for i in range(4)]
+    torch.cuda.synchronize()
+    with torch.cuda.stream(stream):
+        want = [[t.clone() for t in c()] for c in calls]
+    stream.synchronize()
+    bad = []
+
+    def work(i):
+        with torch.cuda.stream(stream):
+            for _ in range(40):
+                got = calls[i]()
+                bad.extend((i, n) for n, (a, b) in enumerate(zip(got, want[i])) if not torch.equal(a, b))
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(4)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not bad, bad[:10]
+    assert nv.status_query() == 0

@@ -158,3 +158,15 @@ def test_a_captured_call_has_scratch_memory_of_its_own(workspaces):
     assert larger is not kept and larger is not a and api._workspace(1000) is larger
     state["stream"] = 6
     assert api._workspace(1000) is not larger
+
+
+def test_threads_do_not_share_scratch_memory(workspaces):
+    """Two threads' calls on one stream: their launches may alternate, so what one call leaves for its later launches must not
+    lie where the other's does."""
+    import threading
+    api, _ = workspaces
+    mine, theirs = api._workspace(1000), []
+    t = threading.Thread(target=lambda: theirs.extend(api._workspace(1000) for _ in range(2)))
+    t.start()
+    t.join()
+    assert theirs[0] is theirs[1] and theirs[0] is not mine and api._workspace(1000) is mine
