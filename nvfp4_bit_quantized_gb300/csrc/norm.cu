@@ -17,8 +17,10 @@
 // rows and writes them once; a second kernel joins the blocks' parts in a fixed order (no atomics).
 #include <cuda_runtime.h>
 #include <cuda_bf16.h>
+#include <atomic>
 #include <cmath>
 #include <cstdint>
+#include <type_traits>
 
 #include "device_common.cuh"
 #include "host_common.h"
@@ -953,9 +955,24 @@ WidePlan wide_plan(int64_t rows, int64_t chunks, int nc, size_t row_bytes_of_thr
     w.grid = std::min<int64_t>((rows + w.rb - 1) / w.rb, sms() * std::max<int64_t>(1, std::min<int64_t>(blocks, 224 * 1024 / (w.smem + 2048))));
     return w;
 }
-template <typename Kernel, typename P>
-cudaError_t launch_ring(Kernel kern, int64_t grid, int threads, size_t smem, cudaStream_t s, const P& p) {
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+// The shared memory that a kernel may take is an attribute of the kernel on a device, and one kernel serves many widths: it is
+// raised once, to all that a block can have beside the kernel's own arrays, and never lowered, so that a call cannot take from
+// a call of another thread what that is about to launch with.
+template <auto kern, typename P>
+cudaError_t launch_ring(int64_t grid, int threads, size_t smem, cudaStream_t s, const P& p) {
+    static std::atomic<uint64_t> set{0};                   // the first 64 devices
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    const uint64_t bit = dev < 64 ? 1ull << dev : 0;
+    if (e == cudaSuccess && !(set.load(std::memory_order_relaxed) & bit)) {
+        cudaFuncAttributes fa;
+        int most = 0;
+        e = cudaFuncGetAttributes(&fa, kern);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&most, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
+        if (e == cudaSuccess)
+            e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, most - (int)fa.sharedSizeBytes);
+        if (e == cudaSuccess) set.fetch_or(bit, std::memory_order_relaxed);
+    }
     return e == cudaSuccess ? launch_pdl(kern, dim3((unsigned)grid), dim3(threads), smem, s, p) : e;
 }
 
@@ -1026,9 +1043,12 @@ extern "C" nvfp4_status nvfp4_layer_norm_forward(const void* x, int32_t x_dtype,
         // stages 4 or 2, with or without residual, for one shape of a thread's part
         auto wide = [&](auto e, auto nc, auto rb, const WidePlan& w) {
             constexpr int E = decltype(e)::value, NC = decltype(nc)::value, RB = decltype(rb)::value;
-            auto kern = residual ? (w.stages == 4 ? norm_fwd_kernel<X, Y, E, NC, RB, 4, true> : norm_fwd_kernel<X, Y, E, NC, RB, 2, true>)
-                                 : (w.stages == 4 ? norm_fwd_kernel<X, Y, E, NC, RB, 4, false> : norm_fwd_kernel<X, Y, E, NC, RB, 2, false>);
-            return to_status(launch_ring(kern, w.grid, w.threads, w.smem, s, p));
+            auto run = [&](auto stages, auto res) {
+                return to_status(launch_ring<norm_fwd_kernel<X, Y, E, NC, RB, decltype(stages)::value, decltype(res)::value>>(
+                    w.grid, w.threads, w.smem, s, p));
+            };
+            if (residual) return w.stages == 4 ? run(Int<4>{}, std::true_type{}) : run(Int<2>{}, std::true_type{});
+            return w.stages == 4 ? run(Int<4>{}, std::false_type{}) : run(Int<2>{}, std::false_type{});
         };
         const size_t elem = sizeof(X) * (residual ? 2 : 1);
         if (vec) {
@@ -1102,9 +1122,12 @@ extern "C" nvfp4_status nvfp4_layer_norm_backward(const void* dy, int32_t y_dtyp
         } else if (plan.kind == BwdPlan::kBlock) {
             auto wide = [&](auto ee, auto nc, auto rb) {
                 constexpr int E = decltype(ee)::value, NC = decltype(nc)::value, RB = decltype(rb)::value;
-                auto kern = dh ? (plan.w.stages == 3 ? norm_bwd_kernel<X, Y, E, NC, RB, 3, true> : norm_bwd_kernel<X, Y, E, NC, RB, 2, true>)
-                               : (plan.w.stages == 3 ? norm_bwd_kernel<X, Y, E, NC, RB, 3, false> : norm_bwd_kernel<X, Y, E, NC, RB, 2, false>);
-                e = launch_ring(kern, plan.parts, plan.w.threads, plan.w.smem, s, p);
+                auto run = [&](auto stages, auto res) {
+                    return launch_ring<norm_bwd_kernel<X, Y, E, NC, RB, decltype(stages)::value, decltype(res)::value>>(
+                        plan.parts, plan.w.threads, plan.w.smem, s, p);
+                };
+                if (dh) e = plan.w.stages == 3 ? run(Int<3>{}, std::true_type{}) : run(Int<2>{}, std::true_type{});
+                else e = plan.w.stages == 3 ? run(Int<3>{}, std::false_type{}) : run(Int<2>{}, std::false_type{});
             };
             if (!vec && cols <= 4096) wide(Int<1>{}, Int<4>{}, Int<1>{});
             else if (!vec) wide(Int<1>{}, Int<8>{}, Int<1>{});

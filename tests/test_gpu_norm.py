@@ -215,3 +215,44 @@ def test_backward_of_no_rows_needs_only_its_outputs(nv, C, bias):
     assert st == 0
     torch.cuda.synchronize()
     assert not dw.any() and (torch.isnan(db).all() if not bias else not db.any())
+
+
+def test_calls_of_several_widths_from_several_threads(nv):
+    """One kernel serves many widths, each with its own amount of shared memory: threads that call the C entries with
+    different ones, nothing between one call and the next, all get their launches, and the results are those of calls made alone."""
+    import threading
+    from nvfp4_bit_quantized_gb300 import _lib as L
+    lib, widths = L.lib(), (8192, 4096, 6144, 2048)
+    X, _, dy, _, W, B = case(3, 8192, BF16, BF16, F32, 1)
+
+    def call(C, bufs, stream):
+        y, mean, rstd, dx, dw, db, ws = (t.data_ptr() for t in bufs)
+        st = lib.nvfp4_layer_norm_forward(X.data_ptr(), L.BF16, 3, C, 8192, None, 0, W.data_ptr(), B.data_ptr(), L.F32, 1e-5, y,
+                                          L.BF16, C, None, 0, mean, rstd, stream)
+        return st or lib.nvfp4_layer_norm_backward(dy.data_ptr(), L.BF16, 8192, X.data_ptr(), L.BF16, 3, C, 8192, W.data_ptr(),
+                                                   L.F32, mean, rstd, None, 0, dx, C, dw, db, ws, bufs[6].numel(), stream)
+
+    def buffers(C):
+        f32 = dict(dtype=F32, device="cuda")
+        return [torch.zeros(3, C, dtype=BF16, device="cuda"), torch.zeros(3, **f32), torch.zeros(3, **f32),
+                torch.zeros(3, C, dtype=BF16, device="cuda"), torch.zeros(C, **f32), torch.zeros(C, **f32),
+                torch.empty(lib.nvfp4_layer_norm_backward_workspace_bytes(3, C), dtype=torch.uint8, device="cuda")]
+    want = [buffers(C) for C in widths]
+    for C, b in zip(widths, want):
+        assert call(C, b, torch.cuda.current_stream().cuda_stream) == 0
+    got, streams = [buffers(C) for C in widths], [torch.cuda.Stream() for _ in widths]
+    torch.cuda.synchronize()
+    refused, gate = [], threading.Barrier(len(widths))
+
+    def work(i):
+        gate.wait()
+        refused.extend(st for st in (call(widths[i], got[i], streams[i].cuda_stream) for _ in range(3000)) if st)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(len(widths))]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert not refused, (len(refused), refused[:5])
+    for a, b in zip(got, want):
+        assert all(torch.equal(x, y) for x, y in zip(a[:6], b[:6]))
