@@ -8,8 +8,11 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import itertools
+import operator
 import struct
 import threading
+from array import array
 from typing import Dict, List, Optional, Sequence, Tuple, Union
 
 import torch
@@ -284,6 +287,7 @@ def attention_backward(dout: torch.Tensor, q: torch.Tensor, k: torch.Tensor, v: 
 # ----------------------------------------------------------------------------- AdamW
 
 STATE_BLOCK = 128                       # elements of an 8-bit state with one scale
+_data_ptr, _device, _contiguous = torch.Tensor.data_ptr, torch.Tensor.get_device, torch.Tensor.is_contiguous
 
 
 class AdamW:
@@ -294,7 +298,9 @@ class AdamW:
     (torch.float8_e4m3fn) with a float32 scale per 128 elements (``m_scale``, ``v_scale``; value =
     code * scale): meant for beta2 up to about 0.99, where the spread that stochastic rounding gives
     v stays below two fifths of v.  ``state`` takes such lists over from elsewhere (a checkpoint) and
-    ``steps`` how many steps they have seen; the object's lists are what a checkpoint stores.
+    ``steps`` how many steps they have seen; the object's lists are what a checkpoint stores.  To go on
+    from other tensors make another object: a step after a parameter or a state was replaced, or given other
+    storage, is refused (new values are copied into them).
     ``weight_decay`` is one number or one per parameter."""
 
     def __init__(self, params: Sequence[torch.Tensor], bits: int = 32,
@@ -332,22 +338,48 @@ class AdamW:
                 want = (p.numel() + STATE_BLOCK - 1) // STATE_BLOCK if blocks else p.numel()
                 if s.device != p.device or s.dtype != dtype or s.numel() != want or not s.is_contiguous():
                     raise _invalid(f"state[{k!r}][{i}] must be contiguous {dtype} of {want} elements beside its parameter")
-        self._kept = [list(self.params)] + [list(v) for v in self.state.values()]   # what the pointers below point to
+        # What the descriptors point to, and aliases of it: its memory stays whatever becomes of the tensors.
+        self._kept = self._tensors_now()
+        self._aliases = [t.detach() for t in self._kept]
+        self._addresses, self._all = [t.data_ptr() for t in self._kept], list(range(len(self._kept)))
         self._shapes = [p.shape for p in self.params]
-        self._ptrs = [p.data_ptr() for p in self.params]
-        self._tensors = (L.AdamWTensorC * max(n, 1))()
+        size, T = ctypes.sizeof(L.AdamWTensorC), L.AdamWTensorC
+        memory = bytearray(size * max(n, 1))
+        self._tensors = (T * max(n, 1)).from_buffer(memory)
         for i, (p, d) in enumerate(zip(self.params, decay)):
-            self._tensors[i] = L.AdamWTensorC(
+            self._tensors[i] = T(
                 p.data_ptr(), None, self.state["m"][i].data_ptr(), self.state["v"][i].data_ptr(),
                 self.state["m_scale"][i].data_ptr() if bits == 8 else None,
                 self.state["v_scale"][i].data_ptr() if bits == 8 else None, p.numel(), _DT[p.dtype], 0, d, i)
-        # the descriptors' fields that change from step to step, as words of the same memory
-        words = (ctypes.c_uint64 * (ctypes.sizeof(self._tensors) // 8)).from_buffer(self._tensors)
-        halves = (ctypes.c_int32 * (ctypes.sizeof(self._tensors) // 4)).from_buffer(self._tensors)
-        size, T = ctypes.sizeof(L.AdamWTensorC), L.AdamWTensorC
-        self._words, self._halves = words, halves
-        self._grad_at = [(i * size + T.grad.offset) // 8 for i in range(n)]
-        self._dtype_at = [(i * size + T.grad_dtype.offset) // 4 for i in range(n)]
+        # the fields that change from step to step: every descriptor's gradient and its type
+        self._grads = memoryview(memory).cast("Q")[T.grad.offset // 8::size // 8]
+        self._grad_dtypes = memoryview(memory).cast("i")[T.grad_dtype.offset // 4::size // 4]
+
+    def _tensors_now(self) -> List[torch.Tensor]:
+        return [*self.params, *itertools.chain.from_iterable(self.state.values())]
+
+    def _unchanged(self) -> bool:
+        """Whether parameters and states are still the tensors, at the addresses, that the descriptors were made from."""
+        now, kept = self._tensors_now(), self._kept
+        return len(now) == len(kept) and all(map(operator.is_, now, kept)) and \
+            torch._C._tensors_data_ptrs_at_indices_equal(now, self._addresses, self._all)
+
+    def _marshalled(self, grads: Sequence[Optional[torch.Tensor]], dev: int) -> Tuple[array, array]:
+        """The gradients' addresses (0 for None) and types."""
+        try:
+            kinds = [_DT[g.dtype] for g in grads]
+            if [g.shape for g in grads] == self._shapes and all(map(_contiguous, grads)) and {*map(_device, grads)} == {dev}:
+                return array("Q", map(_data_ptr, grads)), array("i", kinds)
+        except (AttributeError, KeyError):                  # a None, or a type that is looked at below
+            pass
+        at, kinds = array("Q"), array("i")
+        for i, (g, shape) in enumerate(zip(grads, self._shapes)):
+            code = 0 if g is None else _DT.get(g.dtype)
+            if g is not None and (code is None or g.shape != shape or g.get_device() != dev or not g.is_contiguous()):
+                raise _invalid(f"grads[{i}] must be contiguous float32 or bfloat16 {list(shape)} beside its parameter")
+            at.append(0 if g is None else g.data_ptr())
+            kinds.append(code)
+        return at, kinds
 
     def step(self, grads: Sequence[Optional[torch.Tensor]], lr: float, betas: Tuple[float, float] = (0.9, 0.95),
              eps: float = 1e-8, grad_scale: Optional[torch.Tensor] = None, round: int = L.SR, sr_seed: int = 0) -> None:
@@ -355,29 +387,21 @@ class AdamW:
         (None leaves that parameter and its state alone).  ``grad_scale``: a one-element float32 CUDA tensor
         that multiplies every gradient (loss scale, clipping) without a host read.  ``round`` (RNE
         or SR with ``sr_seed``) is how 8-bit states and bfloat16 parameters are rounded."""
-        params = self._kept[0]
-        if len(grads) != len(params):
-            raise NVFP4Error(L.ERR_SHAPE, f"{len(grads)} gradients for {len(params)} parameters")
-        if not params:
+        n = len(self._shapes)
+        if len(grads) != n:
+            raise NVFP4Error(L.ERR_SHAPE, f"{len(grads)} gradients for {n} parameters")
+        if not self._unchanged():
+            raise _invalid("a parameter or a state was replaced or has other storage than when the optimizer was made")
+        if not n:
             return
-        dev = params[0].get_device()
+        dev = self._kept[0].get_device()
         stream = _here(dev)
         if grad_scale is not None and (grad_scale.get_device() != dev or grad_scale.dtype != torch.float32
                                        or grad_scale.numel() != 1):
             raise _invalid("grad_scale must be one float32 on the parameters' device")
-        if [p.data_ptr() for p in params] != self._ptrs:
-            raise _invalid("a parameter has other storage than when the optimizer was made")
-        words, halves = self._words, self._halves
-        for i, (g, shape, at, kind) in enumerate(zip(grads, self._shapes, self._grad_at, self._dtype_at)):
-            if g is None:
-                words[at] = 0
-                continue
-            code = _DT.get(g.dtype)
-            if code is None or g.shape != shape or g.get_device() != dev or not g.is_contiguous():
-                raise _invalid(f"grads[{i}] must be contiguous float32 or bfloat16 {list(shape)} beside its parameter")
-            words[at] = g.data_ptr()
-            halves[kind] = code
+        at, kinds = self._marshalled(grads, dev)
+        self._grads[:], self._grad_dtypes[:] = at, kinds
         hp = L.AdamWParams(self.bits, round, self.steps + 1, lr, betas[0], betas[1], eps, sr_seed & (2**64 - 1))
-        st = L.lib().nvfp4_adamw_step(self._tensors, len(params), hp, _ptr(grad_scale), _status_ptr(dev), stream)
+        st = L.lib().nvfp4_adamw_step(self._tensors, n, hp, _ptr(grad_scale), _status_ptr(dev), stream)
         L.check(st, "nvfp4_adamw_step")
         self.steps += 1

@@ -258,3 +258,73 @@ def test_refusals(nv):
     p.data = torch.ones(256, device="cuda")
     with pytest.raises(nv.NVFP4Error):
         moved.step([g], lr=0.1)
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_replaced_states_and_parameters_are_refused(nv, bits):
+    """The step works on the tensors that the object was made with.  Others in their place, and other storage under them, are
+    refused before anything is launched: neither the old tensors, which a checkpoint would not store, nor the new are touched.
+    Values copied into them are the next step's."""
+    def made():
+        params = [torch.ones(300, device="cuda"), torch.ones(40, device="cuda")]
+        opt = nv.AdamW(params, bits=bits)
+        grads = [torch.ones_like(p) for p in params]
+        opt.step(grads, lr=0.1)
+        return opt, params, grads
+
+    def replaced(opt, name):
+        opt.state[name][1] = torch.zeros_like(opt.state[name][1])
+
+    def storage(opt, name):
+        opt.state[name][0].data = torch.zeros_like(opt.state[name][0])
+
+    def a_list(opt, name):
+        opt.state[name] = [t.clone() for t in opt.state[name]]
+
+    def shorter(opt, name):
+        opt.state[name] = opt.state[name][:1]
+
+    def no_tensor(opt, name):
+        opt.state[name][0] = None
+
+    def parameter(opt, name):
+        opt.params[1] = torch.ones(40, device="cuda")
+
+    def no_states(opt, name):
+        del opt.state[name]
+    for change in (replaced, storage, a_list, shorter, no_tensor, parameter, no_states):
+        for name in ("m", "v", "m_scale", "v_scale")[:4 if bits == 8 else 2]:
+            opt, params, grads = made()
+            before = [t.clone() for t in params]
+            change(opt, name)
+            with pytest.raises(nv.NVFP4Error):
+                opt.step(grads, lr=0.1)
+            assert opt.steps == 1 and all(torch.equal(a, b) for a, b in zip(params, before))
+    opt, params, grads = made()
+    other, theirs, _ = made()
+    other.step(grads, lr=0.1)
+    for name, states in other.state.items():               # a checkpoint's values, copied in
+        for a, b in zip(opt.state[name], states):
+            a.copy_(b)
+    opt.steps = other.steps
+    for a, b in zip(params, theirs):
+        a.copy_(b)
+    opt.step(grads, lr=0.1)
+    other.step(grads, lr=0.1)
+    assert all(torch.equal(a, b) for a, b in zip(params, theirs))
+    assert nv.status_query() == 0
+
+
+def test_a_refused_gradient_leaves_the_next_step_whole(nv):
+    """A list that is refused at its last entry has changed nothing of what the next step sees."""
+    params = [torch.ones(300, device="cuda"), torch.ones(300, device="cuda")]
+    want = [p.clone() for p in params]
+    opt, ref = nv.AdamW(params), nv.AdamW(want)
+    grads = [torch.randn(300, device="cuda") for _ in params]
+    with pytest.raises(nv.NVFP4Error):
+        opt.step([torch.ones(300, device="cuda", dtype=BF16), torch.ones(7, device="cuda")], lr=0.1)
+    for o in (opt, ref):
+        o.step([grads[0], None], lr=0.1)
+        o.step([None, grads[1].bfloat16()], lr=0.1)
+    assert all(torch.equal(a, b) for a, b in zip(params, want))
+    assert not torch.equal(params[0], torch.ones_like(params[0])) and not torch.equal(params[1], torch.ones_like(params[1]))
