@@ -486,7 +486,8 @@ typedef struct {
 } nvfp4_adamw_params;
 
 /* `tensors` and `params` are HOST pointers, read before the call returns; grad_scale is a device
-   pointer or NULL.  Tensors must not overlap. */
+   pointer or NULL.  Tensors must not overlap.  All of `params`, step among them, is part of the launch: a CUDA
+   graph that captured the call repeats that same step, with its bias corrections and its random bits. */
 NVFP4_API nvfp4_status nvfp4_adamw_step(const nvfp4_adamw_tensor* tensors, int32_t count,
                                         const nvfp4_adamw_params* params, const float* grad_scale,
                                         uint32_t* dev_status, void* stream);

@@ -386,7 +386,8 @@ class AdamW:
         """One update.  ``grads``: one per parameter, of its shape, contiguous, float32 or bfloat16
         (None leaves that parameter and its state alone).  ``grad_scale``: a one-element float32 CUDA tensor
         that multiplies every gradient (loss scale, clipping) without a host read.  ``round`` (RNE
-        or SR with ``sr_seed``) is how 8-bit states and bfloat16 parameters are rounded."""
+        or SR with ``sr_seed``) is how 8-bit states and bfloat16 parameters are rounded.  The step's number is
+        part of the launch: a step cannot be captured in a CUDA graph."""
         n = len(self._shapes)
         if len(grads) != n:
             raise NVFP4Error(L.ERR_SHAPE, f"{len(grads)} gradients for {n} parameters")
@@ -396,6 +397,9 @@ class AdamW:
             return
         dev = self._kept[0].get_device()
         stream = _here(dev)
+        if torch.cuda.is_current_stream_capturing():
+            raise NVFP4Error(L.ERR_UNSUPPORTED, "an AdamW step in a CUDA graph would be replayed with the same step number, and "
+                                                "so with the same bias corrections and random bits")
         if grad_scale is not None and (grad_scale.get_device() != dev or grad_scale.dtype != torch.float32
                                        or grad_scale.numel() != 1):
             raise _invalid("grad_scale must be one float32 on the parameters' device")

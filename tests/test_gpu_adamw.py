@@ -328,3 +328,22 @@ def test_a_refused_gradient_leaves_the_next_step_whole(nv):
         o.step([None, grads[1].bfloat16()], lr=0.1)
     assert all(torch.equal(a, b) for a, b in zip(params, want))
     assert not torch.equal(params[0], torch.ones_like(params[0])) and not torch.equal(params[1], torch.ones_like(params[1]))
+
+
+def test_a_step_in_a_graph_is_refused(nv):
+    """Replayed, it would be the same step number again: the same bias corrections and the same random bits."""
+    p = torch.ones(300, device="cuda")
+    opt, g = nv.AdamW([p], bits=8), torch.ones(300, device="cuda")
+    opt.step([g], lr=0.1)
+    before, side = p.clone(), torch.zeros(4, device="cuda")
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        side.add_(1)
+        with pytest.raises(nv.NVFP4Error):
+            opt.step([g], lr=0.1)
+    graph.replay()
+    torch.cuda.synchronize()
+    assert opt.steps == 1 and torch.equal(p, before) and (side == 1).all()
+    opt.step([g], lr=0.1)
+    assert opt.steps == 2 and not torch.equal(p, before) and nv.status_query() == 0
