@@ -367,8 +367,9 @@ struct Share {
         first = 0;
         count = steps;
         if (p.parts > 1) {                                 // the divisions take longer than some tiles' steps
-            first = steps * part / p.parts;                // at most 2^23 steps and 64 parts
-            count = steps * (part + 1) / p.parts - first;
+            // in 64 bits: dkv's steps, query tiles times the heads that share a key head, may pass 2^25, and there may be 64 parts
+            first = (int)((int64_t)steps * part / p.parts);
+            count = (int)((int64_t)steps * (part + 1) / p.parts) - first;
         }
     }
 };

@@ -358,3 +358,29 @@ def test_a_scale_past_fp32_is_refused(nv):
     for scale in (1e300, float("inf"), float("nan")):
         with pytest.raises(nv.NVFP4Error):
             nv.attention_forward(q, k, v, scale=scale)
+
+
+def test_more_steps_in_parts_than_32_bits_count(nv):
+    """2^25 steps of one tile of keys in 64 parts: the products of steps and part number pass 2^31, and no part's steps are lost.
+    Tokens and heads overlap in memory, so that 2^32 rows of queries are small; only lse and delta are as long.  All
+    probabilities are 1 / 128 (q = 0) and dout is 1, so each step adds exactly 1 to dv, each part 2^19, which fp32 holds."""
+    import ctypes
+    from nvfp4_bit_quantized_gb300 import _lib as L
+    T, S, H, D = 1 << 23, 128, 512, 8
+
+    def rows(value, n=T + H - 1):
+        t = torch.full((n, D), value, dtype=BF16, device="cuda")
+        return t, L.HeadsC(t.data_ptr(), D, D)
+    zero, one, dq = rows(0.0), rows(1.0), rows(1.0)
+    k, v, dk, dv = rows(0.0, S), rows(0.0, S), rows(1.0, S), rows(1.0, S)
+    lse = torch.full((H, T), math.log(128), device="cuda")
+    s = L.AttentionShapeC(T, S, H, 1, D, 0, 1.0, 1, None, None)
+    ref = ctypes.byref
+    need = L.lib().nvfp4_attention_backward_workspace_bytes(ref(s))
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    assert need - 4 * H * T >= 2 * 64 * S * D * 4           # room for 64 parts of dV and dK
+    st = L.lib().nvfp4_attention_backward(ref(s), ref(one[1]), ref(zero[1]), ref(k[1]), ref(v[1]), ref(zero[1]), lse.data_ptr(),
+                                          ref(dq[1]), ref(dk[1]), ref(dv[1]), ws.data_ptr(), need,
+                                          nv.dev_status().data_ptr(), torch.cuda.current_stream().cuda_stream)
+    assert st == 0 and nv.status_query() == 0
+    assert (dv[0] == 2.0 ** 25).all() and not dk[0].any() and not dq[0].any()
