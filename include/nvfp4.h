@@ -504,6 +504,7 @@ NVFP4_API nvfp4_status nvfp4_adamw_step(const nvfp4_adamw_tensor* tensors, int32
  *   lse = log(sum(exp(z)));  out = sum(exp(z - lse) v)
  * fp32 sums and softmax statistics; the probabilities are rounded to BF16 for the product with v.
  * A query that sees no key gets out = 0, lse = -inf.  lse: [heads, tq] fp32.
+ * Tokens and offsets are bounded: (max(tq, tk) / 128 + nseq) * heads may be at most 2^31 - 2^16 - 1.
  * Offsets that break the rules set NVFP4_ERR_INVALID_ARG on dev_status (nothing is read or written
  * out of bounds; the outputs are unspecified).  What lies outside a sequence does not reach it,
  * whatever it holds.

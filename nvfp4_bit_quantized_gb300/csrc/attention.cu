@@ -1562,8 +1562,8 @@ nvfp4_status check_shape(const nvfp4_attention_shape* s) {
         return NVFP4_ERR_SHAPE;
     if (s->nseq < 1 || (!s->cu_q) != (!s->cu_k) || (!s->cu_q && s->nseq != 1) || !std::isfinite(s->scale))
         return NVFP4_ERR_INVALID_ARG;
-    if ((std::max(s->tq, s->tk) / kRows + s->nseq) * s->heads > INT_MAX) return NVFP4_ERR_SHAPE;   // the largest grid (parts only
-                                                                                                 // where it is small)
+    // tiles x heads (parts only where they are few) are counted in 32 bits, by the grid and up to three grids past the last
+    if ((std::max(s->tq, s->tk) / kRows + s->nseq) * s->heads > INT_MAX - (1 << 16)) return NVFP4_ERR_SHAPE;
     if ((reinterpret_cast<uintptr_t>(s->cu_q) | reinterpret_cast<uintptr_t>(s->cu_k)) % 4) return NVFP4_ERR_ALIGNMENT;
     return NVFP4_OK;
 }

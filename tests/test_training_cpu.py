@@ -170,3 +170,15 @@ def test_threads_do_not_share_scratch_memory(workspaces):
     t.start()
     t.join()
     assert theirs[0] is theirs[1] and theirs[0] is not mine and api._workspace(1000) is mine
+
+
+def test_attention_rejects_more_tiles_than_its_counters_hold(lib):
+    """The counter of tiles x heads runs up to three grids past the last one, in 32 bits."""
+    L, ref, h = lib.lib(), ctypes.byref, ctypes.byref(lib.HeadsC(FAR, 512, 64))
+    for nseq, heads, ok in ((2 ** 25 - 1, 64, False), (2 ** 25 - 1024, 64, False), (2 ** 25 - 1025, 64, True), (2 ** 31 - 200, 1, False)):
+        s = lib.AttentionShapeC(8, 8, heads, 1, 64, 1, 0.125, nseq, FAR, FAR)
+        for size in (L.nvfp4_attention_backward_workspace_bytes, L.nvfp4_attention_forward_workspace_bytes):
+            assert (size(ref(s)) > 0) == ok, (nseq, heads)
+        if not ok:
+            assert L.nvfp4_attention_forward(ref(s), h, h, h, h, FAR, None, None) == lib.ERR_SHAPE
+            assert L.nvfp4_attention_backward(ref(s), h, h, h, h, h, FAR, h, h, h, FAR, 1 << 40, None, None) == lib.ERR_SHAPE
