@@ -1075,7 +1075,7 @@ extern "C" size_t nvfp4_layer_norm_backward_workspace_bytes(int64_t rows, int64_
     if (rows < 0 || cols < 1 || cols > (1ll << 30)) return 0;
     // whatever the types and the alignment turn out to be
     int parts = 0;
-    for (size_t bytes : {4, 6, 8, 12})
+    for (size_t bytes : {4, 6, 8, 10, 12})                 // of an element of x, dh (of x's type, if there is one) and dy
         parts = std::max({parts, bwd_plan(rows, cols, false, bytes).parts, cols % 8 ? 0 : bwd_plan(rows, cols, true, bytes).parts});
     return (size_t)parts * 2 * (size_t)cols * sizeof(float);
 }
