@@ -220,6 +220,8 @@ def _attention_shape(q, k, causal, scale, cu_q, cu_k, dev) -> Tuple:
             raise NVFP4Error(L.ERR_SHAPE, "cu_q and cu_k differ in length")
         nseq = cu_q.shape[0] - 1
     T, H, D = q.shape
+    if D < 1:
+        raise NVFP4Error(L.ERR_SHAPE, "q has no elements along dim")
     return (T, k.shape[0], H, k.shape[1], D, bool(causal), D ** -0.5 if scale is None else scale, nseq,
             0 if cu_q is None else cu_q.data_ptr(), 0 if cu_k is None else cu_k.data_ptr())
 

@@ -384,3 +384,16 @@ def test_more_steps_in_parts_than_32_bits_count(nv):
                                           nv.dev_status().data_ptr(), torch.cuda.current_stream().cuda_stream)
     assert st == 0 and nv.status_query() == 0
     assert (dv[0] == 2.0 ** 25).all() and not dk[0].any() and not dq[0].any()
+
+
+@pytest.mark.parametrize("shape", [(4, 2, 0), (0, 2, 0), (4, 0, 64), (0, 0, 0)])
+def test_axes_of_no_elements_are_refused(nv, shape):
+    """No heads, or heads of no elements, with and without tokens: an argument error like any other."""
+    x = torch.zeros(shape, dtype=BF16, device="cuda")
+    lse = torch.zeros(shape[1], shape[0], device="cuda")
+    for scale in (None, 1.0):
+        with pytest.raises(nv.NVFP4Error):
+            nv.attention_forward(x, x, x, scale=scale)
+        with pytest.raises(nv.NVFP4Error):
+            nv.attention_backward(x, x, x, x, x, lse, scale=scale)
+    assert nv.status_query() == 0
