@@ -343,6 +343,9 @@ class AdamW:
         # What the descriptors point to, and aliases of it: its memory stays whatever becomes of the tensors.
         self._kept = self._tensors_now()
         self._aliases = [t.detach() for t in self._kept]
+        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in self._kept if t.numel())
+        if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
+            raise _invalid("parameters and states must not share memory (a shared weight is one parameter, its gradients summed)")
         self._addresses, self._all = [t.data_ptr() for t in self._kept], list(range(len(self._kept)))
         self._shapes = [p.shape for p in self.params]
         size, T = ctypes.sizeof(L.AdamWTensorC), L.AdamWTensorC

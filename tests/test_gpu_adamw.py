@@ -347,3 +347,21 @@ def test_a_step_in_a_graph_is_refused(nv):
     assert opt.steps == 1 and torch.equal(p, before) and (side == 1).all()
     opt.step([g], lr=0.1)
     assert opt.steps == 2 and not torch.equal(p, before) and nv.status_query() == 0
+
+
+def test_tensors_that_share_memory_are_refused(nv):
+    """One launch updates all tensors at once: memory that two of them share would be updated by both, in any order.  Neighbours
+    in one buffer are fine."""
+    flat, other = torch.ones(600, device="cuda"), torch.ones(300, device="cuda")
+    m, v = [torch.zeros(300, device="cuda") for _ in range(2)], [torch.zeros(300, device="cuda") for _ in range(2)]
+    a, b = flat[:300], flat[300:]
+    bad = [lambda: nv.AdamW([a, b, a]), lambda: nv.AdamW([flat, b]), lambda: nv.AdamW([a, flat[299:599]]),
+           lambda: nv.AdamW([a, b], state={"m": [m[0], m[0]], "v": v}), lambda: nv.AdamW([a, b], state={"m": m, "v": m}),
+           lambda: nv.AdamW([other], state={"m": [a], "v": [other]})]
+    for k, fn in enumerate(bad):
+        with pytest.raises(nv.NVFP4Error):
+            fn()
+    opt = nv.AdamW([a, b, torch.empty(0, device="cuda"), torch.empty(0, device="cuda")], state={
+        "m": m + [torch.zeros(0, device="cuda")] * 2, "v": v + [torch.zeros(0, device="cuda")] * 2})
+    opt.step([torch.ones_like(a), None, None, None], lr=0.1)
+    assert (a < 1).all() and (b == 1).all()
