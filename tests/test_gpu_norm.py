@@ -256,3 +256,61 @@ def test_calls_of_several_widths_from_several_threads(nv):
     assert not refused, (len(refused), refused[:5])
     for a, b in zip(got, want):
         assert all(torch.equal(x, y) for x, y in zip(a[:6], b[:6]))
+
+
+@pytest.mark.parametrize("R,C", [(130, 64), (9, 255), (400, 1027), (400, 1024), (700, 5120), (20, 5127), (40, 8192), (40, 8200), (7, 20480),
+                                 (5, 20481)])
+@pytest.mark.parametrize("t", [BF16, F32])
+def test_in_place(nv, R, C, t):
+    """What the C interface allows to be one tensor: h = x, h = residual, y = x, dx = dh, dx = dy.  The bits are those of separate
+    outputs, for rows with a pitch of their own."""
+    from nvfp4_bit_quantized_gb300 import _lib as L
+    lib, code, stream = L.lib(), L.F32 if t == F32 else L.BF16, torch.cuda.current_stream().cuda_stream
+    X, res, dy, dh, W, B = case(R, C, t, t, F32, R + C)
+    pitch = C + 8
+
+    def rows(src=None):
+        full = torch.full((R, pitch), float("nan"), dtype=t, device="cuda")
+        if src is not None:
+            full[:, :C] = src
+        return full
+
+    def forward(x, r, y, h):
+        mean, rstd = torch.empty(R, device="cuda"), torch.empty(R, device="cuda")
+        st = lib.nvfp4_layer_norm_forward(x.data_ptr(), code, R, C, pitch, None if r is None else r.data_ptr(), pitch, W.data_ptr(),
+                                          B.data_ptr(), L.F32, 1e-5, y.data_ptr(), code, pitch,
+                                          None if h is None else h.data_ptr(), pitch, mean.data_ptr(), rstd.data_ptr(), stream)
+        assert st == 0
+        return y, mean, rstd, h
+
+    def backward(g, x, mean, rstd, d, dx):
+        dw, db = torch.empty(C, device="cuda"), torch.empty(C, device="cuda")
+        ws = torch.empty(lib.nvfp4_layer_norm_backward_workspace_bytes(R, C), dtype=torch.uint8, device="cuda")
+        st = lib.nvfp4_layer_norm_backward(g.data_ptr(), code, pitch, x.data_ptr(), code, R, C, pitch, W.data_ptr(), L.F32,
+                                           mean.data_ptr(), rstd.data_ptr(), None if d is None else d.data_ptr(), pitch,
+                                           dx.data_ptr(), pitch, dw.data_ptr(), db.data_ptr(), ws.data_ptr(), ws.numel(), stream)
+        assert st == 0
+        return dx, dw, db
+
+    def equal(got, want):
+        for a, b in zip(got, want):
+            if b is not None:
+                assert torch.equal(a if a.dim() == 1 else a[:, :C], b if b.dim() == 1 else b[:, :C])
+                assert a.dim() == 1 or torch.isnan(a[:, C:]).all()
+    plain, with_res = forward(rows(X), None, rows(), None), forward(rows(X), rows(res), rows(), rows())
+    x = rows(X)
+    equal(forward(x, None, x, None), plain)                # y = x
+    x, r = rows(X), rows(res)
+    equal(forward(x, r, rows(), x), with_res)              # h = x
+    x, r = rows(X), rows(res)
+    equal(forward(x, r, rows(), r), with_res)              # h = residual
+    x, r = rows(X), rows(res)
+    equal(forward(x, r, x, r), with_res)                   # both, y = x and h = residual
+    h, (mean, rstd) = rows(with_res[3][:, :C]), with_res[1:3]
+    want, alone = backward(rows(dy), h, mean, rstd, rows(dh), rows()), backward(rows(dy), h, mean, rstd, None, rows())
+    g, d = rows(dy), rows(dh)
+    equal(backward(g, h, mean, rstd, d, d), want)          # dx = dh
+    g, d = rows(dy), rows(dh)
+    equal(backward(g, h, mean, rstd, d, g), want)          # dx = dy
+    g = rows(dy)
+    equal(backward(g, h, mean, rstd, None, g), alone)      # dx = dy, no dh
