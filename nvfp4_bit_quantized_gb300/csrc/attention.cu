@@ -87,10 +87,33 @@ struct Item {
     int rows, other_len, diag;
 };
 
+// Whole warp: the last of nseq sequences whose slots begin, at cu[s] / tile + s, at or before `want`; 32 candidates at a time.
+// A function of its own: in line it lengthens the code that every tile's start fetches (backward of 48 documents, which are
+// not searched for: 2468 us in line, 2443).
+template <int tile>
+__device__ __noinline__ int search_slot(const int32_t* cu, int nseq, int64_t total, int64_t want) {
+    const int lane = threadIdx.x & 31;
+    int lo = 0, hi = nseq;
+    while (hi - lo > 1) {
+        const int step = (int)(((int64_t)hi - lo + 31) / 32);
+        const int64_t s = lo + (int64_t)lane * step;
+        bool before = lane == 0;
+        if (lane && s < hi) before = min(max((int64_t)cu[s], (int64_t)0), total) / tile + s <= want;
+        lo += (31 - __clz(__ballot_sync(~0u, before))) * step;
+        hi = (int)min((int64_t)hi, (int64_t)lo + step);
+    }
+    return lo;
+}
+
 // Whole warp: the tile and head that `work` stands for.  The longest tiles come first, as they are under a causal mask:
 // a sequence's tiles are as long as the number of them up to them (of queries) or from them on (of keys).  That order runs
 // through all sequences where there are at most 32, whose offsets a warp holds at once; more are taken one after another.
 // Heads are fastest, so that CTAs that run together read the same K and V.
+// Up to kCounted sequences' tiles are counted for each item; with more that would take longer than the tile, and the sequence is
+// searched for, over slots of which some are empty and fall on the CTAs as they come (65536 tokens, 32 / 8 heads of 64,
+// forward / backward: 48 equal documents 521 / 1672 us counted, 620 / 1640 searched for; 128: 375 / 1130 and 338 / 1078; 4096:
+// 41400 / 58300 and 3500 / 6100).
+constexpr int kCounted = 64;
 template <int tile>
 __device__ __forceinline__ void find_item(const Params& p, bool rows_are_q, int heads, int work, Item* out) {
     const int lane = threadIdx.x & 31, block = p.parts > 1 ? work / p.parts : work;
@@ -115,32 +138,30 @@ __device__ __forceinline__ void find_item(const Params& p, bool rows_are_q, int 
             tiles = (int64_t)((uint64_t)(b - a + tile - 1) / tile);
         }
     };
-    int64_t n = 0;                                         // tiles in all
+    // n: tiles in all or, where they are not counted, the host's bound, of slots that are searched: sequence s has those from
+    // cu[s] / tile + s on, and its tiles are the first of them (there is at most one slot more).
+    const bool counted = p.nseq <= kCounted;
+    int64_t n = 0;
+    if (counted) {
 #pragma unroll 1
-    for (int s0 = 0; s0 < p.nseq; s0 += 32) {
-        load(s0);
-        int64_t sum = tiles;
+        for (int s0 = 0; s0 < p.nseq; s0 += 32) {
+            load(s0);
+            int64_t sum = tiles;
 #pragma unroll
-        for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
-        n += sum;
+            for (int d = 16; d; d >>= 1) sum += __shfl_xor_sync(~0u, sum, d);
+            n += sum;
+        }
+    } else {
+        n = total / tile + p.nseq;
+        if ((int64_t)work * 32 < p.nseq) load(work * 32);  // the first items check everybody's offsets
     }
-    if (bad && work == 0) set_status(p.dev_status, NVFP4_ERR_INVALID_ARG);
+    if (bad && (work == 0 || !counted)) set_status(p.dev_status, NVFP4_ERR_INVALID_ARG);
     int64_t want = block / heads;
     if (want >= n) {
         if (lane == 0) out->valid = 0;
         return;
     }
-    auto found = [&](int64_t index) {                      // one lane: tile `index` of its sequence
-        const int64_t t0 = index * tile;
-        out->valid = 1;
-        out->part = p.parts > 1 ? work - block * p.parts : 0;
-        out->head = block % heads;
-        out->first = a + t0;
-        out->rows = (int)min((int64_t)tile, b - a - t0);
-        out->other = oa;
-        out->other_len = (int)(ob - oa);
-        out->diag = (int)(t0 + (ob - oa) - (b - a));
-    };
+    int64_t index = -1;                                    // of the tile in its sequence, in the lane that has that
     if (p.nseq <= 32) {
         // each sequence of at least c tiles has one of length c: bands of c with the same sequences, from the longest on
         const int mine = (int)tiles;
@@ -150,28 +171,49 @@ __device__ __forceinline__ void find_item(const Params& p, bool rows_are_q, int 
             const int count = __popc(mask), next = __reduce_max_sync(~0u, mine < cur ? mine : 0);
             if (left < (cur - next) * count) {
                 const int c = cur - left / count, rank = left % count;
-                if (mine >= cur && __popc(mask & ((1u << lane) - 1u)) == rank) found(rows_are_q ? c - 1 : mine - c);
+                if (mine >= cur && __popc(mask & ((1u << lane) - 1u)) == rank) index = rows_are_q ? c - 1 : mine - c;
                 break;
             }
             left -= (cur - next) * count;
             cur = next;
         }
-        return;
-    }
-    if (rows_are_q) want = n - 1 - want;
+    } else if (counted) {
+        if (rows_are_q) want = n - 1 - want;
 #pragma unroll 1
-    for (int s0 = 0; s0 < p.nseq; s0 += 32) {
-        load(s0);
-        int64_t upto = tiles;                              // inclusive prefix
+        for (int s0 = 0; s0 < p.nseq; s0 += 32) {
+            load(s0);
+            int64_t upto = tiles;                          // inclusive prefix
 #pragma unroll
-        for (int d = 1; d < 32; d <<= 1) {
-            const int64_t v = __shfl_up_sync(~0u, upto, d);
-            if (lane >= d) upto += v;
+            for (int d = 1; d < 32; d <<= 1) {
+                const int64_t v = __shfl_up_sync(~0u, upto, d);
+                if (lane >= d) upto += v;
+            }
+            if (want >= upto - tiles && want < upto) index = want - (upto - tiles);
+            const int64_t all = __shfl_sync(~0u, upto, 31);
+            if (want < all) break;
+            want -= all;
         }
-        if (want >= upto - tiles && want < upto) found(want - (upto - tiles));
-        const int64_t all = __shfl_sync(~0u, upto, 31);
-        if (want < all) break;
-        want -= all;
+    } else {
+        if (rows_are_q) want = n - 1 - want;
+        const int s = search_slot<tile>(cu, p.nseq, total, want);
+        bounds(cu, s, total, a, b);
+        bounds(cu_other, s, total_other, oa, ob);
+        if (lane == 0) {
+            index = want - (a / tile + s);
+            if (index * tile >= b - a) index = -1;         // an empty slot, or offsets that break the rules
+            if (index < 0) out->valid = 0;
+        }
+    }
+    if (index >= 0) {
+        const int64_t t0 = index * tile;
+        out->valid = 1;
+        out->part = p.parts > 1 ? work - block * p.parts : 0;
+        out->head = block % heads;
+        out->first = a + t0;
+        out->rows = (int)min((int64_t)tile, b - a - t0);
+        out->other = oa;
+        out->other_len = (int)(ob - oa);
+        out->diag = (int)(t0 + (ob - oa) - (b - a));
     }
 }
 

@@ -397,3 +397,63 @@ def test_axes_of_no_elements_are_refused(nv, shape):
         with pytest.raises(nv.NVFP4Error):
             nv.attention_backward(x, x, x, x, x, lse, scale=scale)
     assert nv.status_query() == 0
+
+
+@pytest.mark.parametrize("causal", [False, True])
+@pytest.mark.parametrize("kind", ["mixed", "long among empty", "one more than a warp", "tiles' ends"])
+def test_more_sequences_than_a_warp_holds(nv, kind, causal):
+    """Past 32 sequences the tiles are found by a search: every tile of every sequence is worked on, wherever long, short and empty
+    ones lie."""
+    rng = np.random.default_rng(len(kind))
+    lq = {"mixed": rng.integers(0, 5, 150) * rng.integers(0, 90, 150),
+          "long among empty": np.where(np.arange(1100) % 300 == 299, 600, 0),
+          "one more than a warp": rng.integers(1, 120, 33),
+          "tiles' ends": rng.choice([0, 1, 127, 128, 129, 255, 256, 257], 40)}[kind]
+    lk = np.where(rng.random(len(lq)) < 0.5, lq, rng.permutation(lq))
+    o, oks = ([0] + [int(x) for x in np.cumsum(x)] for x in (lq, lk))
+    q, k, v, dout = make(o[-1], oks[-1], 2, 1, 64, 5, fused=False)
+    run_and_check(nv, q, k, v, dout, causal, None, o, oks, True)
+
+
+def test_bad_offsets_among_many_are_reported(nv):
+    good = list(range(0, 3201, 32))
+    q, k, v, dout = make(3200, 3200, 2, 1, 64, 6)
+    out, lse = nv.attention_forward(q, k, v)
+
+    def statuses(o):
+        cu, right = (torch.tensor(x, dtype=torch.int32, device="cuda") for x in (o, good))
+        for a, b in ((cu, cu), (cu, right), (right, cu)):
+            nv.attention_forward(q, k, v, cu_q=a, cu_k=b)
+            yield nv.status_query()
+            nv.reset_status()
+            nv.attention_backward(dout, q, k, v, out, lse, cu_q=a, cu_k=b, causal=True)
+            yield nv.status_query()
+            nv.reset_status()
+    assert set(statuses(good)) == {0}
+    for at, value in ((0, 1), (0, -5), (1, 5000), (31, 1), (32, -2 ** 31), (33, 0), (64, 2 ** 31 - 1), (77, 2400), (99, 3201), (100, 3199),
+                      (100, 0)):
+        assert set(statuses(good[:at] + [value] + good[at + 1:])) == {1}, (at, value)
+
+
+def test_the_time_grows_with_the_sequences_not_with_their_square(nv):
+    """16 times the sequences of 8 tokens, 16 times the work: three times that is allowed for what does not scale."""
+    def time_of(n):
+        q, k, v, dout = make(8 * n, 8 * n, 4, 2, 64, n)
+        cu = torch.arange(0, 8 * n + 1, 8, dtype=torch.int32, device="cuda")
+
+        def call():
+            out, lse = nv.attention_forward(q, k, v, causal=True, cu_q=cu)
+            nv.attention_backward(dout, q, k, v, out, lse, causal=True, cu_q=cu)
+        call()
+        best = math.inf
+        for _ in range(3):
+            a, b = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+            a.record()
+            call()
+            b.record()
+            b.synchronize()
+            best = min(best, a.elapsed_time(b))
+        return best
+    few, many = time_of(1024), time_of(16384)
+    assert many < 3 * 16 * few, (few, many)
+    assert nv.status_query() == 0
