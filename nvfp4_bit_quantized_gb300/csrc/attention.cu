@@ -88,10 +88,8 @@ struct Item {
 };
 
 // Whole warp: the last of nseq sequences whose slots begin, at cu[s] / tile + s, at or before `want`; 32 candidates at a time.
-// A function of its own: in line it lengthens the code that every tile's start fetches (backward of 48 documents, which are
-// not searched for: 2468 us in line, 2443).
 template <int tile>
-__device__ __noinline__ int search_slot(const int32_t* cu, int nseq, int64_t total, int64_t want) {
+__device__ __forceinline__ int search_slot(const int32_t* cu, int nseq, int64_t total, int64_t want) {
     const int lane = threadIdx.x & 31;
     int lo = 0, hi = nseq;
     while (hi - lo > 1) {
@@ -111,8 +109,8 @@ __device__ __noinline__ int search_slot(const int32_t* cu, int nseq, int64_t tot
 // Heads are fastest, so that CTAs that run together read the same K and V.
 // Up to kCounted sequences' tiles are counted for each item; with more that would take longer than the tile, and the sequence is
 // searched for, over slots of which some are empty and fall on the CTAs as they come (65536 tokens, 32 / 8 heads of 64,
-// forward / backward: 48 equal documents 521 / 1672 us counted, 620 / 1640 searched for; 128: 375 / 1130 and 338 / 1078; 4096:
-// 41400 / 58300 and 3500 / 6100).
+// forward / backward: 48 equal documents 521 / 1645 us counted, 616 / 1568 searched for; 128: 387 / 1087 and 342 / 1050; 4096:
+// 41700 / 58500 and 3600 / 6100).
 constexpr int kCounted = 64;
 template <int tile>
 __device__ __forceinline__ void find_item(const Params& p, bool rows_are_q, int heads, int work, Item* out) {
@@ -409,9 +407,10 @@ struct Share {
         first = 0;
         count = steps;
         if (p.parts > 1) {                                 // the divisions take longer than some tiles' steps
-            // in 64 bits: dkv's steps, query tiles times the heads that share a key head, may pass 2^25, and there may be 64 parts
-            first = (int)((int64_t)steps * part / p.parts);
-            count = (int)((int64_t)steps * (part + 1) / p.parts) - first;
+            // steps x parts is below 2^32 (parts_for).  With 64-bit divisions, whose code is long and in every role, the
+            // backward pass of 8192 tokens in 13 documents takes 254 us, not 244.
+            first = (int)((uint32_t)steps * (uint32_t)part / (uint32_t)p.parts);
+            count = (int)((uint32_t)steps * (uint32_t)(part + 1) / (uint32_t)p.parts) - first;
         }
     }
 };
@@ -1658,20 +1657,22 @@ int sms() {
 // their two sums 8 (4096 tokens in 20 documents, 20 / 4 heads of 128, 10 steps a tile: backward 93 us, 111 in parts of 5).
 // 64 queries over 7000 keys, 8 / 2 heads of 128: forward 70 -> 19 us; 8192 tokens, 8 / 1 heads: backward 715 -> 325 us (303
 // with the later steps).
-int parts_for(int64_t ctas, int64_t steps, int64_t wanted, int least) {
+int parts_for(int64_t ctas, int64_t steps, int64_t most_steps, int64_t wanted, int least) {
     if (ctas < 1 || 2 * ctas > wanted) return 1;
-    return (int)std::max<int64_t>(1, std::min<int64_t>({wanted / ctas, steps / least, 64}));
+    // a tile of one long sequence among short ones may have most_steps; Share multiplies by the parts in 32 bits
+    return (int)std::max<int64_t>(1, std::min<int64_t>({wanted / ctas, steps / least, 64, UINT32_MAX / std::max<int64_t>(1, most_steps)}));
 }
 int64_t tile_steps(int64_t tokens, int nseq) { return (tokens / nseq + kRows - 1) / kRows; }
 int parts_of_fwd(const nvfp4_attention_shape* s) {
-    return parts_for(tiles_of(s->tq, s->nseq, 2 * kRows) * s->heads, tile_steps(s->tk, s->nseq), sms(), 4);
+    return parts_for(tiles_of(s->tq, s->nseq, 2 * kRows) * s->heads, tile_steps(s->tk, s->nseq), tile_steps(s->tk, 1), sms(), 4);
 }
 int parts_of_dq(const nvfp4_attention_shape* s) {
-    return parts_for(tiles_of(s->tq, s->nseq, kRows) * s->heads, tile_steps(s->tk, s->nseq), sms(), 4);
+    return parts_for(tiles_of(s->tq, s->nseq, kRows) * s->heads, tile_steps(s->tk, s->nseq), tile_steps(s->tk, 1), sms(), 4);
 }
 int parts_of_dkv(const nvfp4_attention_shape* s) {
-    return parts_for(tiles_of(s->tk, s->nseq, kRows) * s->kv_heads,
-                     tile_steps(s->tq, s->nseq) * (s->heads / s->kv_heads), 3 * sms(), 8);
+    const int64_t share = s->heads / s->kv_heads;
+    return parts_for(tiles_of(s->tk, s->nseq, kRows) * s->kv_heads, tile_steps(s->tq, s->nseq) * share,
+                     tile_steps(s->tq, 1) * share, 3 * sms(), 8);
 }
 size_t sums_bytes(int parts, int64_t tokens, int heads, int dim) {
     return parts > 1 ? (size_t)parts * tokens * heads * dim * sizeof(float) : 0;
