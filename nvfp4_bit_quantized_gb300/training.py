@@ -9,7 +9,6 @@ from __future__ import annotations
 import ctypes
 import functools
 import itertools
-import operator
 import struct
 import threading
 from array import array
@@ -300,9 +299,10 @@ class AdamW:
     (torch.float8_e4m3fn) with a float32 scale per 128 elements (``m_scale``, ``v_scale``; value =
     code * scale): meant for beta2 up to about 0.99, where the spread that stochastic rounding gives
     v stays below two fifths of v.  ``state`` takes such lists over from elsewhere (a checkpoint) and
-    ``steps`` how many steps they have seen; the object's lists are what a checkpoint stores.  To go on
-    from other tensors make another object: a step after a parameter or a state was replaced, or given other
-    storage, is refused (new values are copied into them).
+    ``steps`` how many steps they have seen: it takes over their memory, under tensors of its own in
+    :attr:`state`, whose lists are what a checkpoint stores.  To go on from other tensors make another
+    object: a step after a parameter or a state was replaced, or given other storage, is refused (new
+    values are copied into them).
     ``weight_decay`` is one number or one per parameter."""
 
     def __init__(self, params: Sequence[torch.Tensor], bits: int = 32,
@@ -326,48 +326,58 @@ class AdamW:
         names = ("m", "v") if bits == 32 else ("m", "v", "m_scale", "v_scale")
         if state is not None and (set(state) != set(names) or any(len(state[k]) != n for k in names)):
             raise NVFP4Error(L.ERR_SHAPE, f"state must hold lists of {n} tensors named {names}")
-        self.state: Dict[str, List[torch.Tensor]] = {}
+        states: Dict[str, List[torch.Tensor]] = {}
         for k in names:
             blocks, dtype = k.endswith("_scale"), torch.float32
             if bits == 8 and not blocks:
                 dtype = torch.float8_e4m3fn
             if state is None:
-                self.state[k] = [torch.zeros((p.numel() + STATE_BLOCK - 1) // STATE_BLOCK if blocks else p.shape,
-                                             dtype=dtype, device=p.device) for p in self.params]
+                states[k] = [torch.zeros((p.numel() + STATE_BLOCK - 1) // STATE_BLOCK if blocks else p.shape,
+                                         dtype=dtype, device=p.device) for p in self.params]
                 continue
-            self.state[k] = list(state[k])
-            for i, (s, p) in enumerate(zip(self.state[k], self.params)):
+            for i, (s, p) in enumerate(zip(state[k], self.params)):
                 want = (p.numel() + STATE_BLOCK - 1) // STATE_BLOCK if blocks else p.numel()
                 if s.device != p.device or s.dtype != dtype or s.numel() != want or not s.is_contiguous():
                     raise _invalid(f"state[{k!r}][{i}] must be contiguous {dtype} of {want} elements beside its parameter")
-        # What the descriptors point to, and aliases of it: its memory stays whatever becomes of the tensors.
-        self._kept = self._tensors_now()
-        self._aliases = [t.detach() for t in self._kept]
-        spans = sorted((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size()) for t in self._kept if t.numel())
+            states[k] = [s.detach() for s in state[k]]
+        # What the descriptors point to.  Aliases keep the parameters' memory, whatever becomes of the tensors.  Nobody else has the
+        # tensors of the states until `state` is read; from then on a step looks at them too.
+        self._states, self._state_read = states, False
+        self._aliases = [p.detach() for p in self.params]
+        self._addresses = [p.data_ptr() for p in self.params]
+        kept = [t for k in names for t in states[k]]
+        self._kept_states, self._state_addresses = [t.detach() for t in kept], [t.data_ptr() for t in kept]
+        spans = sorted((at, at + t.numel() * t.element_size())
+                       for at, t in zip(self._addresses + self._state_addresses, self._aliases + kept) if t.numel())
         if any(a[1] > b[0] for a, b in zip(spans, spans[1:])):
             raise _invalid("parameters and states must not share memory (a shared weight is one parameter, its gradients summed)")
-        self._addresses, self._all = [t.data_ptr() for t in self._kept], list(range(len(self._kept)))
         self._shapes = [p.shape for p in self.params]
         size, T = ctypes.sizeof(L.AdamWTensorC), L.AdamWTensorC
         memory = bytearray(size * max(n, 1))
         self._tensors = (T * max(n, 1)).from_buffer(memory)
         for i, (p, d) in enumerate(zip(self.params, decay)):
             self._tensors[i] = T(
-                p.data_ptr(), None, self.state["m"][i].data_ptr(), self.state["v"][i].data_ptr(),
-                self.state["m_scale"][i].data_ptr() if bits == 8 else None,
-                self.state["v_scale"][i].data_ptr() if bits == 8 else None, p.numel(), _DT[p.dtype], 0, d, i)
+                p.data_ptr(), None, states["m"][i].data_ptr(), states["v"][i].data_ptr(),
+                states["m_scale"][i].data_ptr() if bits == 8 else None,
+                states["v_scale"][i].data_ptr() if bits == 8 else None, p.numel(), _DT[p.dtype], 0, d, i)
         # the fields that change from step to step: every descriptor's gradient and its type
         self._grads = memoryview(memory).cast("Q")[T.grad.offset // 8::size // 8]
         self._grad_dtypes = memoryview(memory).cast("i")[T.grad_dtype.offset // 4::size // 4]
 
-    def _tensors_now(self) -> List[torch.Tensor]:
-        return [*self.params, *itertools.chain.from_iterable(self.state.values())]
+    @property
+    def state(self) -> Dict[str, List[torch.Tensor]]:
+        """The states, a list of tensors for each name."""
+        self._state_read = True
+        return self._states
 
     def _unchanged(self) -> bool:
-        """Whether parameters and states are still the tensors, at the addresses, that the descriptors were made from."""
-        now, kept = self._tensors_now(), self._kept
-        return len(now) == len(kept) and all(map(operator.is_, now, kept)) and \
-            torch._C._tensors_data_ptrs_at_indices_equal(now, self._addresses, self._all)
+        """Whether parameters and states are still at the addresses that the descriptors were made from."""
+        try:
+            return list(map(_data_ptr, self.params)) == self._addresses and (
+                not self._state_read or
+                list(map(_data_ptr, itertools.chain.from_iterable(self._states.values()))) == self._state_addresses)
+        except TypeError:                                  # something that is no tensor
+            return False
 
     def _marshalled(self, grads: Sequence[Optional[torch.Tensor]], dev: int) -> Tuple[array, array]:
         """The gradients' addresses (0 for None) and types."""
@@ -400,7 +410,7 @@ class AdamW:
             raise _invalid("a parameter or a state was replaced or has other storage than when the optimizer was made")
         if not n:
             return
-        dev = self._kept[0].get_device()
+        dev = self._aliases[0].get_device()
         stream = _here(dev)
         if torch.cuda.is_current_stream_capturing():
             raise NVFP4Error(L.ERR_UNSUPPORTED, "an AdamW step in a CUDA graph would be replayed with the same step number, and "

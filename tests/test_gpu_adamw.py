@@ -365,3 +365,34 @@ def test_tensors_that_share_memory_are_refused(nv):
         "m": m + [torch.zeros(0, device="cuda")] * 2, "v": v + [torch.zeros(0, device="cuda")] * 2})
     opt.step([torch.ones_like(a), None, None, None], lr=0.1)
     assert (a < 1).all() and (b == 1).all()
+
+
+@pytest.mark.parametrize("bits", [8, 32])
+def test_states_that_are_taken_over_are_the_objects_own(nv, bits):
+    """Tensors given as ``state`` share their memory with the object's, which are what is updated and what a checkpoint stores, whatever
+    becomes of the given ones."""
+    def made(**kw):
+        p = torch.ones(300, device="cuda")
+        return nv.AdamW([p], bits=bits, **kw), p
+    (first, p0), g = made(), torch.randn(300, device="cuda")
+    first.step([g], lr=0.1)
+    given = {k: [t.clone() for t in v] for k, v in first.state.items()}
+    opt, p1 = made(state=given, steps=1)
+    p1.copy_(p0)
+    for name, states in given.items():
+        assert opt.state[name][0].data_ptr() == states[0].data_ptr()
+    opt, _ = made(state=given, steps=1)                    # its states are not read before the steps
+    opt.params[0].copy_(p0)
+    held = {name: states[0].data for name, states in given.items()}
+    for name, states in given.items():
+        states[0].data = torch.zeros_like(states[0])
+        states[0] = None
+    for o in (first, opt):
+        o.step([g], lr=0.1)
+    assert torch.equal(first.params[0], opt.params[0])
+    for name in held:
+        a, b, c = (t.view(torch.uint8) for t in (opt.state[name][0], first.state[name][0], held[name]))
+        assert torch.equal(a, b) and torch.equal(a, c)
+    opt.state["m"][0].data = torch.zeros_like(opt.state["m"][0])
+    with pytest.raises(nv.NVFP4Error):
+        opt.step([g], lr=0.1)
