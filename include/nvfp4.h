@@ -455,10 +455,11 @@ NVFP4_API nvfp4_status nvfp4_layer_norm_backward(const void* dy, int32_t y_dtype
  * 1 - beta computed in fp64 and rounded once.  8-bit states: per block, scale = max|x| * (1 / 448)
  * and inv = min(448 / max|x|, FLT_MAX) (both 0 for an all-zero block), code = e4m3(x * inv), rounded
  * to nearest even or stochastically, saturating; v's code is at least 1 where v > 0, so that no
- * stored denominator falls to zero.  BF16 parameters are rounded likewise.  Random bits: element i
+ * stored denominator falls to zero (but a block's scale does where all of the block is below 4e-43).  BF16 parameters are rounded likewise.  Random bits: element i
  * of tensor `id` draws on word (i & 3) of Philox(key = sr_seed, counter = (lo32(i >> 2),
- * hi32(i >> 2), 2 id + s, step)): s = 0 for the states (low half m, high half v), s = 1, low half, for BF16 parameters; with R those 16 bits and p the position between the two neighbouring
- * grid points, it goes up iff p + R * 2^-16 >= 1.
+ * hi32(i >> 2), 2 id + s, step)): s = 0 for the states (low half m, high half v), s = 1, low half, for BF16
+ * parameters; with R those 16 bits and p the position between the two neighbouring grid points, it goes up
+ * iff p + R * 2^-16 >= 1.
  * n = 0 and grad = NULL leave a tensor alone.  A non-finite gradient (after gs) sets
  * NVFP4_ERR_NONFINITE on dev_status; it reaches the tensor's values as the formulas have it, and an 8-bit
  * block with such a value is left with a non-finite scale.

@@ -11,14 +11,17 @@
 //         S^T = K Q^T, dP^T = V dO^T, dV += P^T dO, dK += dS^T Q.
 // fwd and dq stay on their SM for all their tiles and begin the next one while the last is stored.  Where there are too few
 // tiles for the SMs, CTAs share a tile's steps and leave fp32 parts that a last kernel joins in order.
-// P and dS go back to TMEM as bf16 and are the A operand of their product from there; the streamed
-// tile that was the K-major B operand of the first product is the MN-major B operand of the second, so
+// P and dS go back to TMEM as bf16 and are the A operand of their product from there: the tensor cores want A of B's type, and
+// the inputs are bf16.  Kept in fp32 they would need tf32 products, at half the rate and twice the TMEM, of operands converted
+// from bf16.  What the rounding costs: against 64 bits the outputs are off by 0.00172 of their norm forward, 0.0029 backward (8192
+// tokens, 40 / 8 heads of 128, causal); with P and dS in fp32 by 0.00168 and 0.0024.
+// The streamed tile that was the K-major B operand of the first product is the MN-major B operand of the second, so
 // each tile is loaded once.  The backward pass computes S and dP in both of its kernels (7 products
 // instead of 5): in exchange dQ needs neither atomics (whose order would change the result from run
 // to run) nor a pass of partial sums through memory.
 //
-// 8192 tokens, 40 / 8 heads of 128, causal: forward 399 .. 404 us, 1.70 .. 1.72 PFLOP/s of bf16; backward 1.28 .. 1.33 ms, 1.29 ..
-// 1.34 PFLOP/s counting five products, 1.81 .. 1.88 counting the seven (in a CUDA graph; in a long row of passes at the clocks
+// 8192 tokens, 40 / 8 heads of 128, causal: forward 399 .. 404 us, 1.70 .. 1.72 PFLOP/s of bf16; backward 1.25 .. 1.30 ms, 1.32 ..
+// 1.37 PFLOP/s counting five products, 1.85 .. 1.92 counting the seven (in a CUDA graph; in a long row of passes at the clocks
 // that the power limit leaves, 442 .. 452 us and 1.47 ms).  What bounds them there is the rate of the tensor
 // cores under the power limit (cuBLAS sustains 1.71).  With short sequences (8192 tokens in 13 documents, 32 heads
 // of 64: forward 78 .. 86 us, backward with 8 key heads 202) it is what a tile costs beside its steps: its loads, masks and stores,

@@ -2,16 +2,19 @@
 // the formulas).  Statistics and sums are fp32.
 //
 // Both passes are bound by memory: x (and the residual) in and y (and h) out forward, dy, x (and dh)
-// in and dx out backward, each once.  A row's values stay in registers between the loads, the
-// statistics (mean first, then the squares about it) and the stores.  A thread holds NC chunks of E
+// in and dx out backward, each once up to the widths that registers hold.  A row's values stay there between the
+// loads, the statistics (mean first, then the squares about it) and the stores.  A thread holds NC chunks of E
 // neighbouring elements: E = 8 with 16-byte accesses, E = 1 where a pointer, a pitch or the width does
 // not allow them.
 //   narrow rows: a group of G lanes takes a row, a warp 32 / G of them at a time;
 //   others: a block takes a row, blocks stay for many rows, and each thread copies its own chunks of the next
 //     rows to shared memory ahead (cp.async): the bytes in flight do not depend on how long a row's
-//     two sums and their barriers take.  It waits for its own copies only;
-//   rows too long for the registers go through the loops at the end, which read them again from the
-//     caches.
+//     two sums and their barriers take.  It waits for its own copies only.  Single bf16 elements, too small for
+//     such copies, are loaded and stored there one after another: 4099 x 5121 takes 71 us forward and 93 backward, fp32
+//     rows of twice the bytes 46 and 81;
+//   rows too long for the registers (forward past 16384 columns, backward and single elements past 8192) go through the
+//     loops at the end, which read them two or three times, in part from the caches: 2048 x 20480 bf16 62 us
+//     forward, 124 backward.
 //
 // Backward, a block keeps the column sums of dy * xhat and dy for its columns in registers over all its
 // rows and writes them once; a second kernel joins the blocks' parts in a fixed order (no atomics).
@@ -236,7 +239,7 @@ __device__ __forceinline__ void copy_chunk(Chunk<T, E>* dst, const T* src) {
     } else if constexpr (kBytes == 4) {
         asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(d), "l"(src) : "memory");
     } else {
-        dst->v = *src;                                     // two bytes: there is no such copy
+        dst->v = *src;                                     // two bytes: there is no such copy, the thread waits for the load
     }
 }
 __device__ __forceinline__ void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
@@ -383,7 +386,9 @@ __global__ void __launch_bounds__(128, NC * E > 16 ? 3 : 4) norm_fwd_warp_kernel
 // Registers of a thread of the wide kernels.  Two rows at a time with a residual, forward: 48, with weight and bias read
 // for each batch, so that two blocks of 640 threads share an SM (8192 x 5120, fp32 x: 89 us, 101 us with 96 and one block).
 // Without a residual, and backward with its column sums, 96 with weight and bias kept (bf16: 38 us, 42 us with 48).
-// Blocks of more threads take one row at a time.
+// Blocks of more threads take one row at a time, with 64: there the forward kernel of two chunks a thread spills with a residual
+// (8200 to 16384 columns: 48 to 128 bytes a thread; 2048 x 16384 bf16 50 us, 4.9 TB/s), the other block kernels
+// at most 16 bytes, the narrow fp32 one of 264 to 512 columns 44.
 constexpr int kFewRegs = 48, kRegs = 96, kManyThreadsRegs = 64;
 
 // A block per RB rows, S such batches of copies: S - 1 ahead.  Shared memory: [S][RB][x, residual][NC][threads] chunks.
@@ -922,7 +927,10 @@ bool rows16(const void* p, int64_t ld) { return !p || (aligned16(p) && ld % 8 ==
 
 constexpr int kNarrow = 128;                   // threads of a block of narrow rows
 constexpr int kRingBytes = 200 * 1024;         // shared memory of an SM for copies
-constexpr int kTwoRows = 640;                  // the most threads that take two rows at a time (96 registers each)
+// The most threads that take two rows at a time, 5120 columns in chunks of 8 (96 registers each; the register file would hold 672
+// threads).  8192 rows, with residual, forward / backward: 5120 columns 55 / 57 us (61 / 77 a row at a time); 6144, a row at a time,
+// 64 / 79; 8192: 91 .. 94 / 94.
+constexpr int kTwoRows = 640;
 
 int sms() {
     int dev = 0;
